@@ -1,4 +1,4 @@
-"""Python binding of libft (the C ABI in include/ft.h): argument marshalling only.
+"""Python binding of libft (the C ABI in include/ft.h and include/ft_kv.h): argument marshalling only.
 
 Every function here has the name of the C entry point without its ``ft_``
 prefix and takes plain integers for pointers (device or host addresses, e.g.
@@ -6,8 +6,8 @@ prefix and takes plain integers for pointers (device or host addresses, e.g.
 step of the hot path runs in the CUDA library; there is no Python or CPU
 fallback: if libft.so is missing this module raises on first use.
 
-``Context`` is a small convenience owner of an ``ft_ctx*`` that raises
-``FtError`` on a non-zero status.
+``Context`` and ``KvCache`` are small convenience owners of an ``ft_ctx*`` and
+an ``ft_kv*`` that raise ``FtError`` on a non-zero status.
 """
 from __future__ import annotations
 
@@ -29,8 +29,12 @@ FT_FMT_BF16 = 0
 FT_FMT_NVFP4 = 1
 FT_FMT_MXFP4 = 2
 FT_FMT_FP8 = 3
+FT_KV_BF16 = 0
+FT_KV_F16 = 1
 
 _c_int = ctypes.c_int32
+_c_i64 = ctypes.c_int64
+_c_f = ctypes.c_float
 _c_p = ctypes.c_void_p
 
 
@@ -38,6 +42,10 @@ class CtlInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("layer", "T", "u", "h", "m", "q0", "q1", "q", "nC", "u_gpu", "n_assign")] + \
                [("clock", ctypes.c_uint32)]
+
+
+class KvInfo(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("allocated", "copied", "live")]
 
 
 class Counters(ctypes.Structure):
@@ -80,6 +88,20 @@ _SIGS = {
     "ft_set_wait_limit": (_c_int, [_c_p, ctypes.c_uint64]),
     "ft_get_status": (_c_int, [_c_p]),
     "ft_destroy": (None, [_c_p]),
+    "ft_kv_page_bytes": (ctypes.c_size_t, [_c_int] * 4),
+    "ft_kv_scratch_bytes": (ctypes.c_size_t, [_c_int] * 7),
+    "ft_kv_init": (_c_int, [ctypes.POINTER(_c_p)] + [_c_int] * 11 + [_c_p] * 5),
+    "ft_kv_extend": (_c_int, [_c_p, _c_int, _c_p, _c_p]),
+    "ft_kv_fork": (_c_int, [_c_p, _c_int, _c_p, _c_p]),
+    "ft_kv_free": (_c_int, [_c_p, _c_int, _c_p]),
+    "ft_kv_compact": (_c_int, [_c_p]),
+    "ft_qk_rope_store": (_c_int, [_c_p, _c_int, _c_int, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p, _c_f, _c_p,
+                                  _c_int, _c_int, _c_int]),
+    "ft_attn_plan": (_c_int, [_c_p, _c_int, _c_int, _c_p, _c_p, _c_int, _c_p, _c_p]),
+    "ft_attn_forward": (_c_int, [_c_p, _c_int, _c_p, _c_i64, _c_p, _c_i64, _c_f]),
+    "ft_kv_last": (_c_int, [_c_p, ctypes.POINTER(KvInfo)]),
+    "ft_kv_status": (_c_int, [_c_p]),
+    "ft_kv_destroy": (None, [_c_p]),
 }
 
 _lib = None
@@ -221,6 +243,63 @@ def destroy(ctx) -> None:
     load().ft_destroy(ctx)
 
 
+def kv_page_bytes(L, Hkv, D, page) -> int:
+    return load().ft_kv_page_bytes(L, Hkv, D, page)
+
+
+def kv_scratch_bytes(Hq, Hkv, D, n_pages, n_rows, T_max, B_max) -> int:
+    return load().ft_kv_scratch_bytes(Hq, Hkv, D, n_pages, n_rows, T_max, B_max)
+
+
+def kv_init(L, Hq, Hkv, D, page, n_pages, n_rows, row_pages, dtype, T_max, B_max, pool, table, lens, refs, stream):
+    h = _c_p()
+    st = load().ft_kv_init(ctypes.byref(h), L, Hq, Hkv, D, page, n_pages, n_rows, row_pages, dtype, T_max, B_max, pool,
+                           table, lens, refs, stream)
+    return st, h.value
+
+
+def kv_extend(kv, n, rows, add) -> int:
+    return load().ft_kv_extend(kv, n, rows, add)
+
+
+def kv_fork(kv, n, parents, children) -> int:
+    return load().ft_kv_fork(kv, n, parents, children)
+
+
+def kv_free(kv, n, rows) -> int:
+    return load().ft_kv_free(kv, n, rows)
+
+
+def kv_compact(kv) -> int:
+    return load().ft_kv_compact(kv)
+
+
+def qk_rope_store(kv, layer, T, qkv, ld, row_of, pos, q_out, ld_q, q_norm, k_norm, eps, cos_sin, max_pos, rot,
+                  pair) -> int:
+    return load().ft_qk_rope_store(kv, layer, T, qkv, ld, row_of, pos, q_out, ld_q, q_norm, k_norm, eps, cos_sin,
+                                   max_pos, rot, pair)
+
+
+def attn_plan(kv, B, T, cu_q, rows, n_groups, group_start, group_tokens) -> int:
+    return load().ft_attn_plan(kv, B, T, cu_q, rows, n_groups, group_start, group_tokens)
+
+
+def attn_forward(kv, layer, q, ld_q, out, ld_o, scale) -> int:
+    return load().ft_attn_forward(kv, layer, q, ld_q, out, ld_o, scale)
+
+
+def kv_last(kv, info) -> int:
+    return load().ft_kv_last(kv, info)
+
+
+def kv_status(kv) -> int:
+    return load().ft_kv_status(kv)
+
+
+def kv_destroy(kv) -> None:
+    load().ft_kv_destroy(kv)
+
+
 # ------------------------------------------------------------ convenience
 
 def _ptr(a) -> int | None:
@@ -357,3 +436,69 @@ class Context:
             if pr.launches[i]:
                 out[kernel_name(i)] = {"ms": pr.ms[i], "launches": int(pr.launches[i])}
         return out
+
+
+class KvCache:
+    """Owner of one ft_kv*; every method raises FtError on a non-zero status.
+
+    ``pool`` is a device tensor (or address) of n_pages page records of
+    ``kv_page_bytes(L, Hkv, D, page)`` bytes; ``table`` [n_rows, row_pages],
+    ``lens`` [n_rows] and ``refs`` [n_pages] are int32 device tensors.  They
+    stay the caller's; an empty cache has table -1, lens 0 and refs 0.  All
+    calls run on ``stream`` (a ``torch.cuda.Stream.cuda_stream`` handle, 0: the
+    legacy default stream).  Layouts and meanings are in include/ft_kv.h.
+    """
+
+    def __init__(self, L, Hq, Hkv, D, page, n_pages, n_rows, row_pages, pool, table, lens, refs, *, dtype=FT_KV_BF16,
+                 T_max=16, B_max=16, stream=0):
+        self.h = None
+        st, h = kv_init(L, Hq, Hkv, D, page, n_pages, n_rows, row_pages, dtype, T_max, B_max, _ptr(pool), _ptr(table),
+                        _ptr(lens), _ptr(refs), stream or None)
+        _check(st, "ft_kv_init")
+        self.h = h
+        self._keep = (pool, table, lens, refs)
+
+    def close(self):
+        if self.h:
+            kv_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def extend(self, n, rows, add):
+        _check(kv_extend(self.h, n, _ptr(rows), _ptr(add)), "ft_kv_extend")
+
+    def fork(self, n, parents, children):
+        _check(kv_fork(self.h, n, _ptr(parents), _ptr(children)), "ft_kv_fork")
+
+    def free(self, n, rows):
+        _check(kv_free(self.h, n, _ptr(rows)), "ft_kv_free")
+
+    def compact(self):
+        _check(kv_compact(self.h), "ft_kv_compact")
+
+    def qk_rope_store(self, layer, T, qkv, ld, row_of, pos, q_out, ld_q, *, q_norm=None, k_norm=None, eps=1e-6,
+                      cos_sin=None, max_pos=0, rot=0, pair=False):
+        _check(qk_rope_store(self.h, layer, T, _ptr(qkv), ld, _ptr(row_of), _ptr(pos), _ptr(q_out), ld_q, _ptr(q_norm),
+                             _ptr(k_norm), eps, _ptr(cos_sin), max_pos, rot, 1 if pair else 0), "ft_qk_rope_store")
+
+    def attn_plan(self, B, T, cu_q, *, rows=None, n_groups=0, group_start=None, group_tokens=None):
+        """Lay out the work of a step from the lengths on the stream now; every layer's attn_forward uses it."""
+        _check(attn_plan(self.h, B, T, _ptr(cu_q), _ptr(rows), n_groups, _ptr(group_start), _ptr(group_tokens)),
+               "ft_attn_plan")
+
+    def attn_forward(self, layer, q, ld_q, out, ld_o, scale):
+        _check(attn_forward(self.h, layer, _ptr(q), ld_q, _ptr(out), ld_o, scale), "ft_attn_forward")
+
+    def last(self) -> dict:
+        """What the last page operation did (syncs)."""
+        i = KvInfo()
+        _check(kv_last(self.h, ctypes.byref(i)), "ft_kv_last")
+        return {n: getattr(i, n) for n, _ in KvInfo._fields_}
+
+    def status(self) -> int:
+        return kv_status(self.h)

@@ -1,0 +1,934 @@
+// ft_attn_plan, ft_attn_forward: attention over the page table, with the
+// prefix that the requests of a group share multiplied once for all of them.
+//
+//   S = Q K^T, P = exp2(scale*log2(e)*(S - m)), O = P V, l = sum P
+//
+// with the running maximum m of a row over the tiles seen so far; pieces of
+// the key axis that different CTAs computed join by
+//   out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,   M = max m_k.
+//
+// A work item is up to 128 query rows of one key/value head (the G query heads
+// of a token are G rows) over a range of 64-key tiles.  Where a group shares a
+// prefix, the rows of all its requests form the tiles that run over it, so each
+// key is read once for 128 rows; the requests' own keys follow as items of
+// their own rows.  Work is laid out by the plan kernel: the shared ranges in
+// equal chunks, round robin, so that the CTAs that work on one chunk with
+// different rows do so at the same time and share it in L2; everything else as
+// one line of tiles cut into equal parts, one per CTA, whatever request or head
+// a cut falls into.
+//
+// One CTA: 4 softmax warps (a thread per row), a TMA warp, an MMA warp; K and
+// V tiles in a ring of shared memory with 128-byte swizzle; S (two buffers)
+// and O in TMEM; P goes back to TMEM over its S and is the A operand of P V.
+// The running maximum is let fall behind by up to 2^8 before O is rescaled:
+// the weights stay exact, and almost no tile touches O.
+#include "ft_kv.cuh"
+#include "ft_tc.cuh"
+
+namespace {
+
+constexpr int G_THREADS = 192;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float RESCALE_LAG = 8.f;   // log2 units
+constexpr int OV = 2;                // cost of an item's start, in tiles
+constexpr int OVP = 4;               // the same with the partial result of a prefix item
+constexpr int MROWS = 16;            // rows of a merge record
+
+template <int D>
+struct Cfg {
+    static constexpr int NST = D == 64 ? 8 : D == 128 ? 4 : 5;
+    static constexpr uint32_t STAGE = ATTN_BN * D * 2;
+    static constexpr uint32_t QBYTES = ATTN_BM * D * 2;
+    static constexpr uint32_t TCOLS = D == 256 ? 512 : 256;  // O: D columns, S: 2 x 64
+    static constexpr int CTAS = D == 256 ? 1 : 2;            // per SM
+    static constexpr size_t SMEM = 1024 + QBYTES + (size_t)NST * STAGE;
+};
+
+struct AttnArgs {
+    const AttnWork* works;
+    const int* woff;
+    const uint16_t* q;
+    long long ld_q;
+    uint16_t* out;
+    long long ld_o;
+    const int* table;
+    int row_pages, page, n_pages, L, Hkv, G, layer;
+    float c;        // scale * log2(e)
+    float* part_o;
+    float2* part_ml;
+    unsigned* err;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if (BF) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Shared-memory descriptor of an operand tile whose 64-element rows lie along
+// M or N (the transposed V): 128-byte swizzled atoms of 64 values by 8 keys,
+// 1024 bytes from one group of 8 keys to the next, `lead` bytes from one block
+// of 64 values to the next.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(const void* tile, uint32_t lead) {
+    const uint64_t start = (ft::smem_addr(tile) >> 4) & 0x3FFFull;
+    return start | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// kind::f16 with bf16 (1) or f16 (0) operands, fp32 accumulator; bit 16: B is
+// given with N contiguous.
+constexpr uint32_t idesc_of(bool bf, int N, bool b_mn) {
+    return (1u << 4) | ((bf ? 1u : 0u) << 7) | ((bf ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(ATTN_BM >> 4) << 24);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int D, bool BF>
+__global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __grid_constant__ CUtensorMap map,
+                                                                       const AttnArgs p) {
+    using C = Cfg<D>;
+    constexpr int NST = C::NST;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    __shared__ uint64_t kv_full[NST], kv_empty[NST], s_full[2], p_full[2], pv_done[2], q_full, o_full, o_empty, done;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_fail;
+    unsigned char* smQ = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    unsigned char* ring = smQ + C::QBYTES;
+    const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+
+    ft::grid_dep_launch();
+    const int w0 = p.woff[blockIdx.x], w1 = p.woff[blockIdx.x + 1];
+    if (w0 == w1) return;
+
+    if (tid == 0) {
+        for (int s = 0; s < NST; ++s) {
+            ft::mbar_init(&kv_full[s], 1);
+            ft::mbar_init(&kv_empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ft::mbar_init(&s_full[b], 1);
+            ft::mbar_init(&p_full[b], 4);
+            ft::mbar_init(&pv_done[b], 1);
+        }
+        ft::mbar_init(&q_full, 4);
+        ft::mbar_init(&o_full, 1);
+        ft::mbar_init(&o_empty, 4);
+        ft::mbar_init(&done, 1);
+        ft::mbar_fence_init();
+        s_fail = 0;
+    }
+    if (wid == 4 && lane == 0) tc::prefetch_map(&map);
+    if (wid == 5) tc::tmem_alloc(&s_tmem, C::TCOLS);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem;
+
+    if (wid == 4) {
+        // ------------------------------------------------------------ TMA warp
+        // order of the ring: K0, K1, V0, K2, V1, ...
+        const int sub_rows = min(p.page, ATTN_BN);           // rows of a box
+        constexpr int NB = D / 64;                           // boxes across a row
+        const int boxes = (ATTN_BN / sub_rows) * NB;
+        const int sub = lane / NB, blk = lane % NB;
+        const bool mine = lane < boxes;
+        const int oob = p.n_pages * p.L * 2 * p.Hkv;         // a box past the map's end reads zeros
+        int it = 0;
+        bool ok = true;
+        for (int w = w0; w < w1 && ok && !__any_sync(0xffffffffu, s_fail); ++w) {
+            const AttnWork k = p.works[w];
+            const int* row = p.table + (size_t)k.trow * p.row_pages;
+            auto page_of = [&](int i) {  // page of this lane's box of tile i, or -1 past the keys
+                const int pos = k.pos0 + i * ATTN_BN + sub * sub_rows;
+                if (!mine || i >= k.ntile || pos >= k.kend) return -1;
+                const int id = row[pos / p.page];
+                if (id < 0 || id >= p.n_pages) {
+                    atomicOr(p.err, FT_DEVERR_ARG);
+                    return -1;
+                }
+                return id;
+            };
+            auto issue = [&](int id, int i, int kv) {
+                const int st = it % NST;
+                if (it >= NST && !ft::mbar_wait(&kv_empty[st], ((it / NST) - 1) & 1, p.err)) ok = false;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                if (lane == 0) ft::mbar_arrive_expect_tx(&kv_full[st], C::STAGE);
+                __syncwarp();
+                if (mine) {
+                    const int pos = k.pos0 + i * ATTN_BN + sub * sub_rows;
+                    const int z = id < 0 ? oob : ((id * p.L + p.layer) * 2 + kv) * p.Hkv + k.head;
+                    unsigned char* dst = ring + (size_t)st * C::STAGE + blk * (ATTN_BN * 128) + sub * sub_rows * 128;
+                    tc::tma_load_3d(dst, &map, blk * 64, pos % p.page, z, &kv_full[st]);
+                }
+                ++it;
+            };
+            int prev = -1, cur = page_of(0);
+            for (int i = 0; i <= k.ntile && ok; ++i) {
+                const int next = page_of(i + 1);
+                if (i < k.ntile) issue(cur, i, 0);
+                if (ok && i > 0) issue(prev, i - 1, 1);
+                prev = cur;
+                cur = next;
+            }
+        }
+        if (!ok) s_fail = 1;
+        for (int j = it - NST; j < it; ++j)  // nothing in flight into shared memory at exit
+            if (j >= 0) ft::mbar_wait(&kv_full[j % NST], (j / NST) & 1, p.err);
+    } else if (wid == 5) {
+        // ------------------------------------------------------------ MMA warp
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_of(BF, ATTN_BN, false), id_o = idesc_of(BF, D, true);
+            int it = 0, g = 0, n = 0;
+            bool ok = true;
+            auto wait = [&](uint64_t* b, int ph) {
+                if (ok && !ft::mbar_wait(b, (uint32_t)ph & 1u, p.err)) ok = false;
+                return ok;
+            };
+            auto scores = [&](int t) {  // S[t & 1] = Q K^T with the next tile of the ring
+                const int st = it % NST;
+                if (!wait(&kv_full[st], it / NST)) return;
+                tc::fence_after_sync();
+                const uint32_t d = tmem + (uint32_t)(D + (t & 1) * ATTN_BN);
+                const unsigned char* kt = ring + (size_t)st * C::STAGE;
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b) {
+                    const uint64_t ad = tc::sdesc_k_sw128(smQ + b * (ATTN_BM * 128));
+                    const uint64_t bd = tc::sdesc_k_sw128(kt + b * (ATTN_BN * 128));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        tc::mma_bf16(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), id_s, (b | j) ? 1u : 0u);
+                }
+                tc::mma_commit(&kv_empty[st]);
+                tc::mma_commit(&s_full[t & 1]);
+                ++it;
+            };
+            for (int w = w0; w < w1 && ok && !s_fail; ++w, ++n) {
+                const int nt = p.works[w].ntile;
+                if (!wait(&q_full, n)) break;
+                tc::fence_after_sync();
+                scores(g);
+                if (nt > 1 && ok) scores(g + 1);
+                for (int i = 0; i < nt && ok; ++i, ++g) {
+                    if (!wait(&p_full[g & 1], g >> 1)) break;
+                    if (i == 0 && n > 0 && !wait(&o_empty, n - 1)) break;
+                    const int st = it % NST;
+                    if (!wait(&kv_full[st], it / NST)) break;
+                    tc::fence_after_sync();
+                    const uint32_t a = tmem + (uint32_t)(D + (g & 1) * ATTN_BN);
+                    const uint64_t vd = sdesc_mn_sw128(ring + (size_t)st * C::STAGE, ATTN_BN * 128);
+#pragma unroll
+                    for (int j = 0; j < ATTN_BN / 16; ++j)  // 16 keys: 8 columns of P, 2048 bytes of V
+                        mma_ts(tmem, a + (uint32_t)(8 * j), vd + (uint64_t)(128 * j), id_o, (i | j) ? 1u : 0u);
+                    tc::mma_commit(&kv_empty[st]);
+                    tc::mma_commit(&pv_done[g & 1]);
+                    if (i == nt - 1) tc::mma_commit(&o_full);
+                    ++it;
+                    if (i + 2 < nt) scores(g + 2);
+                }
+            }
+            if (!ok) s_fail = 1;
+            tc::mma_commit(&done);
+            ft::mbar_wait(&done, 0, p.err);
+        }
+    } else {
+        // ------------------------------------------------------- softmax warps
+        const int r = tid;  // row of the item: TMEM lane
+        const uint32_t lane_base = tmem + ((uint32_t)(wid * 32) << 16);
+        auto load_q = [&](const AttnWork& k) {
+            constexpr int CH = D / 8;  // 16-byte chunks of a row
+            for (int i = tid; i < k.nrows * CH; i += 128) {
+                const int rr = i / CH, ch = i % CH;
+                const int R = k.r0 + rr, tok = k.tok0 + R / p.G, gh = k.head * p.G + R % p.G;
+                ft::cp_async16(smQ + (ch >> 3) * (ATTN_BM * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
+                               p.q + (long long)tok * p.ld_q + gh * D + ch * 8);
+            }
+        };
+        auto publish_q = [&]() {
+            ft::cp_async_wait_all();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) ft::mbar_arrive(&q_full);
+        };
+        // the whole warp goes on or gives up: what follows a wait is executed by all its lanes together
+        auto wait = [&](uint64_t* b, int ph) {
+            return __all_sync(0xffffffffu, ft::mbar_wait(b, (uint32_t)ph & 1u, p.err));
+        };
+        int g = 0, it0 = 0, n = 0;
+        bool ok = true;
+        AttnWork k = p.works[w0];
+        load_q(k);
+        publish_q();
+        for (int w = w0; w < w1 && ok && !__any_sync(0xffffffffu, s_fail); ++w, ++n) {
+            const bool rows_here = wid * 32 < k.nrows;
+            const int tok = (k.r0 + min(r, k.nrows - 1)) / p.G;
+            const int lim = min(k.kend, k.vis0 == ATTN_NOMASK ? k.kend : k.vis0 + tok);  // this row sees positions < lim
+            float m = -INFINITY, l = 0.f;
+            AttnWork knext = k;
+            for (int i = 0; i < k.ntile; ++i, ++g) {
+                if (!wait(&s_full[g & 1], g >> 1)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
+                const int pos = k.pos0 + i * ATTN_BN;
+                const bool last = i == k.ntile - 1;
+                if (last && w + 1 < w1) {  // every product with this Q is done
+                    knext = p.works[w + 1];
+                    load_q(knext);
+                }
+                if (rows_here) {
+                    const uint32_t sa = lane_base + (uint32_t)(D + (g & 1) * ATTN_BN);
+                    uint32_t s[64];
+                    tc::tmem_ld32(sa, s);
+                    tc::tmem_ld32(sa + 32, s + 32);
+                    tc::tmem_wait_ld(s);
+                    tc::tmem_wait_ld(s + 32);
+                    float* f = reinterpret_cast<float*>(s);
+                    if (pos + ATTN_BN > lim) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (pos + j >= lim) f[j] = -INFINITY;
+                    }
+                    float mx = f[0];
+#pragma unroll
+                    for (int j = 1; j < 64; ++j) mx = fmaxf(mx, f[j]);
+                    const float mn = fmaxf(m, mx);
+                    if (i == 0) {
+                        m = mn;
+                    } else {
+                        const bool lag = (mn - m) * p.c > RESCALE_LAG;
+                        if (__any_sync(0xffffffffu, lag)) {
+                            if (!wait(&pv_done[(g - 1) & 1], (g - 1) >> 1)) ok = false;
+                            tc::fence_after_sync();
+                            const float fac = lag ? ex2((m - mn) * p.c) : 1.f;
+                            l *= fac;
+                            if (lag) m = mn;
+#pragma unroll
+                            for (int cc = 0; cc < D; cc += 32) {
+                                uint32_t o[32];
+                                tc::tmem_ld32(lane_base + (uint32_t)cc, o);
+                                tc::tmem_wait_ld(o);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fac);
+                                tmem_st32(lane_base + (uint32_t)cc, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.f : m * p.c;  // a row that has seen no key yet
+                    float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int j = 0; j < 64; j += 2) {
+                        const float a = ex2(fmaf(f[j], p.c, -mc)), b = ex2(fmaf(f[j + 1], p.c, -mc));
+                        l4[(j >> 1) & 3] += a + b;
+                        // the weights go to the product in the cache's own type; l keeps their fp32 values
+                        pk[j >> 1] = pack2<BF>(a, b);
+                    }
+                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                    tmem_st32(sa, pk);
+                    tmem_wait_st();
+                }
+                const int valid = k.kend - pos;
+                if (valid < ATTN_BN) {
+                    // what the pool holds past the keys may be anything: its weights are 0, its values are made 0
+                    const int vit = it0 + min(i + 2, k.ntile) + i, st = vit % NST;
+                    if (!wait(&kv_full[st], vit / NST)) ok = false;
+                    unsigned char* vt = ring + (size_t)st * C::STAGE;
+                    const int z0 = max(valid, 0), nz = (ATTN_BN - z0) * 8;
+                    for (int x = tid; x < nz * (D / 64); x += 128) {
+                        const int b = x / nz, y = x % nz;
+                        *reinterpret_cast<uint4*>(vt + b * (ATTN_BN * 128) + z0 * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ft::mbar_arrive(&p_full[g & 1]);
+            }
+            if (!ok) break;
+            if (w + 1 < w1) publish_q();
+            if (!wait(&o_full, n)) {
+                ok = false;
+                break;
+            }
+            tc::fence_after_sync();
+            if (rows_here) {
+                const bool in = r < k.nrows;
+                const int R = k.r0 + min(r, k.nrows - 1);
+                if (k.prow < 0) {
+                    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no key seen: zeros; NaN stays
+                    uint16_t* dst = p.out + (long long)(k.tok0 + R / p.G) * p.ld_o + (k.head * p.G + R % p.G) * D;
+#pragma unroll
+                    for (int cc = 0; cc < D; cc += 32) {
+                        uint32_t o[32];
+                        tc::tmem_ld32(lane_base + (uint32_t)cc, o);
+                        tc::tmem_wait_ld(o);
+                        if (in) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8) {
+                                uint4 v;
+                                v.x = pack2<BF>(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
+                                v.y = pack2<BF>(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+                                v.z = pack2<BF>(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv);
+                                v.w = pack2<BF>(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv);
+                                *reinterpret_cast<uint4*>(dst + cc + j) = v;
+                            }
+                        }
+                    }
+                } else {
+                    float* dst = p.part_o + (size_t)(k.prow + r) * D;
+#pragma unroll
+                    for (int cc = 0; cc < D; cc += 32) {
+                        uint32_t o[32];
+                        tc::tmem_ld32(lane_base + (uint32_t)cc, o);
+                        tc::tmem_wait_ld(o);
+                        if (in) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4)
+                                *reinterpret_cast<uint4*>(dst + cc + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        }
+                    }
+                    if (in) p.part_ml[k.prow + r] = make_float2(m * p.c, l);
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) ft::mbar_arrive(&o_empty);
+            it0 += 2 * k.ntile;
+            k = knext;
+        }
+        if (!ok) s_fail = 1;
+        ft::cp_async_wait_all();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (wid == 5) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, C::TCOLS);
+    }
+}
+
+// Joins the pieces of the rows that have more than one: a warp per row, D/32
+// columns a lane.  The order of the pieces is fixed by the plan.
+template <int D, bool BF>
+__global__ void __launch_bounds__(256) attn_merge_kernel(const AttnHdr* hdr, const AttnMerge* __restrict__ merges,
+                                                         const float* __restrict__ part_o,
+                                                         const float2* __restrict__ part_ml, long long c_row, int G,
+                                                         uint16_t* out, long long ld_o) {
+    constexpr int V = D / 32;
+    ft::grid_dep_wait();
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int n = hdr->n_merge;
+    for (int u = blockIdx.x; u < n; u += gridDim.x) {
+        const AttnMerge k = merges[u];
+        for (int r = wid; r < k.nrows; r += 8) {
+            const int R = k.r0 + r, tok = k.tok0 + R / G, gh = R % G;
+            long long abase = 0;
+            if (k.ptok0 >= 0) {
+                const int PR = (tok - k.ptok0) * G + gh;
+                abase = (long long)(k.pitem + PR / ATTN_BM) * ATTN_BM + PR % ATTN_BM;
+            }
+            const int na = k.ptok0 >= 0 ? k.pnch : 0, np = na + 1 + k.nc;
+            auto prow = [&](int i) -> long long {
+                if (i < na) return abase + (long long)i * k.pnrt * ATTN_BM;
+                if (i == na) return k.brow + r;
+                return c_row + (long long)(k.c0 + i - na - 1) * ATTN_BM + R % ATTN_BM;
+            };
+            float M = -INFINITY;
+            for (int i = lane; i < np; i += 32) M = fmaxf(M, part_ml[prow(i)].x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            if (M == -INFINITY) M = 0.f;
+            float den = 0.f, acc[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[j] = 0.f;
+            for (int b = 0; b < np; b += 32) {
+                float wgt = 0.f;
+                long long pr = 0;
+                if (b + lane < np) {
+                    pr = prow(b + lane);
+                    const float2 ml = part_ml[pr];
+                    wgt = ex2(ml.x - M);
+                    den += wgt * ml.y;
+                }
+                const int e = min(32, np - b);
+#pragma unroll 4
+                for (int i = 0; i < e; ++i) {
+                    const float wi = __shfl_sync(0xffffffffu, wgt, i);
+                    const long long ri = __shfl_sync(0xffffffffu, pr, i);
+                    const float* src = part_o + ri * D + lane * V;
+                    if (V == 2) {
+                        const float2 x = *reinterpret_cast<const float2*>(src);
+                        acc[0] += wi * x.x;
+                        acc[1] += wi * x.y;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < V; j += 4) {
+                            const float4 x = *reinterpret_cast<const float4*>(src + j);
+                            acc[j % V] += wi * x.x;
+                            acc[(j + 1) % V] += wi * x.y;
+                            acc[(j + 2) % V] += wi * x.z;
+                            acc[(j + 3) % V] += wi * x.w;
+                        }
+                    }
+                }
+            }
+            den = ft::warp_sum(den);
+            const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
+            uint16_t* dst = out + (long long)tok * ld_o + (k.head * G + gh) * D + lane * V;
+            uint32_t o[V / 2];
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) o[j] = pack2<BF>(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+            if (V == 2)
+                *reinterpret_cast<uint32_t*>(dst) = o[0];
+            else if (V == 4)
+                *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1 % (V / 2)]);
+            else
+                *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1 % (V / 2)], o[2 % (V / 2)], o[3 % (V / 2)]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the plan
+
+constexpr int PT = ATTN_MAX_B;  // threads: one per request
+
+struct PlanArgs {
+    AttnPlan pl;
+    int B, T, n_groups, G, Hkv, page, n_rows, row_pages;
+    const int *cu_q, *rows, *group_start, *group_tokens, *lens;
+    unsigned* err;
+};
+
+// What the plan kernel keeps of a segment.
+struct SegRec {
+    int b, r0, nrows, ntile, kend;
+    int cum;  // cost of the segments before it
+};
+
+__device__ int scan_excl(int v, int* ws, int& total) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) ws[wid] = x;
+    __syncthreads();
+    if (wid == 0) {
+        int s = ws[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        ws[lane] = s;
+    }
+    __syncthreads();
+    total = ws[31];
+    return x - v + (wid ? ws[wid - 1] : 0);
+}
+
+// largest i in [0, n) with a[i] <= x (a ascending, a[0] <= x)
+template <class F>
+__device__ __forceinline__ int upper(int n, long long x, F a) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((long long)a(mid) <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+__global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
+    __shared__ int s_n[PT], s_len[PT], s_row[PT], s_P[PT], s_pre[PT], s_sb[PT];  // per request
+    __shared__ int g_min[PT], g_rows[PT], g_solo[PT], g_first[PT];               // per group
+    __shared__ int q_g[PT / 2], q_off[PT / 2];  // per group taken together (it has two requests at least)
+    __shared__ int ws[33];
+    __shared__ int s_c, s_iph;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int B = p.B, G = p.G, n_cta = p.pl.n_cta;
+    SegRec* seg = reinterpret_cast<SegRec*>(p.pl.seg);
+
+    // ---- requests and groups
+    bool ok = true;
+    int n = 0, len = 0, row = 0, gi = -1;
+    if (tid < B) {
+        const int a = p.cu_q[tid], e = p.cu_q[tid + 1];
+        n = e - a;
+        row = p.rows ? p.rows[tid] : tid;
+        if (a < 0 || e < a || e > p.T || (tid == 0 && a != 0) || row < 0 || row >= p.n_rows) ok = false;
+        if (ok) {
+            len = p.lens[row];
+            if (len < 0 || len > (long long)p.row_pages * p.page) ok = false;
+        }
+    }
+    if (tid < p.n_groups) {
+        const int a = p.group_start[tid], e = p.group_start[tid + 1];
+        if (a < 0 || e < a || e > B || p.group_tokens[tid] < 0) ok = false;
+    }
+    if (!__syncthreads_and(ok)) {
+        if (tid == 0) {
+            atomicOr(p.err, FT_DEVERR_ARG);
+            *p.pl.hdr = AttnHdr{0, 0, 0, 0};
+        }
+        for (int i = tid; i <= n_cta; i += PT) p.pl.woff[i] = 0;
+        return;
+    }
+    g_min[tid] = 0x7fffffff;
+    g_rows[tid] = 0;
+    g_solo[tid] = 0;
+    g_first[tid] = 0x7fffffff;
+    s_n[tid] = n;
+    s_len[tid] = len;
+    s_row[tid] = row;
+    __syncthreads();
+    if (tid < B && n > 0 && p.n_groups > 0) {
+        if (p.group_start[0] <= tid) {
+            gi = upper(p.n_groups, tid, [&](int i) { return p.group_start[i]; });
+            if (tid >= p.group_start[gi + 1]) gi = -1;
+        }
+        if (gi >= 0) {
+            atomicMin(&g_min[gi], max(0, len - n));
+            atomicAdd(&g_rows[gi], n * G);
+            atomicAdd(&g_solo[gi], cdiv(n * G, ATTN_BM));
+            atomicMin(&g_first[gi], tid);
+        }
+    }
+    __syncthreads();
+    // a group's shared tokens: whole pages before every query; taken together only where that saves at
+    // least a fifth of the row tiles that run over them (else the join costs more than it saves)
+    int P = 0;
+    if (tid < p.n_groups && g_rows[tid] > 0) {
+        P = min(p.group_tokens[tid], g_min[tid]) / p.page * p.page;
+        if (5 * cdiv(g_rows[tid], ATTN_BM) > 4 * g_solo[tid]) P = 0;
+    }
+    int n_pre;
+    const int my_pre = scan_excl(P > 0, ws, n_pre);
+    g_min[tid] = P;  // from here on: the shared tokens taken
+    if (P > 0) q_g[my_pre] = tid;
+    g_solo[tid] = my_pre;
+    __syncthreads();
+    s_P[tid] = gi >= 0 ? g_min[gi] : 0;
+    s_pre[tid] = gi >= 0 && g_min[gi] > 0 ? g_solo[gi] : -1;
+
+    // ---- chunks of the shared ranges: of up to four rounds over the CTAs, the one that ends first
+    int n_seg;
+    const int my_segs = cdiv(n * G, ATTN_BM);
+    s_sb[tid] = scan_excl(my_segs, ws, n_seg);
+    __syncthreads();
+    int cost = 0;
+    for (int base = 0; base < n_seg; base += PT) {
+        const int s = base + tid;
+        SegRec r{};
+        if (s < n_seg) {
+            r.b = upper(B, s, [&](int i) { return s_sb[i]; });
+            // requests without queries share the next one's start: upper() takes the last of them,
+            // which is the one that has rows
+            r.r0 = (s - s_sb[r.b]) * ATTN_BM;
+            r.nrows = min(ATTN_BM, s_n[r.b] * G - r.r0);
+            const int last = (r.r0 + r.nrows - 1) / G;
+            r.kend = max(0, min(s_len[r.b], s_len[r.b] - s_n[r.b] + 1 + last));
+            r.ntile = max(1, cdiv(r.kend - s_P[r.b], ATTN_BN));
+        }
+        int total;
+        r.cum = cost + scan_excl(s < n_seg ? r.ntile + OV : 0, ws, total);
+        if (s < n_seg) seg[s] = r;
+        cost += total;
+    }
+    const long long S = (long long)cost * p.Hkv;
+    if (wid == 0) {
+        int best_c = 1;
+        long long best = 0x7fffffffffffffffll;
+        if (n_pre > 0) {
+            int rts = 0, mt = 1;
+            for (int i = lane; i < n_pre; i += 32) {
+                rts += cdiv(g_rows[q_g[i]], ATTN_BM);
+                mt = max(mt, cdiv(g_min[q_g[i]], ATTN_BN));
+            }
+            rts = __reduce_add_sync(0xffffffffu, rts);
+            mt = __reduce_max_sync(0xffffffffu, mt);
+            auto items = [&](int c) {
+                int x = 0;
+                for (int i = lane; i < n_pre; i += 32)
+                    x += cdiv(g_rows[q_g[i]], ATTN_BM) * cdiv(cdiv(g_min[q_g[i]], ATTN_BN), c);
+                return (int)__reduce_add_sync(0xffffffffu, x) * p.Hkv;
+            };
+            for (int rounds = 1; rounds <= 4; ++rounds) {
+                const int cap = max(rounds * n_cta, rts * p.Hkv);
+                int lo = 1, hi = mt;  // smallest c with items(c) <= cap
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (items(mid) <= cap) hi = mid; else lo = mid + 1;
+                }
+                const int ni = items(lo);
+                const long long each = lo + OVP;
+                const long long end = max((S + ni * each + n_cta - 1) / n_cta, (long long)cdiv(ni, n_cta) * each);
+                if (end < best) {
+                    best = end;
+                    best_c = lo;
+                }
+            }
+        }
+        if (lane == 0) s_c = best_c;
+    }
+    __syncthreads();
+    const int c = s_c;
+    {
+        int x = 0;
+        if (tid < n_pre) x = cdiv(g_rows[q_g[tid]], ATTN_BM) * cdiv(cdiv(g_min[q_g[tid]], ATTN_BN), c);
+        int iph;
+        const int off = scan_excl(x, ws, iph);
+        if (tid < n_pre) q_off[tid] = off;
+        if (tid == 0) s_iph = iph;
+    }
+    __syncthreads();
+    const int iph = s_iph, n_items = iph * p.Hkv;
+
+    // ---- parts of the line of tiles: CTAs with one prefix item more get less
+    const int k0 = n_items / n_cta, n1 = n_items % n_cta, n0 = n_cta - n1;
+    const long long p0 = (long long)k0 * (c + OVP), p1 = p0 + (n1 ? c + OVP : 0);
+    const long long W = (S + n1 * p1 + n0 * p0 + n_cta - 1) / n_cta;
+    long long q1 = 0, q0;
+    if (n1 && W <= p1) {
+        q0 = (S + n0 - 1) / n0;
+    } else {
+        q1 = n1 ? W - p1 : 0;
+        q0 = W - p0;
+    }
+    if (q0 < 1) q0 = 1;
+    auto start_of = [&](int i) { return min(S, i < n1 ? i * q1 : n1 * q1 + (i - n1) * q0); };
+    auto cta_of = [&](long long x) { return x < n1 * q1 ? (int)(x / q1) : n1 + (int)((x - n1 * q1) / q0); };
+    auto linear = [&](long long x) {  // head * n_seg + segment that holds cost position x
+        const int h = (int)(x / cost);
+        return h * n_seg + upper(n_seg, x - (long long)h * cost, [&](int i) { return seg[i].cum; });
+    };
+    auto begin_of = [&](int l) { return (long long)(l / n_seg) * cost + seg[l % n_seg].cum; };
+    __syncthreads();  // seg is complete
+
+    int n_works = 0;
+    for (int base = 0; base < n_cta; base += PT) {
+        const int i = base + tid;
+        int cnt = 0;
+        if (i < n_cta) {
+            cnt = k0 + (i < n1 ? 1 : 0);
+            const long long x0 = start_of(i), x1 = start_of(i + 1);
+            if (x1 > x0) {
+                const int l1 = linear(x1 - 1);
+                cnt += l1 - linear(x0) + 1;
+                if (x1 - begin_of(l1) <= OV) --cnt;  // only the start cost of the last one: its tiles are the next CTA's
+            }
+        }
+        int total;
+        const int at = n_works + scan_excl(cnt, ws, total);
+        if (i < n_cta) p.pl.woff[i] = at;
+        n_works += total;
+    }
+    if (tid == 0) p.pl.woff[n_cta] = n_works;
+    __syncthreads();
+    // a warp per CTA writes its items
+    for (int i = wid; i < n_cta; i += PT / 32) {
+        const int w0 = p.pl.woff[i], k = k0 + (i < n1 ? 1 : 0);
+        for (int j = lane; j < k; j += 32) {
+            const int idx = j * n_cta + i, h = idx / iph, rem = idx % iph;
+            const int q = upper(n_pre, rem, [&](int a) { return q_off[a]; });
+            const int gg = q_g[q], nrt = cdiv(g_rows[gg], ATTN_BM), nt = cdiv(g_min[gg], ATTN_BN);
+            const int nch = cdiv(nt, c), ch = (rem - q_off[q]) / nrt, rt = (rem - q_off[q]) % nrt;
+            const int t0 = (int)((long long)ch * nt / nch), t1 = (int)((long long)(ch + 1) * nt / nch);
+            AttnWork w;
+            w.head = h;
+            w.trow = s_row[g_first[gg]];
+            w.pos0 = t0 * ATTN_BN;
+            w.ntile = t1 - t0;
+            w.kend = min(g_min[gg], t1 * ATTN_BN);
+            w.vis0 = ATTN_NOMASK;
+            w.tok0 = p.cu_q[p.group_start[gg]];
+            w.r0 = rt * ATTN_BM;
+            w.nrows = min(ATTN_BM, g_rows[gg] - w.r0);
+            w.prow = idx * ATTN_BM;
+            p.pl.works[w0 + j] = w;
+        }
+        const long long x0 = start_of(i), x1 = start_of(i + 1);
+        if (x1 <= x0) continue;
+        const int l0 = linear(x0), l1 = linear(x1 - 1);
+        for (int l = l0 + lane; l <= l1; l += 32) {
+            const long long b0 = begin_of(l);
+            const SegRec r = seg[l % n_seg];
+            const int t0 = (int)max(0ll, x0 - b0 - OV), t1 = (int)min((long long)r.ntile, max(0ll, x1 - b0 - OV));
+            if (t0 >= t1) continue;  // (only ever the last one)
+            AttnWork w;
+            w.head = l / n_seg;
+            w.trow = s_row[r.b];
+            w.pos0 = s_P[r.b] + t0 * ATTN_BN;
+            w.ntile = t1 - t0;
+            w.kend = r.kend;
+            w.vis0 = s_len[r.b] - s_n[r.b] + 1;
+            w.tok0 = p.cu_q[r.b];
+            w.r0 = r.r0;
+            w.nrows = r.nrows;
+            const bool whole = t0 == 0 && t1 == r.ntile;
+            w.prow = whole && s_pre[r.b] < 0 ? -1
+                     : t0 == 0 ? (int)(p.pl.b_row + (long long)w.head * p.T * G + (long long)w.tok0 * G + r.r0)
+                               : (int)(p.pl.c_row + (long long)i * ATTN_BM);
+            p.pl.works[w0 + k + (l - l0)] = w;
+        }
+    }
+    // ---- rows with more than one piece
+    int n_merge = 0;
+    for (int base = 0; base < n_seg * p.Hkv; base += PT) {
+        const int l = base + tid;
+        int cnt = 0, c0 = 0, c1 = 0;
+        SegRec r{};
+        if (l < n_seg * p.Hkv) {
+            r = seg[l % n_seg];
+            const long long b0 = begin_of(l) + OV;
+            c0 = cta_of(b0);
+            c1 = cta_of(b0 + r.ntile - 1);
+            if (c0 != c1 || s_pre[r.b] >= 0) cnt = cdiv(r.nrows, MROWS);
+        }
+        int total;
+        const int at = n_merge + scan_excl(cnt, ws, total);
+        for (int j = 0; j < cnt; ++j) {
+            AttnMerge m;
+            m.head = l / n_seg;
+            m.tok0 = p.cu_q[r.b];
+            m.r0 = r.r0 + j * MROWS;
+            m.nrows = min(MROWS, r.nrows - j * MROWS);
+            m.brow = (int)(p.pl.b_row + (long long)m.head * p.T * G + (long long)m.tok0 * G + m.r0);
+            m.c0 = c0 + 1;
+            m.nc = c1 - c0;
+            m.ptok0 = -1;
+            m.pitem = m.pnrt = m.pnch = 0;
+            const int q = s_pre[r.b];
+            if (q >= 0) {
+                const int gg = q_g[q];
+                m.ptok0 = p.cu_q[p.group_start[gg]];
+                m.pnrt = cdiv(g_rows[gg], ATTN_BM);
+                m.pnch = cdiv(cdiv(g_min[gg], ATTN_BN), c);
+                m.pitem = m.head * iph + q_off[q];
+            }
+            p.pl.merges[at + j] = m;
+        }
+        n_merge += total;
+    }
+    if (tid == 0) *p.pl.hdr = AttnHdr{n_merge, 0, n_works, 0};
+}
+
+// -------------------------------------------------------------- host side
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+template <int D, bool BF>
+cudaError_t launch_typed(ft_kv* kv, const AttnArgs& a, const AttnPlan& pl) {
+    cudaError_t e = ensure_dynamic_smem((const void*)attn_kernel<D, BF>, Cfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    attn_kernel<D, BF><<<pl.n_cta, G_THREADS, Cfg<D>::SMEM, kv->stream>>>(kv->map, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_dependent(attn_merge_kernel<D, BF>, dim3(kv->num_sms * 4), dim3(256), 0, kv->stream, pl.hdr, pl.merges,
+                            kv->part_o, kv->part_ml, pl.c_row, a.G, a.out, a.ld_o);
+}
+
+}  // namespace
+
+void attn_plan_sizes(int Hq, int Hkv, int D, int T_max, int B_max, int num_sms, AttnPlan& p) {
+    const int G = Hq / Hkv;
+    const int rts = (int)(((long long)T_max * G + ATTN_BM - 1) / ATTN_BM);
+    p.n_cta = num_sms * (D == 256 ? 1 : 2);
+    p.cap_segs = rts + B_max;                          // a request's last tile may be short
+    p.cap_items = 4 * p.n_cta + Hkv * (rts + B_max);   // four rounds, or a chunk for each row tile
+    p.cap_works = p.cap_items + Hkv * p.cap_segs + p.n_cta;
+    p.cap_merges = Hkv * p.cap_segs * (ATTN_BM / MROWS);
+    p.b_row = (long long)p.cap_items * ATTN_BM;
+    p.c_row = p.b_row + (long long)T_max * Hq;
+    p.part_rows = p.c_row + (long long)p.n_cta * ATTN_BM;
+}
+
+size_t attn_seg_bytes(const AttnPlan& p) { return (size_t)p.cap_segs * sizeof(SegRec); }
+
+// The pool as [n_pages*L*2*Hkv][page][D], read in boxes of 64 values by a
+// page's rows (at most 64) with 128-byte swizzle.
+bool attn_encode_map(ft_kv* kv) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+        return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)kv->D, (cuuint64_t)kv->page, (cuuint64_t)kv->n_pages * kv->L * 2 * kv->Hkv};
+    const cuuint64_t strides[2] = {(cuuint64_t)kv->D * 2, (cuuint64_t)kv->D * 2 * kv->page};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(kv->page < ATTN_BN ? kv->page : ATTN_BN), 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return reinterpret_cast<EncodeTiledFn>(f)(
+               &kv->map, kv->dtype == FT_KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+               kv->pool, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_attn_plan(ft_kv* kv, int B, int T, const int* cu_q, const int* rows, int n_groups,
+                             const int* group_start, const int* group_tokens) {
+    PlanArgs a{kv->plan, B, T, n_groups, kv->Hq / kv->Hkv, kv->Hkv, kv->page, kv->n_rows, kv->row_pages,
+               cu_q, rows, group_start, group_tokens, kv->lens, kv->err};
+    attn_plan_kernel<<<1, PT, 0, kv->stream>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_forward(ft_kv* kv, int layer, const void* q, long long ld_q, void* out, long long ld_o,
+                                float scale) {
+    AttnArgs a{};
+    a.works = kv->plan.works;
+    a.woff = kv->plan.woff;
+    a.q = static_cast<const uint16_t*>(q);
+    a.ld_q = ld_q;
+    a.out = static_cast<uint16_t*>(out);
+    a.ld_o = ld_o;
+    a.table = kv->table;
+    a.row_pages = kv->row_pages; a.page = kv->page; a.n_pages = kv->n_pages; a.L = kv->L; a.Hkv = kv->Hkv;
+    a.G = kv->Hq / kv->Hkv;
+    a.layer = layer;
+    a.c = scale * LOG2E;
+    a.part_o = kv->part_o;
+    a.part_ml = kv->part_ml;
+    a.err = kv->err;
+    const bool bf = kv->dtype == FT_KV_BF16;
+    if (kv->D == 64) return bf ? launch_typed<64, true>(kv, a, kv->plan) : launch_typed<64, false>(kv, a, kv->plan);
+    if (kv->D == 128) return bf ? launch_typed<128, true>(kv, a, kv->plan) : launch_typed<128, false>(kv, a, kv->plan);
+    return bf ? launch_typed<256, true>(kv, a, kv->plan) : launch_typed<256, false>(kv, a, kv->plan);
+}

@@ -1,0 +1,154 @@
+// The paged key/value cache's handle, its plan records and the launchers of
+// its kernels.  Internal to libft (the ABI is include/ft_kv.h).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/ft_kv.h"
+#include "ft_common.cuh"
+
+#define FT_DEVERR_CAPACITY 4u  // too few free pages
+
+// Words of the page operations' summary.
+enum { KV_ALLOCATED = 0, KV_COPIED, KV_LIVE, KV_INFO_WORDS };
+
+// One page to copy: the first `tok` tokens of every bank of record src to dst.
+struct KvCopy {
+    int src, dst, tok;
+};
+
+// ------------------------------------------------------------ attention plan
+//
+// A segment is up to 128 query rows of one key/value head that run over one
+// range of keys.  Row r of an owner (a request, or the requests of a group
+// taken together) is query token tok0 + r / G, query head h*G + r % G, with
+// G = Hq / Hkv: token-major, so that the rows of consecutive requests are
+// consecutive.  A work item is a segment of one head, or the part of one that
+// a CTA got.
+
+constexpr int ATTN_BM = 128;        // rows of a work item (TMEM lanes)
+constexpr int ATTN_BN = 64;         // keys of a tile
+constexpr int ATTN_MAX_B = 1024;    // requests of a plan (one thread each)
+constexpr int ATTN_NOMASK = 1 << 30;
+
+struct AttnWork {
+    int head;     // key/value head
+    int trow;     // table row whose pages hold the keys
+    int pos0;     // position of the first key of the first tile
+    int ntile;    // 64-key tiles
+    int kend;     // keys at positions >= kend are not there
+    int vis0;     // token i of the owner sees positions < vis0 + i
+    int tok0;     // first query token of the owner
+    int r0;       // row of the owner that is row 0 here
+    int nrows;    // 1..128
+    int prow;     // first row of the partial result, or -1: write the output
+};
+
+struct AttnMerge {
+    int head, tok0, r0, nrows;  // as in AttnWork
+    int brow;                   // partial row of the piece that starts the segment
+    int c0, nc;                 // CTAs c0 .. c0+nc-1 hold further pieces
+    int ptok0;                  // first token of the group whose shared prefix these rows ran over, or -1
+    int pitem, pnrt, pnch;      // its first item of this head, row tiles and chunks
+};
+
+struct AttnHdr {
+    int n_merge;
+    int merge_rows;
+    int n_works;
+    int pad;
+};
+
+struct AttnPlan {
+    AttnHdr* hdr;
+    int* woff;          // [n_cta + 1] first work item of each CTA
+    AttnWork* works;    // [cap_works]
+    AttnMerge* merges;  // [cap_merges]
+    // scratch of the plan kernel
+    int* seg;           // [cap_segs * SEG_WORDS]
+    int n_cta;
+    int cap_segs, cap_works, cap_merges;
+    int cap_items;      // prefix items (region A of the partials)
+    long long b_row;    // first row of region B (a segment's first piece)
+    long long c_row;    // first row of region C (one piece per CTA)
+    long long part_rows;
+};
+
+struct ft_kv {
+    int L, Hq, Hkv, D, page, n_pages, n_rows, row_pages, dtype, T_max, B_max;
+    int device, num_sms;
+    uint8_t* pool;
+    int *table, *lens, *refs;
+    cudaStream_t stream;
+    void* arena;
+    unsigned* err;
+    int* info;         // [KV_INFO_WORDS]
+    int* n_copy;       // pages of the copy list
+    KvCopy* copies;    // [n_pages]
+    int* free_list;    // [n_pages]
+    int* remap;        // [n_pages]
+    int* mark;         // [n_rows] zero at rest
+    int* rank;         // [n_rows]
+    AttnPlan plan;
+    float* part_o;     // [part_rows, D] unnormalised partial outputs
+    float2* part_ml;   // [part_rows] running maximum (log2 units) and sum
+    bool have_plan;
+    int plan_T;
+    CUtensorMap map;   // [n_pages*L*2*Hkv][page][D] of the pool
+};
+
+cudaError_t launch_kv_extend(ft_kv* kv, int n, const int* rows, const int* add);
+cudaError_t launch_kv_fork(ft_kv* kv, int n, const int* parents, const int* children);
+cudaError_t launch_kv_free(ft_kv* kv, int n, const int* rows);
+cudaError_t launch_kv_compact(ft_kv* kv);
+
+struct RopeArgs {
+    const void* qkv;
+    long long ld;
+    const int* row_of;
+    const int* pos;
+    void* q_out;
+    long long ld_q;
+    const void* q_norm;
+    const void* k_norm;
+    float eps;
+    const float* cos_sin;
+    int max_pos, rot, pair, layer, T;
+};
+cudaError_t launch_qk_rope_store(ft_kv* kv, const RopeArgs& a);
+
+// sizes of a plan's arrays and of the partial results
+void attn_plan_sizes(int Hq, int Hkv, int D, int T_max, int B_max, int num_sms, AttnPlan& p);
+size_t attn_seg_bytes(const AttnPlan& p);
+bool attn_encode_map(ft_kv* kv);
+cudaError_t launch_attn_plan(ft_kv* kv, int B, int T, const int* cu_q, const int* rows, int n_groups,
+                             const int* group_start, const int* group_tokens);
+cudaError_t launch_attn_forward(ft_kv* kv, int layer, const void* q, long long ld_q, void* out, long long ld_o,
+                                float scale);
+
+// Launch on s as a programmatic dependent of the kernel before it: the kernel
+// may start while that one drains and waits for its end by grid_dep_wait().
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_dependent(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                                    Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, KArgs(args)...);
+}
+
+namespace ft {
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+}  // namespace ft

@@ -1,0 +1,344 @@
+// Page operations of the key/value cache: one control kernel per call (one
+// CTA: it validates the whole list before it changes anything) and, where
+// pages move, a copy kernel over all layers.
+#include "ft_kv.cuh"
+
+namespace {
+
+constexpr int CT = 1024;  // threads of the control kernels
+
+struct KvCtl {
+    int *table, *lens, *refs;
+    int n_pages, n_rows, row_pages, page;
+    int *info, *n_copy, *free_list, *remap, *mark, *rank;
+    KvCopy* copies;
+    unsigned* err;
+};
+
+KvCtl ctl_of(const ft_kv* kv) {
+    return KvCtl{kv->table, kv->lens, kv->refs, kv->n_pages, kv->n_rows, kv->row_pages, kv->page,
+                 kv->info, kv->n_copy, kv->free_list, kv->remap, kv->mark, kv->rank, kv->copies, kv->err};
+}
+
+// Exclusive prefix sum over the CTA; total gets the sum.  ws: 33 ints.
+__device__ int block_scan(int v, int* ws, int& total) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // the previous call's reads of ws are over
+    if (lane == 31) ws[wid] = x;
+    __syncthreads();
+    if (wid == 0) {
+        int s = ws[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        ws[lane] = s;
+    }
+    __syncthreads();
+    total = ws[31];
+    return x - v + (wid ? ws[wid - 1] : 0);
+}
+
+// The lowest `want` free pages, ascending, to list; returns how many there are
+// (at most a few more than `want` are counted).  Four counts a thread and step.
+__device__ int take_free(const KvCtl& c, int want, int* ws) {
+    int have = 0;
+    for (int base = 0; base < c.n_pages && have < want; base += 4 * CT) {
+        const int p = base + 4 * threadIdx.x;
+        unsigned f = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (p + j < c.n_pages && c.refs[p + j] == 0) f |= 1u << j;
+        int total;
+        int at = have + block_scan(__popc(f), ws, total);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (f >> j & 1u) {
+                if (at < want) c.free_list[at] = p + j;
+                ++at;
+            }
+        have += total;
+    }
+    __syncthreads();
+    return have;
+}
+
+// Rows rows[0..n) are in range and distinct, and none of others[0..n) (may be
+// null) is among them (every thread gets the answer).
+__device__ bool rows_ok(const KvCtl& c, int n, const int* rows, const int* others = nullptr) {
+    bool ok = true;
+    for (int i = threadIdx.x; i < n; i += CT) {
+        const int r = rows[i];
+        if (r < 0 || r >= c.n_rows)
+            ok = false;
+        else if (atomicExch(&c.mark[r], 1))
+            ok = false;
+    }
+    __syncthreads();
+    if (others) {
+        for (int i = threadIdx.x; i < n; i += CT) {
+            const int r = others[i];
+            if (r < 0 || r >= c.n_rows || c.mark[r]) ok = false;
+        }
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < n; i += CT) {
+        const int r = rows[i];
+        if (r >= 0 && r < c.n_rows) c.mark[r] = 0;
+    }
+    return __syncthreads_and(ok);
+}
+
+__device__ void set_info(const KvCtl& c, int allocated, int copied, int live) {
+    if (threadIdx.x == 0) {
+        c.info[KV_ALLOCATED] = allocated;
+        c.info[KV_COPIED] = copied;
+        c.info[KV_LIVE] = live;
+        *c.n_copy = copied;
+    }
+}
+
+__device__ void refuse(const KvCtl& c, unsigned bit) {
+    if (threadIdx.x == 0) atomicOr(c.err, bit);
+    set_info(c, 0, 0, -1);
+}
+
+__global__ void __launch_bounds__(CT) kv_extend_kernel(KvCtl c, int n, const int* __restrict__ rows,
+                                                       const int* __restrict__ add) {
+    __shared__ int ws[33];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    if (!rows_ok(c, n, rows)) return refuse(c, FT_DEVERR_ARG);
+    int want = 0;
+    bool ok = true;
+    for (int base = 0; base < n; base += CT) {
+        const int i = base + threadIdx.x;
+        int need = 0;
+        if (i < n) {
+            const long long len = c.lens[rows[i]], to = len + add[i];
+            if (len < 0 || add[i] < 0 || to > (long long)c.row_pages * c.page)
+                ok = false;
+            else
+                need = (int)((to + c.page - 1) / c.page - (len + c.page - 1) / c.page);
+        }
+        int total;
+        const int at = want + block_scan(need, ws, total);
+        if (i < n) c.rank[i] = at;
+        want += total;
+    }
+    if (!__syncthreads_and(ok)) return refuse(c, FT_DEVERR_ARG);
+    if (take_free(c, want, ws) < want) return refuse(c, FT_DEVERR_CAPACITY);
+    for (int i = wid; i < n; i += CT / 32) {
+        const int r = rows[i], len = c.lens[r], to = len + add[i], at = c.rank[i];
+        const int have = (len + c.page - 1) / c.page, end = (to + c.page - 1) / c.page;
+        for (int j = have + lane; j < end; j += 32) {
+            const int p = c.free_list[at + j - have];
+            c.table[(size_t)r * c.row_pages + j] = p;
+            c.refs[p] = 1;
+        }
+        __syncwarp();
+        if (lane == 0) c.lens[r] = to;
+    }
+    set_info(c, want, 0, -1);
+}
+
+__global__ void __launch_bounds__(CT) kv_fork_kernel(KvCtl c, int n, const int* __restrict__ parents,
+                                                     const int* __restrict__ children) {
+    __shared__ int ws[33];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    if (!rows_ok(c, n, children, parents)) return refuse(c, FT_DEVERR_ARG);
+    int want = 0;
+    bool ok = true;
+    for (int base = 0; base < n; base += CT) {
+        const int i = base + threadIdx.x;
+        int need = 0;
+        if (i < n) {
+            const int p = parents[i];
+            if (c.lens[children[i]] != 0) {
+                ok = false;
+            } else {
+                const int len = c.lens[p];
+                if (len < 0 || len > (long long)c.row_pages * c.page) ok = false;
+                need = ok && len % c.page ? 1 : 0;
+            }
+        }
+        int total;
+        const int at = want + block_scan(need, ws, total);
+        if (i < n) c.rank[i] = at;
+        want += total;
+    }
+    if (!__syncthreads_and(ok)) return refuse(c, FT_DEVERR_ARG);
+    for (int i = wid; i < n; i += CT / 32) {
+        const int* row = c.table + (size_t)parents[i] * c.row_pages;
+        const int np = (c.lens[parents[i]] + c.page - 1) / c.page;
+        for (int j = lane; j < np; j += 32)
+            if (row[j] < 0 || row[j] >= c.n_pages) ok = false;
+    }
+    if (!__syncthreads_and(ok)) return refuse(c, FT_DEVERR_ARG);
+    if (take_free(c, want, ws) < want) return refuse(c, FT_DEVERR_CAPACITY);
+    for (int i = wid; i < n; i += CT / 32) {
+        const int p = parents[i], len = c.lens[p], full = len / c.page, tok = len % c.page;
+        const int* src = c.table + (size_t)p * c.row_pages;
+        int* dst = c.table + (size_t)children[i] * c.row_pages;
+        for (int j = lane; j < c.row_pages; j += 32) {
+            int v = -1;
+            if (j < full) {
+                v = src[j];
+                atomicAdd(&c.refs[v], 1);
+            } else if (j == full && tok) {
+                v = c.free_list[c.rank[i]];
+                c.refs[v] = 1;
+                c.copies[c.rank[i]] = KvCopy{src[j], v, tok};
+            }
+            dst[j] = v;
+        }
+        if (lane == 0) c.lens[children[i]] = len;
+    }
+    set_info(c, want, want, -1);
+}
+
+__global__ void __launch_bounds__(CT) kv_free_kernel(KvCtl c, int n, const int* __restrict__ rows) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    bool ok = rows_ok(c, n, rows);
+    if (!ok) return refuse(c, FT_DEVERR_ARG);
+    for (int i = wid; i < n; i += CT / 32) {
+        const int r = rows[i];
+        const long long len = c.lens[r];
+        if (len < 0 || len > (long long)c.row_pages * c.page) ok = false;
+        const int np = ok ? (int)((len + c.page - 1) / c.page) : 0;
+        for (int j = lane; j < np; j += 32) {
+            const int p = c.table[(size_t)r * c.row_pages + j];
+            if (p < 0 || p >= c.n_pages) ok = false;
+        }
+    }
+    if (!__syncthreads_and(ok)) return refuse(c, FT_DEVERR_ARG);
+    for (int i = wid; i < n; i += CT / 32) {
+        const int r = rows[i];
+        const int np = (c.lens[r] + c.page - 1) / c.page;
+        for (int j = lane; j < np; j += 32) {
+            int* e = c.table + (size_t)r * c.row_pages + j;
+            const int p = *e;
+            *e = -1;
+            if (atomicSub(&c.refs[p], 1) <= 0) {
+                atomicAdd(&c.refs[p], 1);
+                ok = false;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) c.lens[r] = 0;
+    }
+    if (!ok) atomicOr(c.err, FT_DEVERR_ARG);
+    set_info(c, 0, 0, -1);
+}
+
+// live = pages in use; the k-th page in use at index >= live pairs with the
+// k-th free page below it (there are equally many).  The two lists fill the
+// copy list's ends independently, so both scans are one pass over refs.
+__global__ void __launch_bounds__(CT) kv_compact_kernel(KvCtl c) {
+    __shared__ int ws[33];
+    int live = 0;
+    for (int p = threadIdx.x; p < c.n_pages; p += CT) live += c.refs[p] > 0;
+    block_scan(live, ws, live);
+    int holes = 0, movers = 0;
+    for (int base = 0; base < c.n_pages; base += CT) {
+        const int p = base + threadIdx.x;
+        const bool in = p < c.n_pages, used = in && c.refs[p] > 0;
+        const bool hole = in && p < live && !used, mover = used && p >= live;
+        // at most 2^10 of each kind in a step: both counts in one word
+        int total;
+        const int at = block_scan((hole ? 1 : 0) | (mover ? 1 << 16 : 0), ws, total);
+        if (hole) c.copies[holes + (at & 0xffff)].dst = p;
+        if (mover) c.copies[movers + (at >> 16)].src = p;
+        holes += total & 0xffff;
+        movers += total >> 16;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < movers; i += CT) {
+        KvCopy& k = c.copies[i];
+        k.tok = c.page;
+        c.remap[k.src] = k.dst;
+        c.refs[k.dst] = c.refs[k.src];
+        c.refs[k.src] = 0;
+    }
+    set_info(c, 0, movers, live);
+}
+
+// The copies of the list.  A unit is 4 KiB of one bank of one page (a warp
+// moves 512 bytes an instruction, eight loads in flight); banks of a page that
+// is copied in part have their first tok*D values copied.  With `live` set,
+// the table's entries past the live pages are replaced too.
+__global__ void __launch_bounds__(256) kv_copy_kernel(const int* n_copy, const KvCopy* __restrict__ copies, uint8_t* pool,
+                                                      int banks, int bank_bytes, int tok_bytes, int* table,
+                                                      long long entries, const int* __restrict__ remap,
+                                                      const int* live, int n_pages) {
+    ft::grid_dep_wait();
+    const int lane = threadIdx.x & 31;
+    const long long wid = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const long long nw = (long long)gridDim.x * (blockDim.x >> 5);
+    const int n = *n_copy;
+    const int subs = (bank_bytes + 4095) / 4096;
+    const long long units = (long long)n * banks * subs;
+    for (long long u = wid; u < units; u += nw) {
+        const int sub = (int)(u % subs);
+        const long long pb = u / subs;
+        const int b = (int)(pb % banks);
+        const KvCopy k = copies[pb / banks];
+        const int bytes = k.tok * tok_bytes - sub * 4096;
+        const size_t off = (size_t)b * bank_bytes + (size_t)sub * 4096 + lane * 16;
+        const uint8_t* s = pool + (size_t)k.src * banks * bank_bytes + off;
+        uint8_t* d = pool + (size_t)k.dst * banks * bank_bytes + off;
+        uint4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j * 512 + lane * 16 < bytes) v[j] = __ldcs(reinterpret_cast<const uint4*>(s + j * 512));
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j * 512 + lane * 16 < bytes) __stcs(reinterpret_cast<uint4*>(d + j * 512), v[j]);
+    }
+    if (live) {
+        const int lv = *live;
+        const long long step = (long long)gridDim.x * blockDim.x;
+        for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < entries; i += step) {
+            const int p = table[i];
+            if (p >= lv && p < n_pages) table[i] = remap[p];
+        }
+    }
+}
+
+cudaError_t launch_copy(ft_kv* kv, bool compact) {
+    const int banks = kv->L * 2 * kv->Hkv, bank_bytes = kv->page * kv->D * 2;
+    const long long entries = compact ? (long long)kv->n_rows * kv->row_pages : 0;
+    return launch_dependent(kv_copy_kernel, dim3(kv->num_sms * 8), dim3(256), 0, kv->stream, kv->n_copy, kv->copies,
+                            kv->pool, banks, bank_bytes, kv->D * 2, kv->table, entries, kv->remap,
+                            compact ? kv->info + KV_LIVE : nullptr, kv->n_pages);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_extend(ft_kv* kv, int n, const int* rows, const int* add) {
+    kv_extend_kernel<<<1, CT, 0, kv->stream>>>(ctl_of(kv), n, rows, add);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_fork(ft_kv* kv, int n, const int* parents, const int* children) {
+    kv_fork_kernel<<<1, CT, 0, kv->stream>>>(ctl_of(kv), n, parents, children);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? launch_copy(kv, false) : e;
+}
+
+cudaError_t launch_kv_free(ft_kv* kv, int n, const int* rows) {
+    kv_free_kernel<<<1, CT, 0, kv->stream>>>(ctl_of(kv), n, rows);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_compact(ft_kv* kv) {
+    kv_compact_kernel<<<1, CT, 0, kv->stream>>>(ctl_of(kv));
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? launch_copy(kv, true) : e;
+}
