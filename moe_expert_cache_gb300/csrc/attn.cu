@@ -8,7 +8,7 @@
 //   out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,   M = max m_k.
 //
 // A work item is up to 128 query rows of one key/value head (the G query heads
-// of a token are G rows) over a range of 64-key tiles.  Where a group shares a
+// of a token are G rows) over a range of 128-key tiles.  Where a group shares a
 // prefix, the rows of all its requests form the tiles that run over it, so each
 // key is read once for 128 rows; the requests' own keys follow as items of
 // their own rows.  Work is laid out by the plan kernel: the shared ranges in
@@ -30,18 +30,19 @@ namespace {
 constexpr int G_THREADS = 192;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_LAG = 8.f;   // log2 units
+constexpr int NWORK = 16;            // work items of a CTA that are kept in shared memory
 constexpr int OV = 2;                // cost of an item's start, in tiles
 constexpr int OVP = 4;               // the same with the partial result of a prefix item
-constexpr int MROWS = 16;            // rows of a merge record
 
 template <int D>
 struct Cfg {
-    static constexpr int NST = D == 64 ? 8 : D == 128 ? 4 : 5;
-    static constexpr uint32_t STAGE = ATTN_BN * D * 2;
-    static constexpr uint32_t QBYTES = ATTN_BM * D * 2;
-    static constexpr uint32_t TCOLS = D == 256 ? 512 : 256;  // O: D columns, S: 2 x 64
     static constexpr int CTAS = D == 256 ? 1 : 2;            // per SM
-    static constexpr size_t SMEM = 1024 + QBYTES + (size_t)NST * STAGE;
+    static constexpr uint32_t TCOLS = D == 256 ? 512 : 256;  // O: D columns, S: NS x 128
+    static constexpr int NS = D == 256 ? 2 : 1;
+    static constexpr uint32_t TILE = ATTN_BN * D * 2;
+    static constexpr uint32_t QBYTES = ATTN_BM * D * 2;
+    static constexpr int NST = D == 64 ? 6 : 2;              // K and V tiles in the ring
+    static constexpr size_t SMEM = QBYTES + (size_t)NST * TILE;
 };
 
 struct AttnArgs {
@@ -63,6 +64,28 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two fp32 operations in one instruction, on the halves of a 64-bit register.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ float2 unf2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 template <bool BF>
@@ -113,63 +136,82 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 32 bytes to global memory in one store (a whole sector of one row).
+__device__ __forceinline__ void st_global32(void* d, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 template <int D, bool BF>
 __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __grid_constant__ CUtensorMap map,
                                                                        const AttnArgs p) {
     using C = Cfg<D>;
-    constexpr int NST = C::NST;
-    extern __shared__ __align__(1024) unsigned char raw[];
-    __shared__ uint64_t kv_full[NST], kv_empty[NST], s_full[2], p_full[2], pv_done[2], q_full, o_full, o_empty, done;
+    constexpr int NST = C::NST, NS = C::NS;
+    extern __shared__ __align__(1024) unsigned char smQ[];  // Q, then the ring
+    __shared__ uint64_t kv_full[NST], kv_empty[NST], s_full[NS], p_full[NS][2], pv_done[2], q_full, o_full, o_empty, done;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_fail;
-    unsigned char* smQ = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    __shared__ AttnWork s_work[NWORK];
     unsigned char* ring = smQ + C::QBYTES;
     const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
 
     ft::grid_dep_launch();
     const int w0 = p.woff[blockIdx.x], w1 = p.woff[blockIdx.x + 1];
     if (w0 == w1) return;
-
-    if (tid == 0) {
+    auto load_q = [&](const AttnWork& k) {
+        constexpr int CH = D / 8;  // 16-byte chunks of a row
+        for (int i = tid; i < k.nrows * CH; i += 128) {
+            const int rr = i / CH, ch = i % CH;
+            const int R = k.r0 + rr, tok = k.tok0 + R / p.G, gh = k.head * p.G + R % p.G;
+            ft::cp_async16(smQ + (ch >> 3) * (ATTN_BM * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
+                           p.q + (long long)tok * p.ld_q + gh * D + ch * 8);
+        }
+    };
+    if (wid < 4) load_q(p.works[w0]);
+    for (int i = tid; i < min(w1 - w0, NWORK) * (int)(sizeof(AttnWork) / 4); i += G_THREADS)
+        reinterpret_cast<int*>(s_work)[i] = reinterpret_cast<const int*>(p.works + w0)[i];
+    if (tid == 128) {
         for (int s = 0; s < NST; ++s) {
             ft::mbar_init(&kv_full[s], 1);
             ft::mbar_init(&kv_empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < NS; ++b) {
             ft::mbar_init(&s_full[b], 1);
-            ft::mbar_init(&p_full[b], 4);
-            ft::mbar_init(&pv_done[b], 1);
+            ft::mbar_init(&p_full[b][0], 4);
+            ft::mbar_init(&p_full[b][1], 4);
         }
+        for (int b = 0; b < 2; ++b) ft::mbar_init(&pv_done[b], 1);
         ft::mbar_init(&q_full, 4);
         ft::mbar_init(&o_full, 1);
         ft::mbar_init(&o_empty, 4);
         ft::mbar_init(&done, 1);
         ft::mbar_fence_init();
         s_fail = 0;
+        tc::prefetch_map(&map);
     }
-    if (wid == 4 && lane == 0) tc::prefetch_map(&map);
     if (wid == 5) tc::tmem_alloc(&s_tmem, C::TCOLS);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = s_tmem;
+    auto work = [&](int w) -> AttnWork { return w - w0 < NWORK ? s_work[w - w0] : p.works[w]; };
 
     if (wid == 4) {
         // ------------------------------------------------------------ TMA warp
-        // order of the ring: K0, K1, V0, K2, V1, ...
-        const int sub_rows = min(p.page, ATTN_BN);           // rows of a box
+        // order of the ring: K0, V0, K1, V1, ... with one S, K0, K1, V0, K2, V1, ... with two
         constexpr int NB = D / 64;                           // boxes across a row
-        const int boxes = (ATTN_BN / sub_rows) * NB;
+        const int boxes = (ATTN_BN / p.page) * NB;           // a box is a page's rows by 64 values
         const int sub = lane / NB, blk = lane % NB;
         const bool mine = lane < boxes;
         const int oob = p.n_pages * p.L * 2 * p.Hkv;         // a box past the map's end reads zeros
         int it = 0;
         bool ok = true;
         for (int w = w0; w < w1 && ok && !__any_sync(0xffffffffu, s_fail); ++w) {
-            const AttnWork k = p.works[w];
+            const AttnWork k = work(w);
             const int* row = p.table + (size_t)k.trow * p.row_pages;
             auto page_of = [&](int i) {  // page of this lane's box of tile i, or -1 past the keys
-                const int pos = k.pos0 + i * ATTN_BN + sub * sub_rows;
+                const int pos = k.pos0 + i * ATTN_BN + sub * p.page;
                 if (!mine || i >= k.ntile || pos >= k.kend) return -1;
                 const int id = row[pos / p.page];
                 if (id < 0 || id >= p.n_pages) {
@@ -178,26 +220,29 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                 }
                 return id;
             };
-            auto issue = [&](int id, int i, int kv) {
+            auto issue = [&](int id, int kv) {
                 const int st = it % NST;
                 if (it >= NST && !ft::mbar_wait(&kv_empty[st], ((it / NST) - 1) & 1, p.err)) ok = false;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
-                if (lane == 0) ft::mbar_arrive_expect_tx(&kv_full[st], C::STAGE);
+                if (lane == 0) ft::mbar_arrive_expect_tx(&kv_full[st], C::TILE);
                 __syncwarp();
                 if (mine) {
-                    const int pos = k.pos0 + i * ATTN_BN + sub * sub_rows;
                     const int z = id < 0 ? oob : ((id * p.L + p.layer) * 2 + kv) * p.Hkv + k.head;
-                    unsigned char* dst = ring + (size_t)st * C::STAGE + blk * (ATTN_BN * 128) + sub * sub_rows * 128;
-                    tc::tma_load_3d(dst, &map, blk * 64, pos % p.page, z, &kv_full[st]);
+                    unsigned char* dst = ring + (size_t)st * C::TILE + blk * (ATTN_BN * 128) + sub * p.page * 128;
+                    tc::tma_load_3d(dst, &map, blk * 64, 0, z, &kv_full[st]);
                 }
                 ++it;
             };
             int prev = -1, cur = page_of(0);
             for (int i = 0; i <= k.ntile && ok; ++i) {
                 const int next = page_of(i + 1);
-                if (i < k.ntile) issue(cur, i, 0);
-                if (ok && i > 0) issue(prev, i - 1, 1);
+                if (i < k.ntile) issue(cur, 0);
+                if (NS == 1) {
+                    if (ok && i < k.ntile) issue(cur, 1);
+                } else {
+                    if (ok && i > 0) issue(prev, 1);
+                }
                 prev = cur;
                 cur = next;
             }
@@ -210,17 +255,18 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
         if (lane == 0) {
             constexpr uint32_t id_s = idesc_of(BF, ATTN_BN, false), id_o = idesc_of(BF, D, true);
             int it = 0, g = 0, n = 0;
+            uint32_t ph = 0;  // phase bits of p_full[b][h], at 2 b + h
             bool ok = true;
             auto wait = [&](uint64_t* b, int ph) {
                 if (ok && !ft::mbar_wait(b, (uint32_t)ph & 1u, p.err)) ok = false;
                 return ok;
             };
-            auto scores = [&](int t) {  // S[t & 1] = Q K^T with the next tile of the ring
+            auto scores = [&](int t) {  // S[t % NS] = Q K^T with the next tile of the ring
                 const int st = it % NST;
                 if (!wait(&kv_full[st], it / NST)) return;
                 tc::fence_after_sync();
-                const uint32_t d = tmem + (uint32_t)(D + (t & 1) * ATTN_BN);
-                const unsigned char* kt = ring + (size_t)st * C::STAGE;
+                const uint32_t d = tmem + (uint32_t)(D + (t % NS) * ATTN_BN);
+                const unsigned char* kt = ring + (size_t)st * C::TILE;
 #pragma unroll
                 for (int b = 0; b < D / 64; ++b) {
                     const uint64_t ad = tc::sdesc_k_sw128(smQ + b * (ATTN_BM * 128));
@@ -230,31 +276,43 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                         tc::mma_bf16(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), id_s, (b | j) ? 1u : 0u);
                 }
                 tc::mma_commit(&kv_empty[st]);
-                tc::mma_commit(&s_full[t & 1]);
+                tc::mma_commit(&s_full[t % NS]);
                 ++it;
             };
             for (int w = w0; w < w1 && ok && !s_fail; ++w, ++n) {
-                const int nt = p.works[w].ntile;
+                const AttnWork k = work(w);
+                const int nt = k.ntile;
                 if (!wait(&q_full, n)) break;
                 tc::fence_after_sync();
                 scores(g);
-                if (nt > 1 && ok) scores(g + 1);
                 for (int i = 0; i < nt && ok; ++i, ++g) {
-                    if (!wait(&p_full[g & 1], g >> 1)) break;
+                    if (NS == 2 && i + 1 < nt) scores(g + 1);
                     if (i == 0 && n > 0 && !wait(&o_empty, n - 1)) break;
                     const int st = it % NST;
                     if (!wait(&kv_full[st], it / NST)) break;
-                    tc::fence_after_sync();
-                    const uint32_t a = tmem + (uint32_t)(D + (g & 1) * ATTN_BN);
-                    const uint64_t vd = sdesc_mn_sw128(ring + (size_t)st * C::STAGE, ATTN_BN * 128);
+                    const uint32_t a = tmem + (uint32_t)(D + (g % NS) * ATTN_BN);
+                    const uint64_t vd = sdesc_mn_sw128(ring + (size_t)st * C::TILE, ATTN_BN * 128);
+                    const bool two = k.kend - (k.pos0 + i * ATTN_BN) > 64;
+                    uint32_t acc = i ? 1u : 0u;
 #pragma unroll
-                    for (int j = 0; j < ATTN_BN / 16; ++j)  // 16 keys: 8 columns of P, 2048 bytes of V
-                        mma_ts(tmem, a + (uint32_t)(8 * j), vd + (uint64_t)(128 * j), id_o, (i | j) ? 1u : 0u);
+                    for (int h = 1; h >= 0; --h) {  // the upper 64 keys first: their weights are ready first
+                        if (h == 1 && !two) continue;
+                        const int b = 2 * (g % NS) + h;
+                        if (!wait(&p_full[g % NS][h], (ph >> b) & 1)) break;
+                        ph ^= 1u << b;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {  // 16 keys: 8 columns of P, 2048 bytes of V
+                            mma_ts(tmem, a + (uint32_t)(64 * h + 8 * j), vd + (uint64_t)(128 * (4 * h + j)), id_o, acc);
+                            acc = 1u;
+                        }
+                    }
+                    if (!ok) break;
                     tc::mma_commit(&kv_empty[st]);
-                    tc::mma_commit(&pv_done[g & 1]);
+                    if (NS == 2) tc::mma_commit(&pv_done[g & 1]);
                     if (i == nt - 1) tc::mma_commit(&o_full);
                     ++it;
-                    if (i + 2 < nt) scores(g + 2);
+                    if (NS == 1 && i + 1 < nt) scores(g + 1);
                 }
             }
             if (!ok) s_fail = 1;
@@ -265,15 +323,6 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
         // ------------------------------------------------------- softmax warps
         const int r = tid;  // row of the item: TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)(wid * 32) << 16);
-        auto load_q = [&](const AttnWork& k) {
-            constexpr int CH = D / 8;  // 16-byte chunks of a row
-            for (int i = tid; i < k.nrows * CH; i += 128) {
-                const int rr = i / CH, ch = i % CH;
-                const int R = k.r0 + rr, tok = k.tok0 + R / p.G, gh = k.head * p.G + R % p.G;
-                ft::cp_async16(smQ + (ch >> 3) * (ATTN_BM * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
-                               p.q + (long long)tok * p.ld_q + gh * D + ch * 8);
-            }
-        };
         auto publish_q = [&]() {
             ft::cp_async_wait_all();
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -286,55 +335,70 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
         };
         int g = 0, it0 = 0, n = 0;
         bool ok = true;
-        AttnWork k = p.works[w0];
-        load_q(k);
         publish_q();
         for (int w = w0; w < w1 && ok && !__any_sync(0xffffffffu, s_fail); ++w, ++n) {
+            const AttnWork k = work(w);
             const bool rows_here = wid * 32 < k.nrows;
             const int tok = (k.r0 + min(r, k.nrows - 1)) / p.G;
             const int lim = min(k.kend, k.vis0 == ATTN_NOMASK ? k.kend : k.vis0 + tok);  // this row sees positions < lim
             float m = -INFINITY, l = 0.f;
-            AttnWork knext = k;
             for (int i = 0; i < k.ntile; ++i, ++g) {
-                if (!wait(&s_full[g & 1], g >> 1)) {
+                if (!wait(&s_full[g % NS], g / NS)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
                 const int pos = k.pos0 + i * ATTN_BN;
-                const bool last = i == k.ntile - 1;
-                if (last && w + 1 < w1) {  // every product with this Q is done
-                    knext = p.works[w + 1];
-                    load_q(knext);
-                }
-                if (rows_here) {
-                    const uint32_t sa = lane_base + (uint32_t)(D + (g & 1) * ATTN_BN);
-                    uint32_t s[64];
-                    tc::tmem_ld32(sa, s);
-                    tc::tmem_ld32(sa + 32, s + 32);
+                if (i == k.ntile - 1 && w + 1 < w1) load_q(work(w + 1));  // every product with this Q is done
+                const int valid = k.kend - pos;
+                const bool two = valid > 64;  // keys in the upper half
+                const uint32_t sa = lane_base + (uint32_t)(D + (g % NS) * ATTN_BN);
+                uint32_t s[64];
+                float* f = reinterpret_cast<float*>(s);
+                auto half = [&](int h) {  // scores of 64 keys, masked
+                    tc::tmem_ld32(sa + 64 * h, s);
+                    tc::tmem_ld32(sa + 64 * h + 32, s + 32);
                     tc::tmem_wait_ld(s);
                     tc::tmem_wait_ld(s + 32);
-                    float* f = reinterpret_cast<float*>(s);
-                    if (pos + ATTN_BN > lim) {
+                    const int left = lim - (pos + 64 * h);
+                    if (left < 64) {
 #pragma unroll
                         for (int j = 0; j < 64; ++j)
-                            if (pos + j >= lim) f[j] = -INFINITY;
+                            if (j >= left) f[j] = -INFINITY;
                     }
-                    float mx = f[0];
+                };
+                float mc = 0.f;
+                if (rows_here) {
+                    float mx[8];  // eight chains
 #pragma unroll
-                    for (int j = 1; j < 64; ++j) mx = fmaxf(mx, f[j]);
-                    const float mn = fmaxf(m, mx);
+                    for (int j = 0; j < 8; ++j) mx[j] = m;
+                    auto maxima = [&]() {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) mx[j & 7] = fmaxf(mx[j & 7], f[j]);
+                    };
+                    half(0);
+                    maxima();
+                    if (two) {
+                        half(1);
+                        maxima();
+                    }
+#pragma unroll
+                    for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+                        for (int j = 0; j < o; ++j) mx[j] = fmaxf(mx[j], mx[j + o]);
+                    const float mn = mx[0];
                     if (i == 0) {
                         m = mn;
                     } else {
                         const bool lag = (mn - m) * p.c > RESCALE_LAG;
                         if (__any_sync(0xffffffffu, lag)) {
-                            if (!wait(&pv_done[(g - 1) & 1], (g - 1) >> 1)) ok = false;
+                            // with one S the scores' own barrier has told that the product before them is done
+                            if (NS == 2 && !wait(&pv_done[(g - 1) & 1], (g - 1) >> 1)) ok = false;
                             tc::fence_after_sync();
                             const float fac = lag ? ex2((m - mn) * p.c) : 1.f;
                             l *= fac;
                             if (lag) m = mn;
-#pragma unroll
+#pragma unroll 2
                             for (int cc = 0; cc < D; cc += 32) {
                                 uint32_t o[32];
                                 tc::tmem_ld32(lane_base + (uint32_t)cc, o);
@@ -346,36 +410,47 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                             tmem_wait_st();
                         }
                     }
-                    const float mc = m == -INFINITY ? 0.f : m * p.c;  // a row that has seen no key yet
-                    float l4[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int j = 0; j < 64; j += 2) {
-                        const float a = ex2(fmaf(f[j], p.c, -mc)), b = ex2(fmaf(f[j + 1], p.c, -mc));
-                        l4[(j >> 1) & 3] += a + b;
-                        // the weights go to the product in the cache's own type; l keeps their fp32 values
-                        pk[j >> 1] = pack2<BF>(a, b);
-                    }
-                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-                    tmem_st32(sa, pk);
-                    tmem_wait_st();
+                    mc = m == -INFINITY ? 0.f : m * p.c;  // a row that has seen no key yet
                 }
-                const int valid = k.kend - pos;
                 if (valid < ATTN_BN) {
                     // what the pool holds past the keys may be anything: its weights are 0, its values are made 0
-                    const int vit = it0 + min(i + 2, k.ntile) + i, st = vit % NST;
+                    const int vit = it0 + (NS == 1 ? 2 * i + 1 : min(i + 2, k.ntile) + i), st = vit % NST;
                     if (!wait(&kv_full[st], vit / NST)) ok = false;
-                    unsigned char* vt = ring + (size_t)st * C::STAGE;
-                    const int z0 = max(valid, 0), nz = (ATTN_BN - z0) * 8;
+                    unsigned char* vt = ring + (size_t)st * C::TILE;
+                    const int z0 = max(valid, 0), nz = ((two ? ATTN_BN : 64) - z0) * 8;
                     for (int x = tid; x < nz * (D / 64); x += 128) {
                         const int b = x / nz, y = x % nz;
                         *reinterpret_cast<uint4*>(vt + b * (ATTN_BN * 128) + z0 * 128 + y * 16) = make_uint4(0, 0, 0, 0);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) ft::mbar_arrive(&p_full[g & 1]);
+                const uint64_t c2 = f2(p.c, p.c), mc2 = f2(-mc, -mc);
+                uint64_t l4[4] = {0, 0, 0, 0};  // pairs of sums
+                // the upper half is still in registers; the lower one is read again
+#pragma unroll
+                for (int h = 1; h >= 0; --h) {
+                    if (h == 1 && !two) continue;
+                    if (rows_here) {
+                        if (h == 0 && two) half(0);
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int j = 0; j < 64; j += 2) {
+                            float2 e = unf2(fma2(f2(f[j], f[j + 1]), c2, mc2));
+                            e.x = ex2(e.x);
+                            e.y = ex2(e.y);
+                            l4[(j >> 1) & 3] = add2(l4[(j >> 1) & 3], f2(e.x, e.y));
+                            // the weights go to the product in the cache's own type; l keeps their fp32 values
+                            pk[j >> 1] = pack2<BF>(e.x, e.y);
+                        }
+                        tmem_st32(sa + 64 * h, pk);
+                        tmem_wait_st();
+                    }
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) ft::mbar_arrive(&p_full[g % NS][h]);
+                }
+                const float2 ls = unf2(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])));
+                l += ls.x + ls.y;
             }
             if (!ok) break;
             if (w + 1 < w1) publish_q();
@@ -390,21 +465,22 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                 if (k.prow < 0) {
                     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no key seen: zeros; NaN stays
                     uint16_t* dst = p.out + (long long)(k.tok0 + R / p.G) * p.ld_o + (k.head * p.G + R % p.G) * D;
+                    const bool wide = (uintptr_t)dst % 32 == 0;
 #pragma unroll
                     for (int cc = 0; cc < D; cc += 32) {
-                        uint32_t o[32];
+                        uint32_t o[32], v[16];
                         tc::tmem_ld32(lane_base + (uint32_t)cc, o);
                         tc::tmem_wait_ld(o);
-                        if (in) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                uint4 v;
-                                v.x = pack2<BF>(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
-                                v.y = pack2<BF>(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
-                                v.z = pack2<BF>(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv);
-                                v.w = pack2<BF>(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv);
-                                *reinterpret_cast<uint4*>(dst + cc + j) = v;
-                            }
+                        for (int j = 0; j < 16; ++j)
+                            v[j] = pack2<BF>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                        if (in && wide) {
+                            st_global32(dst + cc, v);
+                            st_global32(dst + cc + 16, v + 8);
+                        } else if (in) {
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4)
+                                *reinterpret_cast<uint4*>(dst + cc + 2 * j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                         }
                     }
                 } else {
@@ -416,8 +492,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                         tc::tmem_wait_ld(o);
                         if (in) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                *reinterpret_cast<uint4*>(dst + cc + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                            for (int j = 0; j < 32; j += 8) st_global32(dst + cc + j, o + j);
                         }
                     }
                     if (in) p.part_ml[k.prow + r] = make_float2(m * p.c, l);
@@ -427,7 +502,6 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
             __syncwarp();
             if (lane == 0) ft::mbar_arrive(&o_empty);
             it0 += 2 * k.ntile;
-            k = knext;
         }
         if (!ok) s_fail = 1;
         ft::cp_async_wait_all();
@@ -440,72 +514,115 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     }
 }
 
-// Joins the pieces of the rows that have more than one: a warp per row, D/32
-// columns a lane.  The order of the pieces is fixed by the plan.
+// Joins the pieces of the rows that have more than one, D/32 columns a lane.
+// The order of the pieces is fixed by the plan, so is the order of the sums.
+// With fewer records than CTAs a record's rows are spread over several CTAs,
+// and where a CTA has fewer rows than warps the warps of a row share its
+// pieces: a row of a long sequence has one piece per CTA that worked on it.
 template <int D, bool BF>
 __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnHdr* hdr, const AttnMerge* __restrict__ merges,
                                                          const float* __restrict__ part_o,
                                                          const float2* __restrict__ part_ml, long long c_row, int G,
                                                          uint16_t* out, long long ld_o) {
     constexpr int V = D / 32;
+    constexpr int NB = D == 256 ? 4 : 8;  // pieces in flight per warp
+    __shared__ float s_acc[8][D];
+    __shared__ float2 s_md[8];
     ft::grid_dep_wait();
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int n = hdr->n_merge;
-    for (int u = blockIdx.x; u < n; u += gridDim.x) {
+    if (n == 0) return;
+    const int C = max(1, (int)gridDim.x / n);  // CTAs of a record
+    for (int u = blockIdx.x / C; u < n; u += C > 1 ? n : (int)gridDim.x) {
         const AttnMerge k = merges[u];
-        for (int r = wid; r < k.nrows; r += 8) {
+        const int na = k.ptok0 >= 0 ? k.pnch : 0, np = na + 1 + k.nc;
+        const int rpc = (k.nrows + C - 1) / C;             // rows of this CTA
+        const int rbeg = C > 1 ? (int)(blockIdx.x % C) * rpc : 0, rend = min(k.nrows, rbeg + rpc);
+        int wpr = 1;                                       // warps of a row
+        while (wpr < 8 && wpr * 2 * rpc <= 8 && wpr * 2 <= np) wpr *= 2;
+        const int share = wid % wpr;
+        for (int r0 = rbeg; r0 < rend; r0 += 8 / wpr) {    // the same trips for every warp
+            const int r = r0 + wid / wpr;
+            const bool on = r < rend;
             const int R = k.r0 + r, tok = k.tok0 + R / G, gh = R % G;
-            long long abase = 0;
-            if (k.ptok0 >= 0) {
-                const int PR = (tok - k.ptok0) * G + gh;
-                abase = (long long)(k.pitem + PR / ATTN_BM) * ATTN_BM + PR % ATTN_BM;
-            }
-            const int na = k.ptok0 >= 0 ? k.pnch : 0, np = na + 1 + k.nc;
-            auto prow = [&](int i) -> long long {
-                if (i < na) return abase + (long long)i * k.pnrt * ATTN_BM;
-                if (i == na) return k.brow + r;
-                return c_row + (long long)(k.c0 + i - na - 1) * ATTN_BM + R % ATTN_BM;
-            };
-            float M = -INFINITY;
-            for (int i = lane; i < np; i += 32) M = fmaxf(M, part_ml[prow(i)].x);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            if (M == -INFINITY) M = 0.f;
-            float den = 0.f, acc[V];
+            float M = -INFINITY, den = 0.f, acc[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) acc[j] = 0.f;
-            for (int b = 0; b < np; b += 32) {
-                float wgt = 0.f;
-                long long pr = 0;
-                if (b + lane < np) {
-                    pr = prow(b + lane);
-                    const float2 ml = part_ml[pr];
-                    wgt = ex2(ml.x - M);
-                    den += wgt * ml.y;
+            if (on) {
+                long long abase = 0;
+                if (na) {
+                    const int PR = (tok - k.ptok0) * G + gh;
+                    abase = (long long)(k.pitem + PR / ATTN_BM) * ATTN_BM + PR % ATTN_BM;
                 }
-                const int e = min(32, np - b);
-#pragma unroll 4
-                for (int i = 0; i < e; ++i) {
-                    const float wi = __shfl_sync(0xffffffffu, wgt, i);
-                    const long long ri = __shfl_sync(0xffffffffu, pr, i);
-                    const float* src = part_o + ri * D + lane * V;
-                    if (V == 2) {
-                        const float2 x = *reinterpret_cast<const float2*>(src);
-                        acc[0] += wi * x.x;
-                        acc[1] += wi * x.y;
-                    } else {
+                // this warp's pieces are share, share + wpr, ...; 32 of them at a time, one a lane
+                for (int b = share; b < np; b += 32 * wpr) {
+                    const int i = b + lane * wpr;
+                    const long long pr = i < na    ? abase + (long long)i * k.pnrt * ATTN_BM
+                                         : i == na ? (long long)k.brow + r
+                                                   : c_row + (long long)(k.c0 + i - na - 1) * ATTN_BM + R % ATTN_BM;
+                    float2 ml = make_float2(-INFINITY, 0.f);
+                    if (i < np) ml = part_ml[pr];
+                    const int e = min(32, (np - b + wpr - 1) / wpr);
+                    float mb = 0.f, wgt = 0.f;
+                    for (int i0 = 0; i0 < e; i0 += NB) {
+                        float x[NB][V];
 #pragma unroll
-                        for (int j = 0; j < V; j += 4) {
-                            const float4 x = *reinterpret_cast<const float4*>(src + j);
-                            acc[j % V] += wi * x.x;
-                            acc[(j + 1) % V] += wi * x.y;
-                            acc[(j + 2) % V] += wi * x.z;
-                            acc[(j + 3) % V] += wi * x.w;
+                        for (int q = 0; q < NB; ++q) {
+                            const long long ri = __shfl_sync(0xffffffffu, pr, (i0 + q) & 31);
+                            if (i0 + q < e) {
+                                const float* src = part_o + ri * D + lane * V;
+                                if (V == 2) {
+                                    *reinterpret_cast<float2*>(x[q]) = *reinterpret_cast<const float2*>(src);
+                                } else {
+#pragma unroll
+                                    for (int j = 0; j + 3 < V; j += 4)
+                                        *reinterpret_cast<float4*>(x[q] + j) = *reinterpret_cast<const float4*>(src + j);
+                                }
+                            }
+                        }
+                        if (i0 == 0) {  // the statistics arrive while the first values are on their way
+                            mb = ml.x;
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+                            const float Mn = fmaxf(M, mb), ref = Mn == -INFINITY ? 0.f : Mn;
+                            const float f = ex2(M - ref);
+                            wgt = ex2(ml.x - ref);
+                            den = den * f + wgt * ml.y;
+#pragma unroll
+                            for (int j = 0; j < V; ++j) acc[j] *= f;
+                            M = Mn;
+                        }
+#pragma unroll
+                        for (int q = 0; q < NB; ++q) {
+                            const float wi = __shfl_sync(0xffffffffu, wgt, (i0 + q) & 31);
+                            if (i0 + q < e) {
+#pragma unroll
+                                for (int j = 0; j < V; ++j) acc[j] += wi * x[q][j];
+                            }
                         }
                     }
                 }
+                den = ft::warp_sum(den);
             }
-            den = ft::warp_sum(den);
+            if (wpr > 1) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) s_acc[wid][lane * V + j] = acc[j];
+                if (lane == 0) s_md[wid] = make_float2(M, den);
+                __syncthreads();
+                if (on && share == 0) {
+                    for (int q = 1; q < wpr; ++q) {
+                        const float2 md = s_md[wid + q];
+                        const float Mn = fmaxf(M, md.x), ref = Mn == -INFINITY ? 0.f : Mn;
+                        const float f = ex2(M - ref), h = ex2(md.x - ref);
+                        den = den * f + md.y * h;
+#pragma unroll
+                        for (int j = 0; j < V; ++j) acc[j] = acc[j] * f + s_acc[wid + q][lane * V + j] * h;
+                        M = Mn;
+                    }
+                }
+                __syncthreads();
+            }
+            if (!on || share) continue;
             const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
             uint16_t* dst = out + (long long)tok * ld_o + (k.head * G + gh) * D + lane * V;
             uint32_t o[V / 2];
@@ -820,16 +937,16 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
             const long long b0 = begin_of(l) + OV;
             c0 = cta_of(b0);
             c1 = cta_of(b0 + r.ntile - 1);
-            if (c0 != c1 || s_pre[r.b] >= 0) cnt = cdiv(r.nrows, MROWS);
+            cnt = c0 != c1 || s_pre[r.b] >= 0;
         }
         int total;
         const int at = n_merge + scan_excl(cnt, ws, total);
-        for (int j = 0; j < cnt; ++j) {
+        if (cnt) {
             AttnMerge m;
             m.head = l / n_seg;
             m.tok0 = p.cu_q[r.b];
-            m.r0 = r.r0 + j * MROWS;
-            m.nrows = min(MROWS, r.nrows - j * MROWS);
+            m.r0 = r.r0;
+            m.nrows = r.nrows;
             m.brow = (int)(p.pl.b_row + (long long)m.head * p.T * G + (long long)m.tok0 * G + m.r0);
             m.c0 = c0 + 1;
             m.nc = c1 - c0;
@@ -843,7 +960,7 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
                 m.pnch = cdiv(cdiv(g_min[gg], ATTN_BN), c);
                 m.pitem = m.head * iph + q_off[q];
             }
-            p.pl.merges[at + j] = m;
+            p.pl.merges[at] = m;
         }
         n_merge += total;
     }
@@ -876,7 +993,7 @@ void attn_plan_sizes(int Hq, int Hkv, int D, int T_max, int B_max, int num_sms, 
     p.cap_segs = rts + B_max;                          // a request's last tile may be short
     p.cap_items = 4 * p.n_cta + Hkv * (rts + B_max);   // four rounds, or a chunk for each row tile
     p.cap_works = p.cap_items + Hkv * p.cap_segs + p.n_cta;
-    p.cap_merges = Hkv * p.cap_segs * (ATTN_BM / MROWS);
+    p.cap_merges = Hkv * p.cap_segs;
     p.b_row = (long long)p.cap_items * ATTN_BM;
     p.c_row = p.b_row + (long long)T_max * Hq;
     p.part_rows = p.c_row + (long long)p.n_cta * ATTN_BM;
@@ -885,7 +1002,7 @@ void attn_plan_sizes(int Hq, int Hkv, int D, int T_max, int B_max, int num_sms, 
 size_t attn_seg_bytes(const AttnPlan& p) { return (size_t)p.cap_segs * sizeof(SegRec); }
 
 // The pool as [n_pages*L*2*Hkv][page][D], read in boxes of 64 values by a
-// page's rows (at most 64) with 128-byte swizzle.
+// page's rows with 128-byte swizzle.
 bool attn_encode_map(ft_kv* kv) {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -894,7 +1011,7 @@ bool attn_encode_map(ft_kv* kv) {
         return false;
     const cuuint64_t dims[3] = {(cuuint64_t)kv->D, (cuuint64_t)kv->page, (cuuint64_t)kv->n_pages * kv->L * 2 * kv->Hkv};
     const cuuint64_t strides[2] = {(cuuint64_t)kv->D * 2, (cuuint64_t)kv->D * 2 * kv->page};
-    const cuuint32_t box[3] = {64, (cuuint32_t)(kv->page < ATTN_BN ? kv->page : ATTN_BN), 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)kv->page, 1};
     const cuuint32_t es[3] = {1, 1, 1};
     return reinterpret_cast<EncodeTiledFn>(f)(
                &kv->map, kv->dtype == FT_KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,

@@ -31,7 +31,7 @@ struct KvCopy {
 // a CTA got.
 
 constexpr int ATTN_BM = 128;        // rows of a work item (TMEM lanes)
-constexpr int ATTN_BN = 64;         // keys of a tile
+constexpr int ATTN_BN = 128;        // keys of a tile
 constexpr int ATTN_MAX_B = 1024;    // requests of a plan (one thread each)
 constexpr int ATTN_NOMASK = 1 << 30;
 
@@ -39,7 +39,7 @@ struct AttnWork {
     int head;     // key/value head
     int trow;     // table row whose pages hold the keys
     int pos0;     // position of the first key of the first tile
-    int ntile;    // 64-key tiles
+    int ntile;    // tiles of 128 keys
     int kend;     // keys at positions >= kend are not there
     int vis0;     // token i of the owner sees positions < vis0 + i
     int tok0;     // first query token of the owner
