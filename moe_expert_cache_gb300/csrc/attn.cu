@@ -27,9 +27,12 @@
 
 namespace {
 
-constexpr int G_THREADS = 192;
+constexpr int G_THREADS = 256;        // 4 softmax warps, a TMA warp, an MMA warp, two idle ones
+// with two CTAs an SM: 128 registers a thread at launch; 128 x 184 + 128 x 72 = 256 x 128
+constexpr int REGS_SOFTMAX = 184, REGS_OTHER = 72;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_LAG = 8.f;   // log2 units
+constexpr int MERGE_NB(int D) { return D == 256 ? 4 : 8; }  // pieces that a warp of the join has in flight
 constexpr int NWORK = 16;            // work items of a CTA that are kept in shared memory
 constexpr int OV = 2;                // cost of an item's start, in tiles
 constexpr int OVP = 4;               // the same with the partial result of a prefix item
@@ -41,19 +44,22 @@ struct Cfg {
     static constexpr int NS = D == 256 ? 2 : 1;
     static constexpr uint32_t TILE = ATTN_BN * D * 2;
     static constexpr uint32_t QBYTES = ATTN_BM * D * 2;
-    static constexpr int NST = D == 64 ? 6 : 2;              // K and V tiles in the ring
+    static constexpr int NST = D == 64 ? 5 : 2;              // K and V tiles in the ring
     static constexpr size_t SMEM = QBYTES + (size_t)NST * TILE;
 };
 
 struct AttnArgs {
+    const AttnHdr* hdr;
     const AttnWork* works;
-    const int* woff;
+    const AttnCta* ctas;
+    const AttnMerge* merges;
+    long long c_row;
     const uint16_t* q;
     long long ld_q;
     uint16_t* out;
     long long ld_o;
     const int* table;
-    int row_pages, page, n_pages, L, Hkv, G, layer;
+    int row_pages, page, page_log, n_pages, L, Hkv, G, layer;
     float c;        // scale * log2(e)
     float* part_o;
     float2* part_ml;
@@ -143,6 +149,124 @@ __device__ __forceinline__ void st_global32(void* d, const uint32_t* v) {
                  : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Joins the pieces of the rows that have more than one: a CTA per record, D/32
+// columns a lane.  The order of the pieces is fixed by the plan, so is the
+// order of the sums.  Rows with many pieces (a long sequence has one per CTA
+// that worked on it) have several warps, which share the pieces.
+template <int D, bool BF>
+__global__ void __launch_bounds__(256, 3) attn_merge_kernel(const AttnArgs p) {
+    constexpr int V = D / 32, NB = MERGE_NB(D);
+    __shared__ float s_acc[8 * D];
+    __shared__ float2 s_md[8];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    ft::grid_dep_launch();
+    ft::grid_dep_wait();
+    const int n = p.hdr->n_merge;
+    for (int u = blockIdx.x; u < n; u += gridDim.x) {
+        const AttnMerge k = p.merges[u];
+        const int na = k.ptok0 >= 0 ? k.pnch : 0, np = na + 1 + k.nc, wpr = k.wpr;
+        const int share = wid % wpr, r = wid / wpr;  // a record has at most 8 / wpr rows
+        const bool on = r < k.nrows;
+        const int R = k.r0 + r, tok = k.tok0 + R / p.G, gh = R % p.G;
+        float M = -INFINITY, den = 0.f, acc[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = 0.f;
+        if (on) {
+            long long abase = 0;
+            if (na) {
+                const int PR = (tok - k.ptok0) * p.G + gh;
+                abase = (long long)(k.pitem + PR / ATTN_BM) * ATTN_BM + PR % ATTN_BM;
+            }
+            // this warp's pieces are share, share + wpr, ...; 32 of them at a time, one a lane
+            for (int b = share; b < np; b += 32 * wpr) {
+                const int i = b + lane * wpr;
+                const long long pr = i < na    ? abase + (long long)i * k.pnrt * ATTN_BM
+                                     : i == na ? (long long)k.brow + r
+                                               : p.c_row + (long long)(k.c0 + i - na - 1) * ATTN_BM + R % ATTN_BM;
+                float2 ml = make_float2(-INFINITY, 0.f);
+                if (i < np) ml = __ldcg(p.part_ml + pr);
+                const int e = min(32, (np - b + wpr - 1) / wpr);
+                float wgt = 0.f;
+                for (int i0 = 0; i0 < e; i0 += NB) {
+                    float x[NB][V];
+#pragma unroll
+                    for (int q = 0; q < NB; ++q) {
+                        const long long ri = __shfl_sync(0xffffffffu, pr, (i0 + q) & 31);
+                        if (i0 + q < e) {
+                            const float* src = p.part_o + ri * D + lane * V;
+                            if (V == 2) {
+                                *reinterpret_cast<float2*>(x[q]) = __ldcg(reinterpret_cast<const float2*>(src));
+                            } else {
+#pragma unroll
+                                for (int j = 0; j + 3 < V; j += 4)
+                                    *reinterpret_cast<float4*>(x[q] + j) = __ldcg(reinterpret_cast<const float4*>(src + j));
+                            }
+                        }
+                    }
+                    if (i0 == 0) {  // the statistics arrive while the first values are on their way
+                        float mb = ml.x;
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+                        const float Mn = fmaxf(M, mb), ref = Mn == -INFINITY ? 0.f : Mn;
+                        const float f = ex2(M - ref);
+                        wgt = ex2(ml.x - ref);
+                        den = den * f + wgt * ml.y;
+#pragma unroll
+                        for (int j = 0; j < V; ++j) acc[j] *= f;
+                        M = Mn;
+                    }
+#pragma unroll
+                    for (int q = 0; q < NB; ++q) {
+                        const float wi = __shfl_sync(0xffffffffu, wgt, (i0 + q) & 31);
+                        if (i0 + q < e) {
+#pragma unroll
+                            for (int j = 0; j < V; ++j) acc[j] += wi * x[q][j];
+                        }
+                    }
+                }
+            }
+            den = ft::warp_sum(den);
+        }
+        if (wpr > 1) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) s_acc[wid * D + lane * V + j] = acc[j];
+            if (lane == 0) s_md[wid] = make_float2(M, den);
+            __syncthreads();
+            if (on && share == 0) {
+                for (int q = 1; q < wpr; ++q) {
+                    const float2 md = s_md[wid + q];
+                    const float Mn = fmaxf(M, md.x), ref = Mn == -INFINITY ? 0.f : Mn;
+                    const float f = ex2(M - ref), h = ex2(md.x - ref);
+                    den = den * f + md.y * h;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) acc[j] = acc[j] * f + s_acc[(wid + q) * D + lane * V + j] * h;
+                    M = Mn;
+                }
+            }
+            __syncthreads();
+        }
+        if (on && share == 0) {
+            const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
+            uint16_t* dst = p.out + (long long)tok * p.ld_o + (k.head * p.G + gh) * D + lane * V;
+            uint32_t o[V / 2];
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) o[j] = pack2<BF>(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+            if (V == 2)
+                *reinterpret_cast<uint32_t*>(dst) = o[0];
+            else if (V == 4)
+                *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1 % (V / 2)]);
+            else
+                *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1 % (V / 2)], o[2 % (V / 2)], o[3 % (V / 2)]);
+        }
+    }
+}
+
 template <int D, bool BF>
 __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __grid_constant__ CUtensorMap map,
                                                                        const AttnArgs p) {
@@ -157,7 +281,9 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
 
     ft::grid_dep_launch();
-    const int w0 = p.woff[blockIdx.x], w1 = p.woff[blockIdx.x + 1];
+    ft::grid_dep_wait();
+    const AttnCta mine0 = p.ctas[blockIdx.x];
+    const int w0 = mine0.w0, w1 = mine0.w1;
     if (w0 == w1) return;
     auto load_q = [&](const AttnWork& k) {
         constexpr int CH = D / 8;  // 16-byte chunks of a row
@@ -168,7 +294,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                            p.q + (long long)tok * p.ld_q + gh * D + ch * 8);
         }
     };
-    if (wid < 4) load_q(p.works[w0]);
+    if (wid < 4) load_q(mine0.first);
     for (int i = tid; i < min(w1 - w0, NWORK) * (int)(sizeof(AttnWork) / 4); i += G_THREADS)
         reinterpret_cast<int*>(s_work)[i] = reinterpret_cast<const int*>(p.works + w0)[i];
     if (tid == 128) {
@@ -197,7 +323,9 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     const uint32_t tmem = s_tmem;
     auto work = [&](int w) -> AttnWork { return w - w0 < NWORK ? s_work[w - w0] : p.works[w]; };
 
-    if (wid == 4) {
+    if (wid >= 4) {
+        if (C::CTAS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+        if (wid == 4) {
         // ------------------------------------------------------------ TMA warp
         // order of the ring: K0, V0, K1, V1, ... with one S, K0, K1, V0, K2, V1, ... with two
         constexpr int NB = D / 64;                           // boxes across a row
@@ -205,21 +333,25 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
         const int sub = lane / NB, blk = lane % NB;
         const bool mine = lane < boxes;
         const int oob = p.n_pages * p.L * 2 * p.Hkv;         // a box past the map's end reads zeros
-        int it = 0;
+        // the page of this lane's box of a tile is read two tiles ahead, across items, and looked at only when the
+        // box is issued
+        constexpr int NONE = 0x7fffffff;                     // no key of the item there: reads zeros
+        int it = 0, rw = w0, ri = 0;
         bool ok = true;
+        AttnWork kr = work(w0);
+        auto read = [&]() {
+            if (rw >= w1) return NONE;
+            const int pos = kr.pos0 + ri * ATTN_BN + sub * p.page;
+            const int id = !mine || pos >= kr.kend ? NONE : p.table[(size_t)kr.trow * p.row_pages + (pos >> p.page_log)];
+            if (++ri == kr.ntile) {
+                ri = 0;
+                if (++rw < w1) kr = work(rw);
+            }
+            return id;
+        };
+        int prev = NONE, cur = read(), next = read();
         for (int w = w0; w < w1 && ok && !__any_sync(0xffffffffu, s_fail); ++w) {
-            const AttnWork k = work(w);
-            const int* row = p.table + (size_t)k.trow * p.row_pages;
-            auto page_of = [&](int i) {  // page of this lane's box of tile i, or -1 past the keys
-                const int pos = k.pos0 + i * ATTN_BN + sub * p.page;
-                if (!mine || i >= k.ntile || pos >= k.kend) return -1;
-                const int id = row[pos / p.page];
-                if (id < 0 || id >= p.n_pages) {
-                    atomicOr(p.err, FT_DEVERR_ARG);
-                    return -1;
-                }
-                return id;
-            };
+            const int nt = work(w).ntile, head = work(w).head;
             auto issue = [&](int id, int kv) {
                 const int st = it % NST;
                 if (it >= NST && !ft::mbar_wait(&kv_empty[st], ((it / NST) - 1) & 1, p.err)) ok = false;
@@ -228,23 +360,29 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                 if (lane == 0) ft::mbar_arrive_expect_tx(&kv_full[st], C::TILE);
                 __syncwarp();
                 if (mine) {
-                    const int z = id < 0 ? oob : ((id * p.L + p.layer) * 2 + kv) * p.Hkv + k.head;
+                    int z = oob;
+                    if ((unsigned)id < (unsigned)p.n_pages)
+                        z = ((id * p.L + p.layer) * 2 + kv) * p.Hkv + head;
+                    else if (id != NONE)
+                        atomicOr(p.err, FT_DEVERR_ARG);
                     unsigned char* dst = ring + (size_t)st * C::TILE + blk * (ATTN_BN * 128) + sub * p.page * 128;
                     tc::tma_load_3d(dst, &map, blk * 64, 0, z, &kv_full[st]);
                 }
                 ++it;
             };
-            int prev = -1, cur = page_of(0);
-            for (int i = 0; i <= k.ntile && ok; ++i) {
-                const int next = page_of(i + 1);
-                if (i < k.ntile) issue(cur, 0);
+            for (int i = 0; i < nt && ok; ++i) {
+                const int next2 = read();
                 if (NS == 1) {
-                    if (ok && i < k.ntile) issue(cur, 1);
-                } else {
+                    issue(cur, 0);
+                    if (ok) issue(cur, 1);
+                } else {  // K of the tile, then V of the one before
+                    issue(cur, 0);
                     if (ok && i > 0) issue(prev, 1);
+                    if (ok && i == nt - 1) issue(cur, 1);
                 }
                 prev = cur;
                 cur = next;
+                next = next2;
             }
         }
         if (!ok) s_fail = 1;
@@ -295,7 +433,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                     const bool two = k.kend - (k.pos0 + i * ATTN_BN) > 64;
                     uint32_t acc = i ? 1u : 0u;
 #pragma unroll
-                    for (int h = 1; h >= 0; --h) {  // the upper 64 keys first: their weights are ready first
+                    for (int h = 0; h < 2; ++h) {
                         if (h == 1 && !two) continue;
                         const int b = 2 * (g % NS) + h;
                         if (!wait(&p_full[g % NS][h], (ph >> b) & 1)) break;
@@ -319,7 +457,9 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
             tc::mma_commit(&done);
             ft::mbar_wait(&done, 0, p.err);
         }
+        }
     } else {
+        if (C::CTAS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         // ------------------------------------------------------- softmax warps
         const int r = tid;  // row of the item: TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)(wid * 32) << 16);
@@ -353,44 +493,28 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                 const int valid = k.kend - pos;
                 const bool two = valid > 64;  // keys in the upper half
                 const uint32_t sa = lane_base + (uint32_t)(D + (g % NS) * ATTN_BN);
-                uint32_t s[64];
+                uint32_t s[ATTN_BN];
                 float* f = reinterpret_cast<float*>(s);
-                auto half = [&](int h) {  // scores of 64 keys, masked
-                    tc::tmem_ld32(sa + 64 * h, s);
-                    tc::tmem_ld32(sa + 64 * h + 32, s + 32);
-                    tc::tmem_wait_ld(s);
-                    tc::tmem_wait_ld(s + 32);
-                    const int left = lim - (pos + 64 * h);
-                    if (left < 64) {
-#pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            if (j >= left) f[j] = -INFINITY;
-                    }
-                };
                 float mc = 0.f;
                 if (rows_here) {
-                    float mx[8];  // eight chains
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) mx[j] = m;
-                    auto maxima = [&]() {
+                    for (int j = 0; j < ATTN_BN; j += 32) tc::tmem_ld32(sa + j, s + j);
 #pragma unroll
-                        for (int j = 0; j < 64; ++j) mx[j & 7] = fmaxf(mx[j & 7], f[j]);
-                    };
-                    half(0);
-                    maxima();
-                    if (two) {
-                        half(1);
-                        maxima();
+                    for (int j = 0; j < ATTN_BN; j += 32) tc::tmem_wait_ld(s + j);
+                    const int left = lim - pos;
+                    if (left < ATTN_BN) {
+#pragma unroll
+                        for (int j = 0; j < ATTN_BN; ++j)
+                            if (j >= left) f[j] = -INFINITY;
                     }
+                    float mx[4] = {m, m, m, m};  // four chains
 #pragma unroll
-                    for (int o = 4; o > 0; o >>= 1)
-#pragma unroll
-                        for (int j = 0; j < o; ++j) mx[j] = fmaxf(mx[j], mx[j + o]);
-                    const float mn = mx[0];
+                    for (int j = 0; j < ATTN_BN; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], f[j], f[j + 1]);
+                    const float mn = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
                     if (i == 0) {
                         m = mn;
                     } else {
-                        const bool lag = (mn - m) * p.c > RESCALE_LAG;
+                        const bool lag = r < k.nrows && (mn - m) * p.c > RESCALE_LAG;  // lanes past the rows hold anything
                         if (__any_sync(0xffffffffu, lag)) {
                             // with one S the scores' own barrier has told that the product before them is done
                             if (NS == 2 && !wait(&pv_done[(g - 1) & 1], (g - 1) >> 1)) ok = false;
@@ -398,7 +522,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                             const float fac = lag ? ex2((m - mn) * p.c) : 1.f;
                             l *= fac;
                             if (lag) m = mn;
-#pragma unroll 2
+#pragma unroll 1
                             for (int cc = 0; cc < D; cc += 32) {
                                 uint32_t o[32];
                                 tc::tmem_ld32(lane_base + (uint32_t)cc, o);
@@ -426,16 +550,14 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                 }
                 const uint64_t c2 = f2(p.c, p.c), mc2 = f2(-mc, -mc);
                 uint64_t l4[4] = {0, 0, 0, 0};  // pairs of sums
-                // the upper half is still in registers; the lower one is read again
 #pragma unroll
-                for (int h = 1; h >= 0; --h) {
+                for (int h = 0; h < 2; ++h) {
                     if (h == 1 && !two) continue;
                     if (rows_here) {
-                        if (h == 0 && two) half(0);
                         uint32_t pk[32];
 #pragma unroll
                         for (int j = 0; j < 64; j += 2) {
-                            float2 e = unf2(fma2(f2(f[j], f[j + 1]), c2, mc2));
+                            float2 e = unf2(fma2(f2(f[64 * h + j], f[64 * h + j + 1]), c2, mc2));
                             e.x = ex2(e.x);
                             e.y = ex2(e.y);
                             l4[(j >> 1) & 3] = add2(l4[(j >> 1) & 3], f2(e.x, e.y));
@@ -514,137 +636,15 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     }
 }
 
-// Joins the pieces of the rows that have more than one, D/32 columns a lane.
-// The order of the pieces is fixed by the plan, so is the order of the sums.
-// With fewer records than CTAs a record's rows are spread over several CTAs,
-// and where a CTA has fewer rows than warps the warps of a row share its
-// pieces: a row of a long sequence has one piece per CTA that worked on it.
-template <int D, bool BF>
-__global__ void __launch_bounds__(256) attn_merge_kernel(const AttnHdr* hdr, const AttnMerge* __restrict__ merges,
-                                                         const float* __restrict__ part_o,
-                                                         const float2* __restrict__ part_ml, long long c_row, int G,
-                                                         uint16_t* out, long long ld_o) {
-    constexpr int V = D / 32;
-    constexpr int NB = D == 256 ? 4 : 8;  // pieces in flight per warp
-    __shared__ float s_acc[8][D];
-    __shared__ float2 s_md[8];
-    ft::grid_dep_wait();
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int n = hdr->n_merge;
-    if (n == 0) return;
-    const int C = max(1, (int)gridDim.x / n);  // CTAs of a record
-    for (int u = blockIdx.x / C; u < n; u += C > 1 ? n : (int)gridDim.x) {
-        const AttnMerge k = merges[u];
-        const int na = k.ptok0 >= 0 ? k.pnch : 0, np = na + 1 + k.nc;
-        const int rpc = (k.nrows + C - 1) / C;             // rows of this CTA
-        const int rbeg = C > 1 ? (int)(blockIdx.x % C) * rpc : 0, rend = min(k.nrows, rbeg + rpc);
-        int wpr = 1;                                       // warps of a row
-        while (wpr < 8 && wpr * 2 * rpc <= 8 && wpr * 2 <= np) wpr *= 2;
-        const int share = wid % wpr;
-        for (int r0 = rbeg; r0 < rend; r0 += 8 / wpr) {    // the same trips for every warp
-            const int r = r0 + wid / wpr;
-            const bool on = r < rend;
-            const int R = k.r0 + r, tok = k.tok0 + R / G, gh = R % G;
-            float M = -INFINITY, den = 0.f, acc[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) acc[j] = 0.f;
-            if (on) {
-                long long abase = 0;
-                if (na) {
-                    const int PR = (tok - k.ptok0) * G + gh;
-                    abase = (long long)(k.pitem + PR / ATTN_BM) * ATTN_BM + PR % ATTN_BM;
-                }
-                // this warp's pieces are share, share + wpr, ...; 32 of them at a time, one a lane
-                for (int b = share; b < np; b += 32 * wpr) {
-                    const int i = b + lane * wpr;
-                    const long long pr = i < na    ? abase + (long long)i * k.pnrt * ATTN_BM
-                                         : i == na ? (long long)k.brow + r
-                                                   : c_row + (long long)(k.c0 + i - na - 1) * ATTN_BM + R % ATTN_BM;
-                    float2 ml = make_float2(-INFINITY, 0.f);
-                    if (i < np) ml = part_ml[pr];
-                    const int e = min(32, (np - b + wpr - 1) / wpr);
-                    float mb = 0.f, wgt = 0.f;
-                    for (int i0 = 0; i0 < e; i0 += NB) {
-                        float x[NB][V];
-#pragma unroll
-                        for (int q = 0; q < NB; ++q) {
-                            const long long ri = __shfl_sync(0xffffffffu, pr, (i0 + q) & 31);
-                            if (i0 + q < e) {
-                                const float* src = part_o + ri * D + lane * V;
-                                if (V == 2) {
-                                    *reinterpret_cast<float2*>(x[q]) = *reinterpret_cast<const float2*>(src);
-                                } else {
-#pragma unroll
-                                    for (int j = 0; j + 3 < V; j += 4)
-                                        *reinterpret_cast<float4*>(x[q] + j) = *reinterpret_cast<const float4*>(src + j);
-                                }
-                            }
-                        }
-                        if (i0 == 0) {  // the statistics arrive while the first values are on their way
-                            mb = ml.x;
-#pragma unroll
-                            for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-                            const float Mn = fmaxf(M, mb), ref = Mn == -INFINITY ? 0.f : Mn;
-                            const float f = ex2(M - ref);
-                            wgt = ex2(ml.x - ref);
-                            den = den * f + wgt * ml.y;
-#pragma unroll
-                            for (int j = 0; j < V; ++j) acc[j] *= f;
-                            M = Mn;
-                        }
-#pragma unroll
-                        for (int q = 0; q < NB; ++q) {
-                            const float wi = __shfl_sync(0xffffffffu, wgt, (i0 + q) & 31);
-                            if (i0 + q < e) {
-#pragma unroll
-                                for (int j = 0; j < V; ++j) acc[j] += wi * x[q][j];
-                            }
-                        }
-                    }
-                }
-                den = ft::warp_sum(den);
-            }
-            if (wpr > 1) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) s_acc[wid][lane * V + j] = acc[j];
-                if (lane == 0) s_md[wid] = make_float2(M, den);
-                __syncthreads();
-                if (on && share == 0) {
-                    for (int q = 1; q < wpr; ++q) {
-                        const float2 md = s_md[wid + q];
-                        const float Mn = fmaxf(M, md.x), ref = Mn == -INFINITY ? 0.f : Mn;
-                        const float f = ex2(M - ref), h = ex2(md.x - ref);
-                        den = den * f + md.y * h;
-#pragma unroll
-                        for (int j = 0; j < V; ++j) acc[j] = acc[j] * f + s_acc[wid + q][lane * V + j] * h;
-                        M = Mn;
-                    }
-                }
-                __syncthreads();
-            }
-            if (!on || share) continue;
-            const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
-            uint16_t* dst = out + (long long)tok * ld_o + (k.head * G + gh) * D + lane * V;
-            uint32_t o[V / 2];
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) o[j] = pack2<BF>(acc[2 * j] * inv, acc[2 * j + 1] * inv);
-            if (V == 2)
-                *reinterpret_cast<uint32_t*>(dst) = o[0];
-            else if (V == 4)
-                *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1 % (V / 2)]);
-            else
-                *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1 % (V / 2)], o[2 % (V / 2)], o[3 % (V / 2)]);
-        }
-    }
-}
-
 // ------------------------------------------------------------------ the plan
 
 constexpr int PT = ATTN_MAX_B;  // threads: one per request
 
+constexpr int CUM = 2048;       // segments whose running cost is kept in shared memory
+
 struct PlanArgs {
     AttnPlan pl;
-    int B, T, n_groups, G, Hkv, page, n_rows, row_pages;
+    int B, T, n_groups, G, Hkv, page, n_rows, row_pages, merge_nb;
     const int *cu_q, *rows, *group_start, *group_tokens, *lens;
     unsigned* err;
 };
@@ -699,6 +699,9 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
     __shared__ int q_g[PT / 2], q_off[PT / 2];  // per group taken together (it has two requests at least)
     __shared__ int ws[33];
     __shared__ int s_c, s_iph;
+    extern __shared__ int s_cum[];  // [CUM]
+    ft::grid_dep_launch();
+    ft::grid_dep_wait();
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int B = p.B, G = p.G, n_cta = p.pl.n_cta;
     SegRec* seg = reinterpret_cast<SegRec*>(p.pl.seg);
@@ -723,9 +726,9 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
     if (!__syncthreads_and(ok)) {
         if (tid == 0) {
             atomicOr(p.err, FT_DEVERR_ARG);
-            *p.pl.hdr = AttnHdr{0, 0, 0, 0};
+            *p.pl.hdr = AttnHdr{0, 0};
         }
-        for (int i = tid; i <= n_cta; i += PT) p.pl.woff[i] = 0;
+        for (int i = tid; i < n_cta; i += PT) p.pl.ctas[i].w0 = p.pl.ctas[i].w1 = 0;
         return;
     }
     g_min[tid] = 0x7fffffff;
@@ -786,7 +789,10 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         }
         int total;
         r.cum = cost + scan_excl(s < n_seg ? r.ntile + OV : 0, ws, total);
-        if (s < n_seg) seg[s] = r;
+        if (s < n_seg) {
+            seg[s] = r;
+            if (s < CUM) s_cum[s] = r.cum;
+        }
         cost += total;
     }
     const long long S = (long long)cost * p.Hkv;
@@ -807,8 +813,9 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
                     x += cdiv(g_rows[q_g[i]], ATTN_BM) * cdiv(cdiv(g_min[q_g[i]], ATTN_BN), c);
                 return (int)__reduce_add_sync(0xffffffffu, x) * p.Hkv;
             };
-            for (int rounds = 1; rounds <= 4; ++rounds) {
-                const int cap = max(rounds * n_cta, rts * p.Hkv);
+            // a half or a quarter of the CTAs, the rest left to the other work, or up to four rounds over all
+            for (int rounds = 1; rounds <= 16; rounds *= 2) {
+                const int cap = max(rounds * n_cta / 4, rts * p.Hkv);
                 int lo = 1, hi = mt;  // smallest c with items(c) <= cap
                 while (lo < hi) {
                     const int mid = (lo + hi) >> 1;
@@ -852,11 +859,12 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
     if (q0 < 1) q0 = 1;
     auto start_of = [&](int i) { return min(S, i < n1 ? i * q1 : n1 * q1 + (i - n1) * q0); };
     auto cta_of = [&](long long x) { return x < n1 * q1 ? (int)(x / q1) : n1 + (int)((x - n1 * q1) / q0); };
+    auto cum_of = [&](int i) { return i < CUM ? s_cum[i] : seg[i].cum; };
     auto linear = [&](long long x) {  // head * n_seg + segment that holds cost position x
         const int h = (int)(x / cost);
-        return h * n_seg + upper(n_seg, x - (long long)h * cost, [&](int i) { return seg[i].cum; });
+        return h * n_seg + upper(n_seg, x - (long long)h * cost, [&](int i) { return cum_of(i); });
     };
-    auto begin_of = [&](int l) { return (long long)(l / n_seg) * cost + seg[l % n_seg].cum; };
+    auto begin_of = [&](int l) { return (long long)(l / n_seg) * cost + cum_of(l % n_seg); };
     __syncthreads();  // seg is complete
 
     int n_works = 0;
@@ -874,14 +882,20 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         }
         int total;
         const int at = n_works + scan_excl(cnt, ws, total);
-        if (i < n_cta) p.pl.woff[i] = at;
+        if (i < n_cta) {
+            p.pl.ctas[i].w0 = at;
+            p.pl.ctas[i].w1 = at + cnt;
+        }
         n_works += total;
     }
-    if (tid == 0) p.pl.woff[n_cta] = n_works;
     __syncthreads();
     // a warp per CTA writes its items
     for (int i = wid; i < n_cta; i += PT / 32) {
-        const int w0 = p.pl.woff[i], k = k0 + (i < n1 ? 1 : 0);
+        const int w0 = p.pl.ctas[i].w0, k = k0 + (i < n1 ? 1 : 0);
+        auto put = [&](int j, const AttnWork& w) {
+            p.pl.works[w0 + j] = w;
+            if (j == 0) p.pl.ctas[i].first = w;
+        };
         for (int j = lane; j < k; j += 32) {
             const int idx = j * n_cta + i, h = idx / iph, rem = idx % iph;
             const int q = upper(n_pre, rem, [&](int a) { return q_off[a]; });
@@ -899,7 +913,7 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
             w.r0 = rt * ATTN_BM;
             w.nrows = min(ATTN_BM, g_rows[gg] - w.r0);
             w.prow = idx * ATTN_BM;
-            p.pl.works[w0 + j] = w;
+            put(j, w);
         }
         const long long x0 = start_of(i), x1 = start_of(i + 1);
         if (x1 <= x0) continue;
@@ -923,7 +937,7 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
             w.prow = whole && s_pre[r.b] < 0 ? -1
                      : t0 == 0 ? (int)(p.pl.b_row + (long long)w.head * p.T * G + (long long)w.tok0 * G + r.r0)
                                : (int)(p.pl.c_row + (long long)i * ATTN_BM);
-            p.pl.works[w0 + k + (l - l0)] = w;
+            put(k + (l - l0), w);
         }
     }
     // ---- rows with more than one piece
@@ -932,39 +946,46 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         const int l = base + tid;
         int cnt = 0, c0 = 0, c1 = 0;
         SegRec r{};
+        AttnMerge m{};
         if (l < n_seg * p.Hkv) {
             r = seg[l % n_seg];
             const long long b0 = begin_of(l) + OV;
             c0 = cta_of(b0);
             c1 = cta_of(b0 + r.ntile - 1);
-            cnt = c0 != c1 || s_pre[r.b] >= 0;
+            const int q = s_pre[r.b];
+            if (c0 != c1 || q >= 0) {
+                m.head = l / n_seg;
+                m.tok0 = p.cu_q[r.b];
+                m.brow = (int)(p.pl.b_row + (long long)m.head * p.T * G + (long long)m.tok0 * G + r.r0);
+                m.c0 = c0 + 1;
+                m.nc = c1 - c0;
+                m.ptok0 = -1;
+                m.pitem = m.pnrt = m.pnch = 0;
+                if (q >= 0) {
+                    const int gg = q_g[q];
+                    m.ptok0 = p.cu_q[p.group_start[gg]];
+                    m.pnrt = cdiv(g_rows[gg], ATTN_BM);
+                    m.pnch = cdiv(cdiv(g_min[gg], ATTN_BN), c);
+                    m.pitem = m.head * iph + q_off[q];
+                }
+                // as many warps as bring a warp's loads down to one round, at most eight
+                const int np = m.pnch + 1 + m.nc;
+                m.wpr = np > 4 * p.merge_nb ? 8 : np > 2 * p.merge_nb ? 4 : np > p.merge_nb ? 2 : 1;
+                cnt = cdiv(r.nrows, 8 / m.wpr);
+            }
         }
         int total;
         const int at = n_merge + scan_excl(cnt, ws, total);
-        if (cnt) {
-            AttnMerge m;
-            m.head = l / n_seg;
-            m.tok0 = p.cu_q[r.b];
-            m.r0 = r.r0;
-            m.nrows = r.nrows;
-            m.brow = (int)(p.pl.b_row + (long long)m.head * p.T * G + (long long)m.tok0 * G + m.r0);
-            m.c0 = c0 + 1;
-            m.nc = c1 - c0;
-            m.ptok0 = -1;
-            m.pitem = m.pnrt = m.pnch = 0;
-            const int q = s_pre[r.b];
-            if (q >= 0) {
-                const int gg = q_g[q];
-                m.ptok0 = p.cu_q[p.group_start[gg]];
-                m.pnrt = cdiv(g_rows[gg], ATTN_BM);
-                m.pnch = cdiv(cdiv(g_min[gg], ATTN_BN), c);
-                m.pitem = m.head * iph + q_off[q];
-            }
-            p.pl.merges[at] = m;
+        const int step = cnt ? 8 / m.wpr : 0, brow = m.brow;
+        for (int j = 0; j < cnt; ++j) {
+            m.r0 = r.r0 + j * step;
+            m.nrows = min(step, r.nrows - j * step);
+            m.brow = brow + j * step;
+            p.pl.merges[at + j] = m;
         }
         n_merge += total;
     }
-    if (tid == 0) *p.pl.hdr = AttnHdr{n_merge, 0, n_works, 0};
+    if (tid == 0) *p.pl.hdr = AttnHdr{n_merge, n_works};
 }
 
 // -------------------------------------------------------------- host side
@@ -977,11 +998,10 @@ template <int D, bool BF>
 cudaError_t launch_typed(ft_kv* kv, const AttnArgs& a, const AttnPlan& pl) {
     cudaError_t e = ensure_dynamic_smem((const void*)attn_kernel<D, BF>, Cfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    attn_kernel<D, BF><<<pl.n_cta, G_THREADS, Cfg<D>::SMEM, kv->stream>>>(kv->map, a);
-    e = cudaGetLastError();
+    void* args[] = {const_cast<CUtensorMap*>(&kv->map), const_cast<AttnArgs*>(&a)};
+    e = launch_dependent((const void*)attn_kernel<D, BF>, pl.n_cta, G_THREADS, Cfg<D>::SMEM, kv->stream, args);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attn_merge_kernel<D, BF>, dim3(kv->num_sms * 4), dim3(256), 0, kv->stream, pl.hdr, pl.merges,
-                            kv->part_o, kv->part_ml, pl.c_row, a.G, a.out, a.ld_o);
+    return launch_dependent((const void*)attn_merge_kernel<D, BF>, kv->num_sms * 4, 256, 0, kv->stream, args + 1);
 }
 
 }  // namespace
@@ -993,7 +1013,7 @@ void attn_plan_sizes(int Hq, int Hkv, int D, int T_max, int B_max, int num_sms, 
     p.cap_segs = rts + B_max;                          // a request's last tile may be short
     p.cap_items = 4 * p.n_cta + Hkv * (rts + B_max);   // four rounds, or a chunk for each row tile
     p.cap_works = p.cap_items + Hkv * p.cap_segs + p.n_cta;
-    p.cap_merges = Hkv * p.cap_segs;
+    p.cap_merges = (int)((long long)T_max * Hq) + Hkv * p.cap_segs;  // a row each, or a short last record of a segment
     p.b_row = (long long)p.cap_items * ATTN_BM;
     p.c_row = p.b_row + (long long)T_max * Hq;
     p.part_rows = p.c_row + (long long)p.n_cta * ATTN_BM;
@@ -1022,22 +1042,27 @@ bool attn_encode_map(ft_kv* kv) {
 cudaError_t launch_attn_plan(ft_kv* kv, int B, int T, const int* cu_q, const int* rows, int n_groups,
                              const int* group_start, const int* group_tokens) {
     PlanArgs a{kv->plan, B, T, n_groups, kv->Hq / kv->Hkv, kv->Hkv, kv->page, kv->n_rows, kv->row_pages,
-               cu_q, rows, group_start, group_tokens, kv->lens, kv->err};
-    attn_plan_kernel<<<1, PT, 0, kv->stream>>>(a);
-    return cudaGetLastError();
+               MERGE_NB(kv->D), cu_q, rows, group_start, group_tokens, kv->lens, kv->err};
+    const cudaError_t e = ensure_dynamic_smem((const void*)attn_plan_kernel, CUM * 4);
+    if (e != cudaSuccess) return e;
+    void* args[] = {&a};
+    return launch_dependent((const void*)attn_plan_kernel, 1, PT, CUM * 4, kv->stream, args);
 }
 
 cudaError_t launch_attn_forward(ft_kv* kv, int layer, const void* q, long long ld_q, void* out, long long ld_o,
                                 float scale) {
     AttnArgs a{};
     a.works = kv->plan.works;
-    a.woff = kv->plan.woff;
+    a.hdr = kv->plan.hdr;
+    a.ctas = kv->plan.ctas;
+    a.merges = kv->plan.merges;
+    a.c_row = kv->plan.c_row;
     a.q = static_cast<const uint16_t*>(q);
     a.ld_q = ld_q;
     a.out = static_cast<uint16_t*>(out);
     a.ld_o = ld_o;
     a.table = kv->table;
-    a.row_pages = kv->row_pages; a.page = kv->page; a.n_pages = kv->n_pages; a.L = kv->L; a.Hkv = kv->Hkv;
+    a.row_pages = kv->row_pages; a.page = kv->page; a.page_log = __builtin_ctz(kv->page); a.n_pages = kv->n_pages; a.L = kv->L; a.Hkv = kv->Hkv;
     a.G = kv->Hq / kv->Hkv;
     a.layer = layer;
     a.c = scale * LOG2E;

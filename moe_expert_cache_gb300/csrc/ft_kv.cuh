@@ -48,28 +48,33 @@ struct AttnWork {
     int prow;     // first row of the partial result, or -1: write the output
 };
 
+// What a CTA finds first: its items and a copy of the first of them.
+struct AttnCta {
+    int w0, w1;
+    AttnWork first;
+};
+
+// Rows to join, at most 8 / wpr of them.
 struct AttnMerge {
     int head, tok0, r0, nrows;  // as in AttnWork
-    int brow;                   // partial row of the piece that starts the segment
+    int brow;                   // partial row of the first row's piece that starts its segment
     int c0, nc;                 // CTAs c0 .. c0+nc-1 hold further pieces
     int ptok0;                  // first token of the group whose shared prefix these rows ran over, or -1
     int pitem, pnrt, pnch;      // its first item of this head, row tiles and chunks
+    int wpr;                    // warps of a row: 1, 2, 4 or 8
 };
 
 struct AttnHdr {
     int n_merge;
-    int merge_rows;
     int n_works;
-    int pad;
 };
 
 struct AttnPlan {
     AttnHdr* hdr;
-    int* woff;          // [n_cta + 1] first work item of each CTA
+    AttnCta* ctas;      // [n_cta]
     AttnWork* works;    // [cap_works]
     AttnMerge* merges;  // [cap_merges]
-    // scratch of the plan kernel
-    int* seg;           // [cap_segs * SEG_WORDS]
+    int* seg;           // scratch of the plan kernel
     int n_cta;
     int cap_segs, cap_works, cap_merges;
     int cap_items;      // prefix items (region A of the partials)
@@ -130,14 +135,13 @@ cudaError_t launch_attn_plan(ft_kv* kv, int B, int T, const int* cu_q, const int
 cudaError_t launch_attn_forward(ft_kv* kv, int layer, const void* q, long long ld_q, void* out, long long ld_o,
                                 float scale);
 
-// Launch on s as a programmatic dependent of the kernel before it: the kernel
-// may start while that one drains and waits for its end by grid_dep_wait().
-template <typename... KArgs, typename... Args>
-inline cudaError_t launch_dependent(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                                    Args... args) {
+// Launch on s as a programmatic dependent of the kernel before it: the CTAs may
+// start while that one drains, set themselves up, and wait for its end (and its
+// writes) by grid_dep_wait() before they touch any global memory.
+inline cudaError_t launch_dependent(const void* k, int grid, int block, size_t smem, cudaStream_t s, void** args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -145,7 +149,7 @@ inline cudaError_t launch_dependent(void (*k)(KArgs...), dim3 grid, dim3 block, 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, KArgs(args)...);
+    return cudaLaunchKernelExC(&cfg, k, args);
 }
 
 namespace ft {

@@ -5,6 +5,8 @@
 #include "ft_kv.cuh"
 
 #include <cmath>
+#include <cstdio>
+#include <cstdlib>
 #include <new>
 
 namespace {
@@ -19,7 +21,7 @@ size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Offsets of the arrays in the scratch allocation.
 struct Layout {
-    size_t err, info, n_copy, copies, free_list, remap, mark, rank, hdr, woff, works, merges, seg, part_o, part_ml,
+    size_t err, info, n_copy, copies, free_list, remap, mark, rank, hdr, ctas, works, merges, seg, part_o, part_ml,
         total;
 };
 
@@ -40,7 +42,7 @@ Layout layout(const AttnPlan& p, int D, int n_pages, int n_rows) {
     l.mark = carve((size_t)n_rows * 4);
     l.rank = carve((size_t)n_rows * 4);
     l.hdr = carve(sizeof(AttnHdr));
-    l.woff = carve((size_t)(p.n_cta + 1) * 4);
+    l.ctas = carve((size_t)p.n_cta * sizeof(AttnCta));
     l.works = carve((size_t)p.cap_works * sizeof(AttnWork));
     l.merges = carve((size_t)p.cap_merges * sizeof(AttnMerge));
     l.seg = carve(attn_seg_bytes(p));
@@ -50,7 +52,11 @@ Layout layout(const AttnPlan& p, int D, int n_pages, int n_rows) {
     return l;
 }
 
-ft_status launched(cudaError_t e) { return e == cudaSuccess ? FT_OK : FT_ERR_CUDA; }
+ft_status launched(cudaError_t e) {
+    if (e == cudaSuccess) return FT_OK;
+    if (getenv("FT_DEBUG")) fprintf(stderr, "libft: launch -> %s\n", cudaGetErrorString(e));
+    return FT_ERR_CUDA;
+}
 
 bool misaligned(const void* p, size_t a) { return (uintptr_t)p % a != 0; }
 
@@ -124,7 +130,7 @@ ft_status ft_kv_init(ft_kv** out, int32_t L, int32_t Hq, int32_t Hkv, int32_t D,
     kv->mark = (int*)(a + l.mark);
     kv->rank = (int*)(a + l.rank);
     kv->plan.hdr = (AttnHdr*)(a + l.hdr);
-    kv->plan.woff = (int*)(a + l.woff);
+    kv->plan.ctas = (AttnCta*)(a + l.ctas);
     kv->plan.works = (AttnWork*)(a + l.works);
     kv->plan.merges = (AttnMerge*)(a + l.merges);
     kv->plan.seg = (int*)(a + l.seg);

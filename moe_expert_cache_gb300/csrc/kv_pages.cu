@@ -112,6 +112,8 @@ __device__ void refuse(const KvCtl& c, unsigned bit) {
 
 __global__ void __launch_bounds__(CT) kv_extend_kernel(KvCtl c, int n, const int* __restrict__ rows,
                                                        const int* __restrict__ add) {
+    ft::grid_dep_launch();
+    ft::grid_dep_wait();
     __shared__ int ws[33];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     if (!rows_ok(c, n, rows)) return refuse(c, FT_DEVERR_ARG);
@@ -150,6 +152,8 @@ __global__ void __launch_bounds__(CT) kv_extend_kernel(KvCtl c, int n, const int
 
 __global__ void __launch_bounds__(CT) kv_fork_kernel(KvCtl c, int n, const int* __restrict__ parents,
                                                      const int* __restrict__ children) {
+    ft::grid_dep_launch();
+    ft::grid_dep_wait();
     __shared__ int ws[33];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     if (!rows_ok(c, n, children, parents)) return refuse(c, FT_DEVERR_ARG);
@@ -204,6 +208,8 @@ __global__ void __launch_bounds__(CT) kv_fork_kernel(KvCtl c, int n, const int* 
 }
 
 __global__ void __launch_bounds__(CT) kv_free_kernel(KvCtl c, int n, const int* __restrict__ rows) {
+    ft::grid_dep_launch();
+    ft::grid_dep_wait();
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     bool ok = rows_ok(c, n, rows);
     if (!ok) return refuse(c, FT_DEVERR_ARG);
@@ -241,6 +247,8 @@ __global__ void __launch_bounds__(CT) kv_free_kernel(KvCtl c, int n, const int* 
 // k-th free page below it (there are equally many).  The two lists fill the
 // copy list's ends independently, so both scans are one pass over refs.
 __global__ void __launch_bounds__(CT) kv_compact_kernel(KvCtl c) {
+    ft::grid_dep_launch();
+    ft::grid_dep_wait();
     __shared__ int ws[33];
     int live = 0;
     for (int p = threadIdx.x; p < c.n_pages; p += CT) live += c.refs[p] > 0;
@@ -277,6 +285,7 @@ __global__ void __launch_bounds__(256) kv_copy_kernel(const int* n_copy, const K
                                                       int banks, int bank_bytes, int tok_bytes, int* table,
                                                       long long entries, const int* __restrict__ remap,
                                                       const int* live, int n_pages) {
+    ft::grid_dep_launch();
     ft::grid_dep_wait();
     const int lane = threadIdx.x & 31;
     const long long wid = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -312,33 +321,38 @@ __global__ void __launch_bounds__(256) kv_copy_kernel(const int* n_copy, const K
 }
 
 cudaError_t launch_copy(ft_kv* kv, bool compact) {
-    const int banks = kv->L * 2 * kv->Hkv, bank_bytes = kv->page * kv->D * 2;
-    const long long entries = compact ? (long long)kv->n_rows * kv->row_pages : 0;
-    return launch_dependent(kv_copy_kernel, dim3(kv->num_sms * 8), dim3(256), 0, kv->stream, kv->n_copy, kv->copies,
-                            kv->pool, banks, bank_bytes, kv->D * 2, kv->table, entries, kv->remap,
-                            compact ? kv->info + KV_LIVE : nullptr, kv->n_pages);
+    int banks = kv->L * 2 * kv->Hkv, bank_bytes = kv->page * kv->D * 2, tok_bytes = kv->D * 2;
+    long long entries = compact ? (long long)kv->n_rows * kv->row_pages : 0;
+    const int* live = compact ? kv->info + KV_LIVE : nullptr;
+    void* args[] = {&kv->n_copy, &kv->copies, &kv->pool, &banks, &bank_bytes, &tok_bytes,
+                    &kv->table, &entries, &kv->remap, &live, &kv->n_pages};
+    return launch_dependent((const void*)kv_copy_kernel, kv->num_sms * 8, 256, 0, kv->stream, args);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_extend(ft_kv* kv, int n, const int* rows, const int* add) {
-    kv_extend_kernel<<<1, CT, 0, kv->stream>>>(ctl_of(kv), n, rows, add);
-    return cudaGetLastError();
+    KvCtl c = ctl_of(kv);
+    void* args[] = {&c, &n, &rows, &add};
+    return launch_dependent((const void*)kv_extend_kernel, 1, CT, 0, kv->stream, args);
 }
 
 cudaError_t launch_kv_fork(ft_kv* kv, int n, const int* parents, const int* children) {
-    kv_fork_kernel<<<1, CT, 0, kv->stream>>>(ctl_of(kv), n, parents, children);
-    const cudaError_t e = cudaGetLastError();
+    KvCtl c = ctl_of(kv);
+    void* args[] = {&c, &n, &parents, &children};
+    const cudaError_t e = launch_dependent((const void*)kv_fork_kernel, 1, CT, 0, kv->stream, args);
     return e == cudaSuccess ? launch_copy(kv, false) : e;
 }
 
 cudaError_t launch_kv_free(ft_kv* kv, int n, const int* rows) {
-    kv_free_kernel<<<1, CT, 0, kv->stream>>>(ctl_of(kv), n, rows);
-    return cudaGetLastError();
+    KvCtl c = ctl_of(kv);
+    void* args[] = {&c, &n, &rows};
+    return launch_dependent((const void*)kv_free_kernel, 1, CT, 0, kv->stream, args);
 }
 
 cudaError_t launch_kv_compact(ft_kv* kv) {
-    kv_compact_kernel<<<1, CT, 0, kv->stream>>>(ctl_of(kv));
-    const cudaError_t e = cudaGetLastError();
+    KvCtl c = ctl_of(kv);
+    void* args[] = {&c};
+    const cudaError_t e = launch_dependent((const void*)kv_compact_kernel, 1, CT, 0, kv->stream, args);
     return e == cudaSuccess ? launch_copy(kv, true) : e;
 }

@@ -62,12 +62,16 @@ constexpr int U = 4;  // heads whose loads a lane has in flight
 
 template <int D, bool BF>
 __global__ void __launch_bounds__(256) qk_rope_store_kernel(const RopeParams p) {
+    ft::grid_dep_launch();
     constexpr int GL = D / 16;      // lanes of a head
     constexpr int HPW = 32 / GL;    // heads of a warp step
     const int lane = threadIdx.x & 31, j = lane % GL, sub = lane / GL;
     const long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int t = (int)(w / p.parts), part = (int)(w % p.parts);
-    if (t >= p.a.T) return;
+    if (t >= p.a.T) {
+        ft::grid_dep_wait();
+        return;
+    }
     const int rot = p.a.rot, half = rot / 2;
     // offsets of this lane's two vectors within a head
     const bool turns = 16 * j < rot;
@@ -77,6 +81,7 @@ __global__ void __launch_bounds__(256) qk_rope_store_kernel(const RopeParams p) 
     const uint16_t* x = static_cast<const uint16_t*>(p.a.qkv) + (long long)t * p.a.ld;
     const int step0 = part * p.spw, step1 = min(step0 + p.spw, p.steps);
 
+    ft::grid_dep_wait();
     uint4 va[U], vb[U];
     auto load = [&](int s0) {
 #pragma unroll
@@ -189,15 +194,6 @@ __global__ void __launch_bounds__(256) qk_rope_store_kernel(const RopeParams p) 
     }
 }
 
-template <int D>
-cudaError_t launch_d(const RopeParams& p, bool bf, int grid, cudaStream_t s) {
-    if (bf)
-        qk_rope_store_kernel<D, true><<<grid, 256, 0, s>>>(p);
-    else
-        qk_rope_store_kernel<D, false><<<grid, 256, 0, s>>>(p);
-    return cudaGetLastError();
-}
-
 }  // namespace
 
 cudaError_t launch_qk_rope_store(ft_kv* kv, const RopeArgs& a) {
@@ -217,7 +213,9 @@ cudaError_t launch_qk_rope_store(ft_kv* kv, const RopeArgs& a) {
     const long long warps = (long long)a.T * p.parts;
     const int grid = (int)((warps + 7) / 8);
     const bool bf = kv->dtype == FT_KV_BF16;
-    if (kv->D == 64) return launch_d<64>(p, bf, grid, kv->stream);
-    if (kv->D == 128) return launch_d<128>(p, bf, grid, kv->stream);
-    return launch_d<256>(p, bf, grid, kv->stream);
+    const void* k = kv->D == 64    ? (bf ? (const void*)qk_rope_store_kernel<64, true> : (const void*)qk_rope_store_kernel<64, false>)
+                    : kv->D == 128 ? (bf ? (const void*)qk_rope_store_kernel<128, true> : (const void*)qk_rope_store_kernel<128, false>)
+                                   : (bf ? (const void*)qk_rope_store_kernel<256, true> : (const void*)qk_rope_store_kernel<256, false>);
+    void* args[] = {&p};
+    return launch_dependent(k, grid, 256, 0, kv->stream, args);
 }
