@@ -28,8 +28,8 @@
 namespace {
 
 constexpr int G_THREADS = 256;        // 4 softmax warps, a TMA warp, an MMA warp, two idle ones
-// with two CTAs an SM: 128 registers a thread at launch; 128 x 184 + 128 x 72 = 256 x 128
-constexpr int REGS_SOFTMAX = 184, REGS_OTHER = 72;
+// with two CTAs an SM: 128 registers a thread at launch; 128 x 208 + 128 x 48 = 256 x 128
+constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 48;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_LAG = 8.f;   // log2 units
 constexpr int MERGE_NB(int D) { return D == 256 ? 4 : 8; }  // pieces that a warp of the join has in flight
@@ -104,13 +104,16 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Shared-memory descriptor of an operand tile whose 64-element rows lie along
-// M or N (the transposed V): 128-byte swizzled atoms of 64 values by 8 keys,
-// 1024 bytes from one group of 8 keys to the next, `lead` bytes from one block
-// of 64 values to the next.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(const void* tile, uint32_t lead) {
-    const uint64_t start = (ft::smem_addr(tile) >> 4) & 0x3FFFull;
-    return start | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory descriptors, split into the low word (start >> 4, and at bit 16
+// the leading byte offset >> 4) and a constant high word (stride 1024 bytes,
+// version 1, 128-byte swizzle).  K-major (Q, K): rows of 64 values, 8-row groups
+// 1024 bytes apart; the leading offset is not used.  V lies transposed: atoms of
+// 64 values by 8 keys, 1024 bytes from one group of 8 keys to the next, `lead`
+// bytes from one block of 64 values to the next.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(const void* tile) { return (ft::smem_addr(tile) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_v(const void* tile, uint32_t lead) {
+    return (ft::smem_addr(tile) >> 4) | ((lead >> 4) << 16);
 }
 
 // kind::f16 with bf16 (1) or f16 (0) operands, fp32 accumulator; bit 16: B is
@@ -120,14 +123,69 @@ constexpr uint32_t idesc_of(bool bf, int N, bool b_mn) {
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(ATTN_BM >> 4) << 24);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The MMA warp runs converged and elects the issuing thread inside each
+// instruction: its operands then stay in uniform registers.  Beside two busy
+// softmax warps on its scheduler a 128 x 128 x 16 product measured 81 cycles an
+// instruction this way (64 is its own time), 220 issued by one diverged thread,
+// which moves every operand from its own registers.
+
+// D[tmem] (+)= A[smem] * B[smem]^T
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t.reg .b32 t;\n\t"
+        "mov.b64 da, {%1, %5};\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "elect.sync t|q, 0xffffffff;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(DESC_HI)
         : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t.reg .b32 t;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "elect.sync t|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(DESC_HI)
+        : "memory");
+}
+// Arrive once on `bar` when all that the elected thread has issued so far is done.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t.reg .b32 t;\n\t"
+        "elect.sync t|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(ft::smem_addr(bar))
+        : "memory");
+}
+// S = Q K^T of a tile: D / 16 steps; 8 values of 16 bytes a step, 64 a block.
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mma_ss(d, q + b * (128 * 128 / 16) + 2 * i, k + b * (ATTN_BN * 128 / 16) + 2 * i, idesc, (b | i) ? 1u : 0u);
+}
+// O (+)= P V over 64 keys: steps of 16 keys, 8 columns of P and 2048 bytes of V.
+__device__ __forceinline__ void mma_values(uint32_t o, uint32_t pt, uint32_t v, uint32_t idesc, uint32_t accumulate) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mma_ts(o, pt + 8 * i, v + 128 * i, idesc, i ? 1u : accumulate);
+}
+
+// A place in the ring and the parity of its phase.
+struct Slot {
+    int st = 0;
+    uint32_t ph = 0;
+};
+template <int NST>
+__device__ __forceinline__ void advance(Slot& s) {
+    if (++s.st == NST) {
+        s.st = 0;
+        s.ph ^= 1u;
+    }
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
@@ -167,9 +225,11 @@ __global__ void __launch_bounds__(256, 3) attn_merge_kernel(const AttnArgs p) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     ft::grid_dep_launch();
     ft::grid_dep_wait();
+    // the first record is read beside the count (there is room for as many records as CTAs)
+    AttnMerge k = p.merges[blockIdx.x];
     const int n = p.hdr->n_merge;
     for (int u = blockIdx.x; u < n; u += gridDim.x) {
-        const AttnMerge k = p.merges[u];
+        if (u != (int)blockIdx.x) k = p.merges[u];
         const int na = k.ptok0 >= 0 ? k.pnch : 0, np = na + 1 + k.nc, wpr = k.wpr;
         const int share = wid % wpr, r = wid / wpr;  // a record has at most 8 / wpr rows
         const bool on = r < k.nrows;
@@ -273,30 +333,15 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     using C = Cfg<D>;
     constexpr int NST = C::NST, NS = C::NS;
     extern __shared__ __align__(1024) unsigned char smQ[];  // Q, then the ring
-    __shared__ uint64_t kv_full[NST], kv_empty[NST], s_full[NS], p_full[NS][2], pv_done[2], q_full, o_full, o_empty, done;
+    __shared__ uint64_t kv_full[NST], kv_empty[NST], s_full[NS], p_full[NS][2], pv_done[2], q_full, o_full, o_empty, w_full,
+        done;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_fail;
-    __shared__ AttnWork s_work[NWORK];
+    __shared__ __align__(16) AttnWork s_work[NWORK];
     unsigned char* ring = smQ + C::QBYTES;
     const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
 
     ft::grid_dep_launch();
-    ft::grid_dep_wait();
-    const AttnCta mine0 = p.ctas[blockIdx.x];
-    const int w0 = mine0.w0, w1 = mine0.w1;
-    if (w0 == w1) return;
-    auto load_q = [&](const AttnWork& k) {
-        constexpr int CH = D / 8;  // 16-byte chunks of a row
-        for (int i = tid; i < k.nrows * CH; i += 128) {
-            const int rr = i / CH, ch = i % CH;
-            const int R = k.r0 + rr, tok = k.tok0 + R / p.G, gh = k.head * p.G + R % p.G;
-            ft::cp_async16(smQ + (ch >> 3) * (ATTN_BM * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
-                           p.q + (long long)tok * p.ld_q + gh * D + ch * 8);
-        }
-    };
-    if (wid < 4) load_q(mine0.first);
-    for (int i = tid; i < min(w1 - w0, NWORK) * (int)(sizeof(AttnWork) / 4); i += G_THREADS)
-        reinterpret_cast<int*>(s_work)[i] = reinterpret_cast<const int*>(p.works + w0)[i];
     if (tid == 128) {
         for (int s = 0; s < NST; ++s) {
             ft::mbar_init(&kv_full[s], 1);
@@ -311,6 +356,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
         ft::mbar_init(&q_full, 4);
         ft::mbar_init(&o_full, 1);
         ft::mbar_init(&o_empty, 4);
+        ft::mbar_init(&w_full, 1);
         ft::mbar_init(&done, 1);
         ft::mbar_fence_init();
         s_fail = 0;
@@ -321,6 +367,26 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = s_tmem;
+    // up to here nothing touched global memory: it ran beside the end of the kernel before this one
+    ft::grid_dep_wait();
+    const AttnCta mine0 = p.ctas[blockIdx.x];
+    const int w0 = mine0.w0, w1 = mine0.w1;
+    auto load_q = [&](const AttnWork& k) {
+        constexpr int CH = D / 8;  // 16-byte chunks of a row
+        for (int i = tid; i < k.nrows * CH; i += 128) {
+            const int rr = i / CH, ch = i % CH;
+            const int R = k.r0 + rr, tok = k.tok0 + R / p.G, gh = k.head * p.G + R % p.G;
+            ft::cp_async16(smQ + (ch >> 3) * (ATTN_BM * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
+                           p.q + (long long)tok * p.ld_q + gh * D + ch * 8);
+        }
+    };
+    // the first item came with the range for what starts at once (its queries and pages); all arrive by a bulk copy
+    // that the first use waits for
+    const int nw = min(w1 - w0, NWORK);
+    if (tid == 160 && nw > 0) {
+        ft::mbar_arrive_expect_tx(&w_full, nw * (uint32_t)sizeof(AttnWork));
+        ft::bulk_g2s(s_work, p.works + w0, nw * (uint32_t)sizeof(AttnWork), &w_full);
+    }
     auto work = [&](int w) -> AttnWork { return w - w0 < NWORK ? s_work[w - w0] : p.works[w]; };
 
     if (wid >= 4) {
@@ -338,18 +404,21 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
         constexpr int NONE = 0x7fffffff;                     // no key of the item there: reads zeros
         int it = 0, rw = w0, ri = 0;
         bool ok = true;
-        AttnWork kr = work(w0);
+        AttnWork kr = mine0.first;
         auto read = [&]() {
-            if (rw >= w1) return NONE;
-            const int pos = kr.pos0 + ri * ATTN_BN + sub * p.page;
-            const int id = !mine || pos >= kr.kend ? NONE : p.table[(size_t)kr.trow * p.row_pages + (pos >> p.page_log)];
-            if (++ri == kr.ntile) {
+            if (rw < w1 && ri == kr.ntile) {                 // the next item, if there is one
                 ri = 0;
                 if (++rw < w1) kr = work(rw);
             }
-            return id;
+            if (rw >= w1) return NONE;
+            const int pos = kr.pos0 + ri * ATTN_BN + sub * p.page;
+            ++ri;
+            return !mine || pos >= kr.kend ? NONE : p.table[(size_t)kr.trow * p.row_pages + (pos >> p.page_log)];
         };
-        int prev = NONE, cur = read(), next = read();
+        // the first tile's pages need the first item only: they are read while the items are still on their way
+        int prev = NONE, cur = read();
+        if (nw > 0) ok = __all_sync(0xffffffffu, ft::mbar_wait(&w_full, 0, p.err));
+        int next = ok ? read() : NONE;
         for (int w = w0; w < w1 && ok && !__any_sync(0xffffffffu, s_fail); ++w) {
             const int nt = work(w).ntile, head = work(w).head;
             auto issue = [&](int id, int kv) {
@@ -390,71 +459,59 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
             if (j >= 0) ft::mbar_wait(&kv_full[j % NST], (j / NST) & 1, p.err);
     } else if (wid == 5) {
         // ------------------------------------------------------------ MMA warp
-        if (lane == 0) {
+        {
             constexpr uint32_t id_s = idesc_of(BF, ATTN_BN, false), id_o = idesc_of(BF, D, true);
-            int it = 0, g = 0, n = 0;
+            const uint32_t kdesc = desc_k(ring), vdesc = desc_v(ring, ATTN_BN * 128), qdesc = desc_k(smQ);
+            constexpr uint32_t TW = C::TILE / 16;
+            int g = 0, n = 0;
             uint32_t ph = 0;  // phase bits of p_full[b][h], at 2 b + h
+            Slot r;
             bool ok = true;
-            auto wait = [&](uint64_t* b, int ph) {
-                if (ok && !ft::mbar_wait(b, (uint32_t)ph & 1u, p.err)) ok = false;
-                return ok;
+            auto wait = [&](uint64_t* b, uint32_t phase) {
+                if (!__all_sync(0xffffffffu, ft::mbar_wait(b, phase & 1u, p.err))) ok = false;
             };
-            auto scores = [&](int t) {  // S[t % NS] = Q K^T with the next tile of the ring
-                const int st = it % NST;
-                if (!wait(&kv_full[st], it / NST)) return;
+            Slot sc;  // score buffer of the next tile
+            auto scores = [&]() {  // S = Q K^T with the next tile of the ring
+                wait(&kv_full[r.st], r.ph);
                 tc::fence_after_sync();
-                const uint32_t d = tmem + (uint32_t)(D + (t % NS) * ATTN_BN);
-                const unsigned char* kt = ring + (size_t)st * C::TILE;
-#pragma unroll
-                for (int b = 0; b < D / 64; ++b) {
-                    const uint64_t ad = tc::sdesc_k_sw128(smQ + b * (ATTN_BM * 128));
-                    const uint64_t bd = tc::sdesc_k_sw128(kt + b * (ATTN_BN * 128));
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        tc::mma_bf16(d, ad + (uint64_t)(2 * j), bd + (uint64_t)(2 * j), id_s, (b | j) ? 1u : 0u);
-                }
-                tc::mma_commit(&kv_empty[st]);
-                tc::mma_commit(&s_full[t % NS]);
-                ++it;
+                mma_scores<D>(tmem + (uint32_t)(D + sc.st * ATTN_BN), qdesc, kdesc + r.st * TW, id_s);
+                mma_commit(&kv_empty[r.st]);
+                mma_commit(&s_full[sc.st]);
+                advance<NST>(r);
+                advance<NS>(sc);
             };
-            for (int w = w0; w < w1 && ok && !s_fail; ++w, ++n) {
+            int sb = 0;
+            if (nw > 0) wait(&w_full, 0);
+            for (int w = w0; w < w1 && ok && !__any_sync(0xffffffffu, s_fail); ++w, ++n) {
                 const AttnWork k = work(w);
-                const int nt = k.ntile;
-                if (!wait(&q_full, n)) break;
-                tc::fence_after_sync();
-                scores(g);
+                const int nt = k.ntile, keys = k.kend - k.pos0;
+                wait(&q_full, n);
+                scores();
                 for (int i = 0; i < nt && ok; ++i, ++g) {
-                    if (NS == 2 && i + 1 < nt) scores(g + 1);
-                    if (i == 0 && n > 0 && !wait(&o_empty, n - 1)) break;
-                    const int st = it % NST;
-                    if (!wait(&kv_full[st], it / NST)) break;
-                    const uint32_t a = tmem + (uint32_t)(D + (g % NS) * ATTN_BN);
-                    const uint64_t vd = sdesc_mn_sw128(ring + (size_t)st * C::TILE, ATTN_BN * 128);
-                    const bool two = k.kend - (k.pos0 + i * ATTN_BN) > 64;
-                    uint32_t acc = i ? 1u : 0u;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (h == 1 && !two) continue;
-                        const int b = 2 * (g % NS) + h;
-                        if (!wait(&p_full[g % NS][h], (ph >> b) & 1)) break;
-                        ph ^= 1u << b;
+                    if (NS == 2 && i + 1 < nt) scores();
+                    if (i == 0 && n > 0) wait(&o_empty, n - 1);
+                    wait(&kv_full[r.st], r.ph);
+                    const uint32_t pt = tmem + (uint32_t)(D + sb * ATTN_BN), vd = vdesc + r.st * TW;
+                    wait(&p_full[sb][0], ph >> (2 * sb));
+                    ph ^= 1u << (2 * sb);
+                    tc::fence_after_sync();
+                    mma_values(tmem, pt, vd, id_o, i ? 1u : 0u);
+                    if (keys - i * ATTN_BN > 64) {
+                        wait(&p_full[sb][1], ph >> (2 * sb + 1));
+                        ph ^= 2u << (2 * sb);
                         tc::fence_after_sync();
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {  // 16 keys: 8 columns of P, 2048 bytes of V
-                            mma_ts(tmem, a + (uint32_t)(64 * h + 8 * j), vd + (uint64_t)(128 * (4 * h + j)), id_o, acc);
-                            acc = 1u;
-                        }
+                        mma_values(tmem, pt + 64, vd + 512, id_o, 1u);
                     }
-                    if (!ok) break;
-                    tc::mma_commit(&kv_empty[st]);
-                    if (NS == 2) tc::mma_commit(&pv_done[g & 1]);
-                    if (i == nt - 1) tc::mma_commit(&o_full);
-                    ++it;
-                    if (NS == 1 && i + 1 < nt) scores(g + 1);
+                    mma_commit(&kv_empty[r.st]);
+                    if (NS == 2) mma_commit(&pv_done[g & 1]);
+                    if (i == nt - 1) mma_commit(&o_full);
+                    advance<NST>(r);
+                    if (NS == 2) sb ^= 1;
+                    if (NS == 1 && i + 1 < nt) scores();
                 }
             }
             if (!ok) s_fail = 1;
-            tc::mma_commit(&done);
+            mma_commit(&done);
             ft::mbar_wait(&done, 0, p.err);
         }
         }
@@ -475,7 +532,11 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
         };
         int g = 0, it0 = 0, n = 0;
         bool ok = true;
-        publish_q();
+        if (w0 < w1) {
+            load_q(mine0.first);
+            publish_q();
+            ok = wait(&w_full, 0);
+        }
         for (int w = w0; w < w1 && ok && !__any_sync(0xffffffffu, s_fail); ++w, ++n) {
             const AttnWork k = work(w);
             const bool rows_here = wid * 32 < k.nrows;
@@ -495,7 +556,26 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                 const uint32_t sa = lane_base + (uint32_t)(D + (g % NS) * ATTN_BN);
                 uint32_t s[ATTN_BN];
                 float* f = reinterpret_cast<float*>(s);
-                float mc = 0.f;
+                float mc = 0.f, lh = 0.f;
+                uint32_t pk[32];
+                const uint64_t c2 = f2(p.c, p.c);
+                // weights of 64 keys on the reference mc; returns their sum.  The weights go to the product in the
+                // cache's own type; l keeps their fp32 values.
+                auto weights = [&](int h) {
+                    const uint64_t mc2 = f2(-mc, -mc);
+                    uint64_t l4[4] = {0, 0, 0, 0};  // pairs of sums
+#pragma unroll
+                    for (int j = 0; j < 64; j += 2) {
+                        float2 e = unf2(fma2(f2(f[64 * h + j], f[64 * h + j + 1]), c2, mc2));
+                        e.x = ex2(e.x);
+                        e.y = ex2(e.y);
+                        l4[(j >> 1) & 3] = add2(l4[(j >> 1) & 3], f2(e.x, e.y));
+                        pk[j >> 1] = pack2<BF>(e.x, e.y);
+                    }
+                    const float2 ls = unf2(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])));
+                    return ls.x + ls.y;
+                };
+                auto reference = [&]() { mc = m == -INFINITY ? 0.f : m * p.c; };  // -inf: a row that has seen no key yet
                 if (rows_here) {
 #pragma unroll
                     for (int j = 0; j < ATTN_BN; j += 32) tc::tmem_ld32(sa + j, s + j);
@@ -508,11 +588,19 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                             if (j >= left) f[j] = -INFINITY;
                     }
                     float mx[4] = {m, m, m, m};  // four chains
+                    // past the first tile the reference is almost always good enough: the weights are begun on it,
+                    // beside the maxima that tell whether it is
+                    if (i > 0) {
+                        reference();
+                        lh = weights(0);
+                    }
 #pragma unroll
                     for (int j = 0; j < ATTN_BN; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], f[j], f[j + 1]);
                     const float mn = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
                     if (i == 0) {
                         m = mn;
+                        reference();
+                        lh = weights(0);
                     } else {
                         const bool lag = r < k.nrows && (mn - m) * p.c > RESCALE_LAG;  // lanes past the rows hold anything
                         if (__any_sync(0xffffffffu, lag)) {
@@ -532,9 +620,10 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                                 tmem_st32(lane_base + (uint32_t)cc, o);
                             }
                             tmem_wait_st();
+                            reference();
+                            lh = weights(0);
                         }
                     }
-                    mc = m == -INFINITY ? 0.f : m * p.c;  // a row that has seen no key yet
                 }
                 if (valid < ATTN_BN) {
                     // what the pool holds past the keys may be anything: its weights are 0, its values are made 0
@@ -548,31 +637,19 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                const uint64_t c2 = f2(p.c, p.c), mc2 = f2(-mc, -mc);
-                uint64_t l4[4] = {0, 0, 0, 0};  // pairs of sums
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (h == 1 && !two) continue;
                     if (rows_here) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int j = 0; j < 64; j += 2) {
-                            float2 e = unf2(fma2(f2(f[64 * h + j], f[64 * h + j + 1]), c2, mc2));
-                            e.x = ex2(e.x);
-                            e.y = ex2(e.y);
-                            l4[(j >> 1) & 3] = add2(l4[(j >> 1) & 3], f2(e.x, e.y));
-                            // the weights go to the product in the cache's own type; l keeps their fp32 values
-                            pk[j >> 1] = pack2<BF>(e.x, e.y);
-                        }
+                        l += lh;
                         tmem_st32(sa + 64 * h, pk);
                         tmem_wait_st();
                     }
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) ft::mbar_arrive(&p_full[g % NS][h]);
+                    if (h == 0 && two && rows_here) lh = weights(1);
                 }
-                const float2 ls = unf2(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])));
-                l += ls.x + ls.y;
             }
             if (!ok) break;
             if (w + 1 < w1) publish_q();
@@ -1013,7 +1090,8 @@ void attn_plan_sizes(int Hq, int Hkv, int D, int T_max, int B_max, int num_sms, 
     p.cap_segs = rts + B_max;                          // a request's last tile may be short
     p.cap_items = 4 * p.n_cta + Hkv * (rts + B_max);   // four rounds, or a chunk for each row tile
     p.cap_works = p.cap_items + Hkv * p.cap_segs + p.n_cta;
-    p.cap_merges = (int)((long long)T_max * Hq) + Hkv * p.cap_segs;  // a row each, or a short last record of a segment
+    // a row each, a short last record of a segment, and what each CTA of the join reads first
+    p.cap_merges = T_max * Hq + Hkv * p.cap_segs + 4 * num_sms;
     p.b_row = (long long)p.cap_items * ATTN_BM;
     p.c_row = p.b_row + (long long)T_max * Hq;
     p.part_rows = p.c_row + (long long)p.n_cta * ATTN_BM;

@@ -35,7 +35,7 @@ constexpr int ATTN_BN = 128;        // keys of a tile
 constexpr int ATTN_MAX_B = 1024;    // requests of a plan (one thread each)
 constexpr int ATTN_NOMASK = 1 << 30;
 
-struct AttnWork {
+struct __align__(16) AttnWork {
     int head;     // key/value head
     int trow;     // table row whose pages hold the keys
     int pos0;     // position of the first key of the first tile
@@ -46,11 +46,12 @@ struct AttnWork {
     int r0;       // row of the owner that is row 0 here
     int nrows;    // 1..128
     int prow;     // first row of the partial result, or -1: write the output
+    int pad[2];   // 48 bytes: records are fetched by bulk copies of 16-byte multiples
 };
 
 // What a CTA finds first: its items and a copy of the first of them.
-struct AttnCta {
-    int w0, w1;
+struct __align__(16) AttnCta {
+    int w0, w1, pad[2];
     AttnWork first;
 };
 
