@@ -721,7 +721,7 @@ constexpr int CUM = 2048;       // segments whose running cost is kept in shared
 
 struct PlanArgs {
     AttnPlan pl;
-    int B, T, n_groups, G, Hkv, page, n_rows, row_pages, merge_nb;
+    int B, T, n_groups, G, Hkv, page, n_rows, row_pages, merge_nb, merge_warps;
     const int *cu_q, *rows, *group_start, *group_tokens, *lens;
     unsigned* err;
 };
@@ -1018,6 +1018,21 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         }
     }
     // ---- rows with more than one piece
+    auto pieces_of = [&](int l, const SegRec& r, int& c0, int& c1) {  // the CTAs that have some of its tiles
+        const long long b0 = begin_of(l) + OV;
+        c0 = cta_of(b0);
+        c1 = cta_of(b0 + r.ntile - 1);
+        return c0 != c1 || s_pre[r.b] >= 0;
+    };
+    int rows = 0;
+    for (int l = tid; l < n_seg * p.Hkv; l += PT) {
+        const SegRec r = seg[l % n_seg];
+        int c0, c1;
+        if (pieces_of(l, r, c0, c1)) rows += r.nrows;
+    }
+    scan_excl(rows, ws, rows);
+    // several warps share a row's pieces as long as all warps run at once
+    const int warps = max(1, p.merge_warps / max(1, rows));
     int n_merge = 0;
     for (int base = 0; base < n_seg * p.Hkv; base += PT) {
         const int l = base + tid;
@@ -1026,11 +1041,8 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         AttnMerge m{};
         if (l < n_seg * p.Hkv) {
             r = seg[l % n_seg];
-            const long long b0 = begin_of(l) + OV;
-            c0 = cta_of(b0);
-            c1 = cta_of(b0 + r.ntile - 1);
             const int q = s_pre[r.b];
-            if (c0 != c1 || q >= 0) {
+            if (pieces_of(l, r, c0, c1)) {
                 m.head = l / n_seg;
                 m.tok0 = p.cu_q[r.b];
                 m.brow = (int)(p.pl.b_row + (long long)m.head * p.T * G + (long long)m.tok0 * G + r.r0);
@@ -1045,9 +1057,8 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
                     m.pnch = cdiv(cdiv(g_min[gg], ATTN_BN), c);
                     m.pitem = m.head * iph + q_off[q];
                 }
-                // as many warps as bring a warp's loads down to one round, at most eight
-                const int np = m.pnch + 1 + m.nc;
-                m.wpr = np > 4 * p.merge_nb ? 8 : np > 2 * p.merge_nb ? 4 : np > p.merge_nb ? 2 : 1;
+                const int np = m.pnch + 1 + m.nc, most = min(warps, cdiv(np, p.merge_nb));
+                m.wpr = most >= 8 ? 8 : most >= 4 ? 4 : most >= 2 ? 2 : 1;
                 cnt = cdiv(r.nrows, 8 / m.wpr);
             }
         }
@@ -1120,7 +1131,7 @@ bool attn_encode_map(ft_kv* kv) {
 cudaError_t launch_attn_plan(ft_kv* kv, int B, int T, const int* cu_q, const int* rows, int n_groups,
                              const int* group_start, const int* group_tokens) {
     PlanArgs a{kv->plan, B, T, n_groups, kv->Hq / kv->Hkv, kv->Hkv, kv->page, kv->n_rows, kv->row_pages,
-               MERGE_NB(kv->D), cu_q, rows, group_start, group_tokens, kv->lens, kv->err};
+               MERGE_NB(kv->D), kv->num_sms * 24, cu_q, rows, group_start, group_tokens, kv->lens, kv->err};
     const cudaError_t e = ensure_dynamic_smem((const void*)attn_plan_kernel, CUM * 4);
     if (e != cudaSuccess) return e;
     void* args[] = {&a};
