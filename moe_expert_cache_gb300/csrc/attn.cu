@@ -27,7 +27,7 @@
 
 namespace {
 
-constexpr int G_THREADS = 256;        // 4 softmax warps, a TMA warp, an MMA warp, two idle ones
+constexpr int G_THREADS = 256;        // 4 softmax warps, two TMA warps, an MMA warp, an idle one
 // with two CTAs an SM: 128 registers a thread at launch; 128 x 208 + 128 x 48 = 256 x 128
 constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 48;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -42,10 +42,14 @@ struct Cfg {
     static constexpr int CTAS = D == 256 ? 1 : 2;            // per SM
     static constexpr uint32_t TCOLS = D == 256 ? 512 : 256;  // O: D columns, S: NS x 128
     static constexpr int NS = D == 256 ? 2 : 1;
-    static constexpr uint32_t TILE = ATTN_BN * D * 2;
     static constexpr uint32_t QBYTES = ATTN_BM * D * 2;
-    static constexpr int NST = D == 64 ? 5 : 2;              // K and V tiles in the ring
-    static constexpr size_t SMEM = QBYTES + (size_t)NST * TILE;
+    // K and V have a ring each.  At head size 256 their tiles come in halves (K by values, V by keys), so that a stage
+    // is free again, and the next load under way, while the other half is still in use (prompts 441 -> 413 us); with two
+    // CTAs an SM the other CTA covers that, and the doubled number of copies cost 3%
+    static constexpr int HALVES = D == 256 ? 2 : 1;
+    static constexpr uint32_t STAGE = ATTN_BN * D * 2 / HALVES;
+    static constexpr int NK = D == 64 ? 3 : D == 128 ? 1 : 2, NV = D == 128 ? 1 : 3;  // stages
+    static constexpr size_t SMEM = QBYTES + (size_t)(NK + NV) * STAGE;
 };
 
 struct AttnArgs {
@@ -160,14 +164,15 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(ft::smem_addr(bar))
         : "memory");
 }
-// S = Q K^T of a tile: D / 16 steps; 8 values of 16 bytes a step, 64 a block.
-template <int D>
-__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
+// S (+)= Q K^T over NB blocks of 64 values: steps of 16 values.
+template <int NB>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc, uint32_t accumulate) {
 #pragma unroll
-    for (int b = 0; b < D / 64; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            mma_ss(d, q + b * (128 * 128 / 16) + 2 * i, k + b * (ATTN_BN * 128 / 16) + 2 * i, idesc, (b | i) ? 1u : 0u);
+            mma_ss(d, q + b * (ATTN_BM * 128 / 16) + 2 * i, k + b * (ATTN_BN * 128 / 16) + 2 * i, idesc,
+                   (b | i) ? 1u : accumulate);
 }
 // O (+)= P V over 64 keys: steps of 16 keys, 8 columns of P and 2048 bytes of V.
 __device__ __forceinline__ void mma_values(uint32_t o, uint32_t pt, uint32_t v, uint32_t idesc, uint32_t accumulate) {
@@ -331,21 +336,25 @@ template <int D, bool BF>
 __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __grid_constant__ CUtensorMap map,
                                                                        const AttnArgs p) {
     using C = Cfg<D>;
-    constexpr int NST = C::NST, NS = C::NS;
+    constexpr int NK = C::NK, NV = C::NV, NS = C::NS;
     extern __shared__ __align__(1024) unsigned char smQ[];  // Q, then the ring
-    __shared__ uint64_t kv_full[NST], kv_empty[NST], s_full[NS], p_full[NS][2], pv_done[2], q_full, o_full, o_empty, w_full,
+    __shared__ uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full[NS], p_full[NS][2], pv_done[2], q_full, o_full, o_empty, w_full,
         done;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_fail;
     __shared__ __align__(16) AttnWork s_work[NWORK];
-    unsigned char* ring = smQ + C::QBYTES;
+    unsigned char *ring_k = smQ + C::QBYTES, *ring_v = ring_k + NK * C::STAGE;
     const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
 
     ft::grid_dep_launch();
     if (tid == 128) {
-        for (int s = 0; s < NST; ++s) {
-            ft::mbar_init(&kv_full[s], 1);
-            ft::mbar_init(&kv_empty[s], 1);
+        for (int s = 0; s < NK; ++s) {
+            ft::mbar_init(&k_full[s], 1);
+            ft::mbar_init(&k_empty[s], 1);
+        }
+        for (int s = 0; s < NV; ++s) {
+            ft::mbar_init(&v_full[s], 1);
+            ft::mbar_init(&v_empty[s], 1);
         }
         for (int b = 0; b < NS; ++b) {
             ft::mbar_init(&s_full[b], 1);
@@ -391,18 +400,19 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
 
     if (wid >= 4) {
         if (C::CTAS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-        if (wid == 4) {
-        // ------------------------------------------------------------ TMA warp
-        // order of the ring: K0, V0, K1, V1, ... with one S, K0, K1, V0, K2, V1, ... with two
-        constexpr int NB = D / 64;                           // boxes across a row
-        const int boxes = (ATTN_BN / p.page) * NB;           // a box is a page's rows by 64 values
-        const int sub = lane / NB, blk = lane % NB;
-        const bool mine = lane < boxes;
+        if (wid == 4 || wid == 6) {
+        // ---------------------------------------- TMA warps: keys, values
+        const int kv = wid == 4 ? 0 : 1, NST = kv ? NV : NK;
+        uint64_t *full = kv ? v_full : k_full, *empty = kv ? v_empty : k_empty;
+        unsigned char* ring = kv ? ring_v : ring_k;
+        constexpr int NB = D / 64, H = C::HALVES;            // blocks of 64 values across a row
+        const int rows = min(p.page, 64), nsub = ATTN_BN / rows;  // a box is 64 values of a page's rows, at most 64
         const int oob = p.n_pages * p.L * 2 * p.Hkv;         // a box past the map's end reads zeros
-        // the page of this lane's box of a tile is read two tiles ahead, across items, and looked at only when the
-        // box is issued
+        // lane i < nsub reads the page of the tile's i-th run of rows, two tiles ahead, across items; it is looked at
+        // only when a box of it is issued
         constexpr int NONE = 0x7fffffff;                     // no key of the item there: reads zeros
-        int it = 0, rw = w0, ri = 0;
+        int st = 0, n = 0, rw = w0, ri = 0;  // st, par: next stage, parity of its phase; n stages issued
+        uint32_t par = 0;
         bool ok = true;
         AttnWork kr = mine0.first;
         auto read = [&]() {
@@ -411,73 +421,85 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                 if (++rw < w1) kr = work(rw);
             }
             if (rw >= w1) return NONE;
-            const int pos = kr.pos0 + ri * ATTN_BN + sub * p.page;
+            const int pos = kr.pos0 + ri * ATTN_BN + lane * rows;
             ++ri;
-            return !mine || pos >= kr.kend ? NONE : p.table[(size_t)kr.trow * p.row_pages + (pos >> p.page_log)];
+            return lane >= nsub || pos >= kr.kend ? NONE : p.table[(size_t)kr.trow * p.row_pages + (pos >> p.page_log)];
         };
         // the first tile's pages need the first item only: they are read while the items are still on their way
-        int prev = NONE, cur = read();
+        int cur = read();
         if (nw > 0) ok = __all_sync(0xffffffffu, ft::mbar_wait(&w_full, 0, p.err));
         int next = ok ? read() : NONE;
         for (int w = w0; w < w1 && ok && !__any_sync(0xffffffffu, s_fail); ++w) {
-            const int nt = work(w).ntile, head = work(w).head;
-            auto issue = [&](int id, int kv) {
-                const int st = it % NST;
-                if (it >= NST && !ft::mbar_wait(&kv_empty[st], ((it / NST) - 1) & 1, p.err)) ok = false;
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) return;
-                if (lane == 0) ft::mbar_arrive_expect_tx(&kv_full[st], C::TILE);
-                __syncwarp();
-                if (mine) {
+            const AttnWork k = work(w);
+            // one stage: boxes of runs [sub0, sub0 + ns) by blocks [blk0, blk0 + nb), a block `bytes` after the other
+            auto stage = [&](int id, int sub0, int ns, int blk0, int nb, uint32_t bytes) {
+                // (a new barrier passes for the phase before its first)
+                if (!__all_sync(0xffffffffu, ft::mbar_wait(&empty[st], par ^ 1u, p.err))) {
+                    ok = false;
+                    return;
+                }
+                if (lane == 0) ft::mbar_arrive_expect_tx(&full[st], C::STAGE);
+                const int sub = lane / nb, blk = lane % nb, mine = __shfl_sync(0xffffffffu, id, sub0 + sub);
+                if (sub < ns) {
                     int z = oob;
-                    if ((unsigned)id < (unsigned)p.n_pages)
-                        z = ((id * p.L + p.layer) * 2 + kv) * p.Hkv + head;
-                    else if (id != NONE)
+                    if ((unsigned)mine < (unsigned)p.n_pages)
+                        z = ((mine * p.L + p.layer) * 2 + kv) * p.Hkv + k.head;
+                    else if (mine != NONE)
                         atomicOr(p.err, FT_DEVERR_ARG);
-                    unsigned char* dst = ring + (size_t)st * C::TILE + blk * (ATTN_BN * 128) + sub * p.page * 128;
-                    tc::tma_load_3d(dst, &map, blk * 64, 0, z, &kv_full[st]);
+                    tc::tma_load_3d(ring + (size_t)st * C::STAGE + blk * bytes + sub * rows * 128, &map, (blk0 + blk) * 64,
+                                    ((sub0 + sub) * rows) & (p.page - 1), z, &full[st]);
                 }
-                ++it;
+                ++n;
+                if (++st == NST) {
+                    st = 0;
+                    par ^= 1u;
+                }
             };
-            for (int i = 0; i < nt && ok; ++i) {
+            for (int i = 0; i < k.ntile && ok; ++i) {
                 const int next2 = read();
-                if (NS == 1) {
-                    issue(cur, 0);
-                    if (ok) issue(cur, 1);
-                } else {  // K of the tile, then V of the one before
-                    issue(cur, 0);
-                    if (ok && i > 0) issue(prev, 1);
-                    if (ok && i == nt - 1) issue(cur, 1);
+                if (kv == 0) {
+                    for (int h = 0; h < H && ok; ++h) stage(cur, 0, nsub, h * (NB / H), NB / H, ATTN_BN * 128);
+                } else {  // an upper half without keys is left out
+                    const int halves = H == 2 && k.kend - (k.pos0 + i * ATTN_BN) <= 64 ? 1 : H;
+                    for (int h = 0; h < halves && ok; ++h) stage(cur, h * (nsub / H), nsub / H, 0, NB, ATTN_BN / H * 128);
                 }
-                prev = cur;
                 cur = next;
                 next = next2;
             }
         }
         if (!ok) s_fail = 1;
-        for (int j = it - NST; j < it; ++j)  // nothing in flight into shared memory at exit
-            if (j >= 0) ft::mbar_wait(&kv_full[j % NST], (j / NST) & 1, p.err);
+        for (int j = max(0, n - NST); j < n; ++j)  // nothing in flight into shared memory at exit
+            ft::mbar_wait(&full[j % NST], (j / NST) & 1, p.err);
     } else if (wid == 5) {
         // ------------------------------------------------------------ MMA warp
         {
             constexpr uint32_t id_s = idesc_of(BF, ATTN_BN, false), id_o = idesc_of(BF, D, true);
-            const uint32_t kdesc = desc_k(ring), vdesc = desc_v(ring, ATTN_BN * 128), qdesc = desc_k(smQ);
-            constexpr uint32_t TW = C::TILE / 16;
+            constexpr int H = C::HALVES;
+            const uint32_t kdesc = desc_k(ring_k), vdesc = desc_v(ring_v, ATTN_BN / H * 128), qdesc = desc_k(smQ);
+            constexpr uint32_t SW = C::STAGE / 16, QW = (D / 64) / H * (ATTN_BM * 128 / 16);
             int g = 0, n = 0;
             uint32_t ph = 0;  // phase bits of p_full[b][h], at 2 b + h
-            Slot r;
+            Slot rk, rv;
             bool ok = true;
             auto wait = [&](uint64_t* b, uint32_t phase) {
                 if (!__all_sync(0xffffffffu, ft::mbar_wait(b, phase & 1u, p.err))) ok = false;
             };
             Slot sc;  // score buffer of the next tile
+            auto release_v = [&]() {
+                mma_commit(&v_empty[rv.st]);
+                advance<NV>(rv);
+            };
             auto scores = [&]() {  // S = Q K^T with the next tile of the ring
-                wait(&kv_full[r.st], r.ph);
-                tc::fence_after_sync();
-                mma_scores<D>(tmem + (uint32_t)(D + sc.st * ATTN_BN), qdesc, kdesc + r.st * TW, id_s);
-                mma_commit(&kv_empty[r.st]);
-                mma_commit(&s_full[sc.st]);
-                advance<NST>(r);
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    wait(&k_full[rk.st], rk.ph);
+                    tc::fence_after_sync();
+                    mma_scores<(D / 64) / H>(tmem + (uint32_t)(D + sc.st * ATTN_BN), qdesc + h * QW, kdesc + rk.st * SW, id_s,
+                                             h ? 1u : 0u);
+                    if (h == H - 1) mma_commit(&s_full[sc.st]);
+                    mma_commit(&k_empty[rk.st]);
+                    advance<NK>(rk);
+                }
                 advance<NS>(sc);
             };
             int sb = 0;
@@ -490,22 +512,25 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                 for (int i = 0; i < nt && ok; ++i, ++g) {
                     if (NS == 2 && i + 1 < nt) scores();
                     if (i == 0 && n > 0) wait(&o_empty, n - 1);
-                    wait(&kv_full[r.st], r.ph);
-                    const uint32_t pt = tmem + (uint32_t)(D + sb * ATTN_BN), vd = vdesc + r.st * TW;
+                    wait(&v_full[rv.st], rv.ph);
+                    const uint32_t pt = tmem + (uint32_t)(D + sb * ATTN_BN);
                     wait(&p_full[sb][0], ph >> (2 * sb));
                     ph ^= 1u << (2 * sb);
                     tc::fence_after_sync();
-                    mma_values(tmem, pt, vd, id_o, i ? 1u : 0u);
+                    mma_values(tmem, pt, vdesc + rv.st * SW, id_o, i ? 1u : 0u);
                     if (keys - i * ATTN_BN > 64) {
+                        if (H == 2) {
+                            release_v();
+                            wait(&v_full[rv.st], rv.ph);
+                        }
                         wait(&p_full[sb][1], ph >> (2 * sb + 1));
                         ph ^= 2u << (2 * sb);
                         tc::fence_after_sync();
-                        mma_values(tmem, pt + 64, vd + 512, id_o, 1u);
+                        mma_values(tmem, pt + 64, vdesc + rv.st * SW + (H == 2 ? 0 : 512), id_o, 1u);
                     }
-                    mma_commit(&kv_empty[r.st]);
+                    release_v();
                     if (NS == 2) mma_commit(&pv_done[g & 1]);
                     if (i == nt - 1) mma_commit(&o_full);
-                    advance<NST>(r);
                     if (NS == 2) sb ^= 1;
                     if (NS == 1 && i + 1 < nt) scores();
                 }
@@ -518,6 +543,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     } else {
         if (C::CTAS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         // ------------------------------------------------------- softmax warps
+        constexpr int H = C::HALVES;
         const int r = tid;  // row of the item: TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)(wid * 32) << 16);
         auto publish_q = [&]() {
@@ -625,15 +651,16 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                         }
                     }
                 }
-                if (valid < ATTN_BN) {
+                if (valid < ATTN_BN && (H == 1 || valid != 64)) {
                     // what the pool holds past the keys may be anything: its weights are 0, its values are made 0
-                    const int vit = it0 + (NS == 1 ? 2 * i + 1 : min(i + 2, k.ntile) + i), st = vit % NST;
-                    if (!wait(&kv_full[st], vit / NST)) ok = false;
-                    unsigned char* vt = ring + (size_t)st * C::TILE;
-                    const int z0 = max(valid, 0), nz = ((two ? ATTN_BN : 64) - z0) * 8;
+                    const int vit = it0 + H * i + (H == 2 && two), st = vit % NV;
+                    if (!wait(&v_full[st], vit / NV)) ok = false;
+                    unsigned char* vt = ring_v + (size_t)st * C::STAGE;
+                    // rows of this stage (of 64 keys, or of the whole tile) that hold no key
+                    const int z0 = max(H == 2 && two ? valid - 64 : valid, 0), nz = ((H == 1 && two ? ATTN_BN : 64) - z0) * 8;
                     for (int x = tid; x < nz * (D / 64); x += 128) {
                         const int b = x / nz, y = x % nz;
-                        *reinterpret_cast<uint4*>(vt + b * (ATTN_BN * 128) + z0 * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(vt + b * (ATTN_BN / H * 128) + z0 * 128 + y * 16) = make_uint4(0, 0, 0, 0);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
@@ -700,7 +727,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) ft::mbar_arrive(&o_empty);
-            it0 += 2 * k.ntile;
+            it0 += H * k.ntile - (H == 2 && k.kend - (k.pos0 + (k.ntile - 1) * ATTN_BN) <= 64);
         }
         if (!ok) s_fail = 1;
         ft::cp_async_wait_all();
@@ -1111,7 +1138,7 @@ void attn_plan_sizes(int Hq, int Hkv, int D, int T_max, int B_max, int num_sms, 
 size_t attn_seg_bytes(const AttnPlan& p) { return (size_t)p.cap_segs * sizeof(SegRec); }
 
 // The pool as [n_pages*L*2*Hkv][page][D], read in boxes of 64 values by a
-// page's rows with 128-byte swizzle.
+// page's rows (at most 64) with 128-byte swizzle.
 bool attn_encode_map(ft_kv* kv) {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -1120,7 +1147,7 @@ bool attn_encode_map(ft_kv* kv) {
         return false;
     const cuuint64_t dims[3] = {(cuuint64_t)kv->D, (cuuint64_t)kv->page, (cuuint64_t)kv->n_pages * kv->L * 2 * kv->Hkv};
     const cuuint64_t strides[2] = {(cuuint64_t)kv->D * 2, (cuuint64_t)kv->D * 2 * kv->page};
-    const cuuint32_t box[3] = {64, (cuuint32_t)kv->page, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(kv->page < 64 ? kv->page : 64), 1};
     const cuuint32_t es[3] = {1, 1, 1};
     return reinterpret_cast<EncodeTiledFn>(f)(
                &kv->map, kv->dtype == FT_KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
