@@ -31,7 +31,7 @@ constexpr int G_THREADS = 256;        // 4 softmax warps, two TMA warps, an MMA 
 // with two CTAs an SM: 128 registers a thread at launch; 128 x 208 + 128 x 48 = 256 x 128
 constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 48;
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float RESCALE_LAG = 8.f;   // log2 units
+constexpr float MAX_SUM = 4096.f;    // of a tile's weights on a reference that has fallen behind (f16 holds 65504)
 constexpr int MERGE_NB(int D) { return D == 256 ? 4 : 8; }  // pieces that a warp of the join has in flight
 constexpr int NWORK = 16;            // work items of a CTA that are kept in shared memory
 constexpr int OV = 2;                // cost of an item's start, in tiles
@@ -39,16 +39,16 @@ constexpr int OVP = 4;               // the same with the partial result of a pr
 
 template <int D>
 struct Cfg {
-    static constexpr int CTAS = D == 256 ? 1 : 2;            // per SM
-    static constexpr uint32_t TCOLS = D == 256 ? 512 : 256;  // O: D columns, S: NS x 128
-    static constexpr int NS = D == 256 ? 2 : 1;
+    static constexpr int CTAS = D == 64 ? 2 : 1;             // per SM
+    static constexpr uint32_t TCOLS = CTAS == 1 ? 512 : 256; // O: D columns, S: NS x 128
+    static constexpr int NS = CTAS == 1 ? 2 : 1;
     static constexpr uint32_t QBYTES = ATTN_BM * D * 2;
     // K and V have a ring each.  At head size 256 their tiles come in halves (K by values, V by keys), so that a stage
     // is free again, and the next load under way, while the other half is still in use (prompts 441 -> 413 us); with two
     // CTAs an SM the other CTA covers that, and the doubled number of copies cost 3%
     static constexpr int HALVES = D == 256 ? 2 : 1;
     static constexpr uint32_t STAGE = ATTN_BN * D * 2 / HALVES;
-    static constexpr int NK = D == 64 ? 3 : D == 128 ? 1 : 2, NV = D == 128 ? 1 : 3;  // stages
+    static constexpr int NK = D == 256 ? 2 : 3, NV = 3;      // stages
     static constexpr size_t SMEM = QBYTES + (size_t)(NK + NV) * STAGE;
 };
 
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     using C = Cfg<D>;
     constexpr int NK = C::NK, NV = C::NV, NS = C::NS;
     extern __shared__ __align__(1024) unsigned char smQ[];  // Q, then the ring
-    __shared__ uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full[NS], p_full[NS][2], pv_done[2], q_full, o_full, o_empty, w_full,
+    __shared__ uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full[NS], p_full[NS], pv_done[2], q_full, o_full, o_empty, w_full,
         done;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_fail;
@@ -358,8 +358,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
         }
         for (int b = 0; b < NS; ++b) {
             ft::mbar_init(&s_full[b], 1);
-            ft::mbar_init(&p_full[b][0], 4);
-            ft::mbar_init(&p_full[b][1], 4);
+            ft::mbar_init(&p_full[b], 4);
         }
         for (int b = 0; b < 2; ++b) ft::mbar_init(&pv_done[b], 1);
         ft::mbar_init(&q_full, 4);
@@ -478,7 +477,6 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
             const uint32_t kdesc = desc_k(ring_k), vdesc = desc_v(ring_v, ATTN_BN / H * 128), qdesc = desc_k(smQ);
             constexpr uint32_t SW = C::STAGE / 16, QW = (D / 64) / H * (ATTN_BM * 128 / 16);
             int g = 0, n = 0;
-            uint32_t ph = 0;  // phase bits of p_full[b][h], at 2 b + h
             Slot rk, rv;
             bool ok = true;
             auto wait = [&](uint64_t* b, uint32_t phase) {
@@ -514,19 +512,16 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                     if (i == 0 && n > 0) wait(&o_empty, n - 1);
                     wait(&v_full[rv.st], rv.ph);
                     const uint32_t pt = tmem + (uint32_t)(D + sb * ATTN_BN);
-                    wait(&p_full[sb][0], ph >> (2 * sb));
-                    ph ^= 1u << (2 * sb);
+                    wait(&p_full[sb], g / NS);
                     tc::fence_after_sync();
                     mma_values(tmem, pt, vdesc + rv.st * SW, id_o, i ? 1u : 0u);
                     if (keys - i * ATTN_BN > 64) {
                         if (H == 2) {
                             release_v();
                             wait(&v_full[rv.st], rv.ph);
+                            tc::fence_after_sync();
                         }
-                        wait(&p_full[sb][1], ph >> (2 * sb + 1));
-                        ph ^= 2u << (2 * sb);
-                        tc::fence_after_sync();
-                        mma_values(tmem, pt + 64, vdesc + rv.st * SW + (H == 2 ? 0 : 512), id_o, 1u);
+                        mma_values(tmem, pt + 32, vdesc + rv.st * SW + (H == 2 ? 0 : 512), id_o, 1u);
                     }
                     release_v();
                     if (NS == 2) mma_commit(&pv_done[g & 1]);
@@ -580,11 +575,24 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                 const int valid = k.kend - pos;
                 const bool two = valid > 64;  // keys in the upper half
                 const uint32_t sa = lane_base + (uint32_t)(D + (g % NS) * ATTN_BN);
-                uint32_t s[ATTN_BN];
+                uint32_t s[ATTN_BN];  // scores, then (in the first half of each half) the weights in the cache's type
                 float* f = reinterpret_cast<float*>(s);
-                float mc = 0.f, lh = 0.f;
-                uint32_t pk[32];
                 const uint64_t c2 = f2(p.c, p.c);
+                float mc = 0.f, lt = 0.f;
+                auto load = [&](int h) {
+                    tc::tmem_ld32(sa + 64 * h, s + 64 * h);
+                    tc::tmem_ld32(sa + 64 * h + 32, s + 64 * h + 32);
+                };
+                auto loaded = [&](int h) {  // ... and masked
+                    tc::tmem_wait_ld(s + 64 * h);
+                    tc::tmem_wait_ld(s + 64 * h + 32);
+                    const int left = lim - (pos + 64 * h);
+                    if (left < 64) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (j >= left) f[64 * h + j] = -INFINITY;
+                    }
+                };
                 // weights of 64 keys on the reference mc; returns their sum.  The weights go to the product in the
                 // cache's own type; l keeps their fp32 values.
                 auto weights = [&](int h) {
@@ -596,40 +604,45 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                         e.x = ex2(e.x);
                         e.y = ex2(e.y);
                         l4[(j >> 1) & 3] = add2(l4[(j >> 1) & 3], f2(e.x, e.y));
-                        pk[j >> 1] = pack2<BF>(e.x, e.y);
+                        s[64 * h + (j >> 1)] = pack2<BF>(e.x, e.y);
                     }
                     const float2 ls = unf2(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])));
                     return ls.x + ls.y;
                 };
                 auto reference = [&]() { mc = m == -INFINITY ? 0.f : m * p.c; };  // -inf: a row that has seen no key yet
                 if (rows_here) {
-#pragma unroll
-                    for (int j = 0; j < ATTN_BN; j += 32) tc::tmem_ld32(sa + j, s + j);
-#pragma unroll
-                    for (int j = 0; j < ATTN_BN; j += 32) tc::tmem_wait_ld(s + j);
-                    const int left = lim - pos;
-                    if (left < ATTN_BN) {
-#pragma unroll
-                        for (int j = 0; j < ATTN_BN; ++j)
-                            if (j >= left) f[j] = -INFINITY;
-                    }
-                    float mx[4] = {m, m, m, m};  // four chains
-                    // past the first tile the reference is almost always good enough: the weights are begun on it,
-                    // beside the maxima that tell whether it is
-                    if (i > 0) {
+                    load(0);
+                    bool exact = i == 0;
+                    if (!exact) {
+                        // the reference of the tiles before is almost always good enough; whether it is, the sum tells
                         reference();
-                        lh = weights(0);
+                        loaded(0);
+                        if (two) load(1);
+                        lt = weights(0);
+                        if (two) {
+                            loaded(1);
+                            lt += weights(1);
+                        }
+                        // (lanes past the rows hold anything)
+                        exact = __any_sync(0xffffffffu, r < k.nrows && lt > MAX_SUM);
+                        if (exact) load(0);
                     }
+                    if (exact) {
+                        if (two) load(1);
+                        loaded(0);
+                        float mx[4] = {m, m, m, m};  // four chains
 #pragma unroll
-                    for (int j = 0; j < ATTN_BN; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], f[j], f[j + 1]);
-                    const float mn = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                    if (i == 0) {
-                        m = mn;
-                        reference();
-                        lh = weights(0);
-                    } else {
-                        const bool lag = r < k.nrows && (mn - m) * p.c > RESCALE_LAG;  // lanes past the rows hold anything
-                        if (__any_sync(0xffffffffu, lag)) {
+                        for (int j = 0; j < 64; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], f[j], f[j + 1]);
+                        if (two) {
+                            loaded(1);
+#pragma unroll
+                            for (int j = 64; j < ATTN_BN; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], f[j], f[j + 1]);
+                        }
+                        const float mn = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                        if (i == 0) {
+                            m = mn;
+                        } else {
+                            const bool lag = r < k.nrows && lt > MAX_SUM;
                             // with one S the scores' own barrier has told that the product before them is done
                             if (NS == 2 && !wait(&pv_done[(g - 1) & 1], (g - 1) >> 1)) ok = false;
                             tc::fence_after_sync();
@@ -645,11 +658,14 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                                 for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fac);
                                 tmem_st32(lane_base + (uint32_t)cc, o);
                             }
-                            tmem_wait_st();
-                            reference();
-                            lh = weights(0);
                         }
+                        reference();
+                        lt = weights(0);
+                        if (two) lt += weights(1);
                     }
+                    l += lt;
+                    tmem_st32(sa, s);
+                    if (two) tmem_st32(sa + 32, s + 64);
                 }
                 if (valid < ATTN_BN && (H == 1 || valid != 64)) {
                     // what the pool holds past the keys may be anything: its weights are 0, its values are made 0
@@ -664,19 +680,10 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1 && !two) continue;
-                    if (rows_here) {
-                        l += lh;
-                        tmem_st32(sa + 64 * h, pk);
-                        tmem_wait_st();
-                    }
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) ft::mbar_arrive(&p_full[g % NS][h]);
-                    if (h == 0 && two && rows_here) lh = weights(1);
-                }
+                if (rows_here) tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ft::mbar_arrive(&p_full[g % NS]);
             }
             if (!ok) break;
             if (w + 1 < w1) publish_q();
@@ -1124,7 +1131,7 @@ cudaError_t launch_typed(ft_kv* kv, const AttnArgs& a, const AttnPlan& pl) {
 void attn_plan_sizes(int Hq, int Hkv, int D, int T_max, int B_max, int num_sms, AttnPlan& p) {
     const int G = Hq / Hkv;
     const int rts = (int)(((long long)T_max * G + ATTN_BM - 1) / ATTN_BM);
-    p.n_cta = num_sms * (D == 256 ? 1 : 2);
+    p.n_cta = num_sms * (D == 64 ? 2 : 1);
     p.cap_segs = rts + B_max;                          // a request's last tile may be short
     p.cap_items = 4 * p.n_cta + Hkv * (rts + B_max);   // four rounds, or a chunk for each row tile
     p.cap_works = p.cap_items + Hkv * p.cap_segs + p.n_cta;
