@@ -39,7 +39,7 @@ constexpr int OVP = 4;               // the same with the partial result of a pr
 
 template <int D>
 struct Cfg {
-    static constexpr int CTAS = D == 64 ? 2 : 1;             // per SM
+    static constexpr int CTAS = D != 256 ? 2 : 1;             // per SM
     static constexpr uint32_t TCOLS = CTAS == 1 ? 512 : 256; // O: D columns, S: NS x 128
     static constexpr int NS = CTAS == 1 ? 2 : 1;
     static constexpr uint32_t QBYTES = ATTN_BM * D * 2;
@@ -48,7 +48,7 @@ struct Cfg {
     // CTAs an SM the other CTA covers that, and the doubled number of copies cost 3%
     static constexpr int HALVES = D == 256 ? 2 : 1;
     static constexpr uint32_t STAGE = ATTN_BN * D * 2 / HALVES;
-    static constexpr int NK = D == 256 ? 2 : 3, NV = 3;      // stages
+    static constexpr int NK = D == 256 ? 2 : D == 128 ? 1 : 3, NV = D == 128 ? 1 : 3;      // stages
     static constexpr size_t SMEM = QBYTES + (size_t)(NK + NV) * STAGE;
 };
 
@@ -1131,7 +1131,7 @@ cudaError_t launch_typed(ft_kv* kv, const AttnArgs& a, const AttnPlan& pl) {
 void attn_plan_sizes(int Hq, int Hkv, int D, int T_max, int B_max, int num_sms, AttnPlan& p) {
     const int G = Hq / Hkv;
     const int rts = (int)(((long long)T_max * G + ATTN_BM - 1) / ATTN_BM);
-    p.n_cta = num_sms * (D == 64 ? 2 : 1);
+    p.n_cta = num_sms * (D != 256 ? 2 : 1);
     p.cap_segs = rts + B_max;                          // a request's last tile may be short
     p.cap_items = 4 * p.n_cta + Hkv * (rts + B_max);   // four rounds, or a chunk for each row tile
     p.cap_works = p.cap_items + Hkv * p.cap_segs + p.n_cta;
