@@ -64,7 +64,8 @@ size_t ft_kv_scratch_bytes(int32_t Hq, int32_t Hkv, int32_t D, int32_t n_pages, 
  *                  reads key/value head i / (Hq/Hkv)), head size 64, 128 or 256.
  *   page           tokens of a page: 16, 32, 64 or 128.
  *   n_pages, n_rows, row_pages  sizes of the pool and the table;
- *                  row_pages*page and n_pages*L*2*Hkv below 2^31.
+ *                  row_pages*page and n_pages*L*2*Hkv below 2^31, n_rows
+ *                  at most 65536.
  *   dtype          FT_KV_BF16 or FT_KV_F16: type of the pool, the queries and
  *                  the outputs.
  *   T_max, B_max   largest number of query tokens and of requests of an

@@ -17,11 +17,29 @@
 // one line of tiles cut into equal parts, one per CTA, whatever request or head
 // a cut falls into.
 //
-// One CTA: 4 softmax warps (a thread per row), a TMA warp, an MMA warp; K and
-// V tiles in a ring of shared memory with 128-byte swizzle; S (two buffers)
-// and O in TMEM; P goes back to TMEM over its S and is the A operand of P V.
-// The running maximum is let fall behind by up to 2^8 before O is rescaled:
-// the weights stay exact, and almost no tile touches O.
+// One CTA: 4 softmax warps (a thread per row), a TMA warp each for keys and
+// values, an MMA warp; K and V tiles in rings of shared memory with 128-byte
+// swizzle; S and O in TMEM; P goes back to TMEM over its S and is the A operand
+// of P V.  Two CTAs an SM at head sizes 64 and 128: while one's softmax works,
+// the tensor core has the other's products.  At 256, where O takes half of
+// TMEM, one CTA with two score buffers.
+//
+// The running maximum is a reference that may fall behind: past an item's first
+// tile the weights are taken on the present one, and only where a tile's weights
+// sum to more than 4096 is the tile done again on its own maximum and O rescaled.
+// The weights stay as exact (they are floating-point numbers on any scale), no
+// maxima are taken, and almost no tile touches O.
+//
+// What bounds it: few rows, HBM (8 rows over 262144 keys: 537 MB in 88 us with
+// the join, 90% of the copy rate); many rows, the chain scores -> weights ->
+// product of a CTA beside the other CTA's (a prompt of 4096 tokens behind 8192
+// at head size 128: 512 us, 1340 TFLOP/s, 70% of cuBLAS; 411 us at head size
+// 256); short items, the latency of their start (about 3 us).
+// Tried at head size 128 and left: tiles of 64 keys (the products of 128 x 64
+// wait for Q's reads; 4% slower), one CTA with two streams of 128 rows over
+// shared tiles (prompts 4% faster, short items 1.6 times slower) or over
+// alternate tiles (the ring could not keep up), rings of half tiles (3% slower),
+// a cooperative launch with the join at its end (launch +2 us).
 #include "ft_kv.cuh"
 #include "ft_tc.cuh"
 
@@ -337,7 +355,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                                                                        const AttnArgs p) {
     using C = Cfg<D>;
     constexpr int NK = C::NK, NV = C::NV, NS = C::NS;
-    extern __shared__ __align__(1024) unsigned char smQ[];  // Q, then the ring
+    extern __shared__ __align__(1024) unsigned char smQ[];  // Q, then the rings of K and V
     __shared__ uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full[NS], p_full[NS], pv_done[2], q_full, o_full, o_empty, w_full,
         done;
     __shared__ uint32_t s_tmem;
@@ -346,7 +364,6 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     unsigned char *ring_k = smQ + C::QBYTES, *ring_v = ring_k + NK * C::STAGE;
     const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
 
-    ft::grid_dep_launch();
     if (tid == 128) {
         for (int s = 0; s < NK; ++s) {
             ft::mbar_init(&k_full[s], 1);
@@ -375,6 +392,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = s_tmem;
+    ft::grid_dep_launch();  // (its TMEM is allocated: no CTA of a later kernel can hold what this one needs)
     // up to here nothing touched global memory: it ran beside the end of the kernel before this one
     ft::grid_dep_wait();
     const AttnCta mine0 = p.ctas[blockIdx.x];
@@ -400,7 +418,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     if (wid >= 4) {
         if (C::CTAS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
         if (wid == 4 || wid == 6) {
-        // ---------------------------------------- TMA warps: keys, values
+        // ---------------------------------------------------- TMA warps: keys, values
         const int kv = wid == 4 ? 0 : 1, NST = kv ? NV : NK;
         uint64_t *full = kv ? v_full : k_full, *empty = kv ? v_empty : k_empty;
         unsigned char* ring = kv ? ring_v : ring_k;
@@ -810,7 +828,8 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
     __shared__ int q_g[PT / 2], q_off[PT / 2];  // per group taken together (it has two requests at least)
     __shared__ int ws[33];
     __shared__ int s_c, s_iph;
-    extern __shared__ int s_cum[];  // [CUM]
+    extern __shared__ __align__(16) int s_cum[];                   // [CUM]
+    int4* s_cta = reinterpret_cast<int4*>(s_cum + CUM);            // [n_cta] first item, first and last segment
     ft::grid_dep_launch();
     ft::grid_dep_wait();
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -986,28 +1005,30 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
             cnt = k0 + (i < n1 ? 1 : 0);
             const long long x0 = start_of(i), x1 = start_of(i + 1);
             if (x1 > x0) {
-                const int l1 = linear(x1 - 1);
-                cnt += l1 - linear(x0) + 1;
+                const int l0 = linear(x0), l1 = linear(x1 - 1);
+                cnt += l1 - l0 + 1;
                 if (x1 - begin_of(l1) <= OV) --cnt;  // only the start cost of the last one: its tiles are the next CTA's
+                s_cta[i] = make_int4(0, l0, l1, 0);
             }
         }
         int total;
         const int at = n_works + scan_excl(cnt, ws, total);
         if (i < n_cta) {
-            p.pl.ctas[i].w0 = at;
+            p.pl.ctas[i].w0 = s_cta[i].x = at;
             p.pl.ctas[i].w1 = at + cnt;
         }
         n_works += total;
     }
     __syncthreads();
-    // a warp per CTA writes its items
-    for (int i = wid; i < n_cta; i += PT / 32) {
-        const int w0 = p.pl.ctas[i].w0, k = k0 + (i < n1 ? 1 : 0);
+    // eight lanes per CTA write its items
+    for (int i = tid >> 3; i < n_cta; i += PT / 8) {
+        const int4 mine = s_cta[i];
+        const int w0 = mine.x, k = k0 + (i < n1 ? 1 : 0), sl = tid & 7;
         auto put = [&](int j, const AttnWork& w) {
             p.pl.works[w0 + j] = w;
             if (j == 0) p.pl.ctas[i].first = w;
         };
-        for (int j = lane; j < k; j += 32) {
+        for (int j = sl; j < k; j += 8) {
             const int idx = j * n_cta + i, h = idx / iph, rem = idx % iph;
             const int q = upper(n_pre, rem, [&](int a) { return q_off[a]; });
             const int gg = q_g[q], nrt = cdiv(g_rows[gg], ATTN_BM), nt = cdiv(g_min[gg], ATTN_BN);
@@ -1028,8 +1049,8 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         }
         const long long x0 = start_of(i), x1 = start_of(i + 1);
         if (x1 <= x0) continue;
-        const int l0 = linear(x0), l1 = linear(x1 - 1);
-        for (int l = l0 + lane; l <= l1; l += 32) {
+        const int l0 = mine.y, l1 = mine.z;
+        for (int l = l0 + sl; l <= l1; l += 8) {
             const long long b0 = begin_of(l);
             const SegRec r = seg[l % n_seg];
             const int t0 = (int)max(0ll, x0 - b0 - OV), t1 = (int)min((long long)r.ntile, max(0ll, x1 - b0 - OV));
@@ -1166,10 +1187,11 @@ cudaError_t launch_attn_plan(ft_kv* kv, int B, int T, const int* cu_q, const int
                              const int* group_start, const int* group_tokens) {
     PlanArgs a{kv->plan, B, T, n_groups, kv->Hq / kv->Hkv, kv->Hkv, kv->page, kv->n_rows, kv->row_pages,
                MERGE_NB(kv->D), kv->num_sms * 24, cu_q, rows, group_start, group_tokens, kv->lens, kv->err};
-    const cudaError_t e = ensure_dynamic_smem((const void*)attn_plan_kernel, CUM * 4);
+    const size_t smem = CUM * 4 + (size_t)kv->plan.n_cta * 16;
+    const cudaError_t e = ensure_dynamic_smem((const void*)attn_plan_kernel, smem);
     if (e != cudaSuccess) return e;
     void* args[] = {&a};
-    return launch_dependent((const void*)attn_plan_kernel, 1, PT, CUM * 4, kv->stream, args);
+    return launch_dependent((const void*)attn_plan_kernel, 1, PT, smem, kv->stream, args);
 }
 
 cudaError_t launch_attn_forward(ft_kv* kv, int layer, const void* q, long long ld_q, void* out, long long ld_o,

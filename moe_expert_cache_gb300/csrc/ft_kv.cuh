@@ -13,6 +13,8 @@
 
 #define FT_DEVERR_CAPACITY 4u  // too few free pages
 
+constexpr int KV_MAX_ROWS = 65536;  // rows of a table (a bit each in shared memory)
+
 // Words of the page operations' summary.
 enum { KV_ALLOCATED = 0, KV_COPIED, KV_LIVE, KV_INFO_WORDS };
 
@@ -97,7 +99,6 @@ struct ft_kv {
     KvCopy* copies;    // [n_pages]
     int* free_list;    // [n_pages]
     int* remap;        // [n_pages]
-    int* mark;         // [n_rows] zero at rest
     int* rank;         // [n_rows]
     AttnPlan plan;
     float* part_o;     // [part_rows, D] unnormalised partial outputs

@@ -13,7 +13,7 @@ namespace {
 
 bool sizes_ok(int Hq, int Hkv, int D, int n_pages, int n_rows, int T_max, int B_max) {
     return Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq / Hkv <= ATTN_BM && (D == 64 || D == 128 || D == 256) &&
-           n_pages >= 1 && n_rows >= 1 && T_max >= 1 && B_max >= 1 && B_max <= ATTN_MAX_B &&
+           n_pages >= 1 && n_rows >= 1 && n_rows <= KV_MAX_ROWS && T_max >= 1 && B_max >= 1 && B_max <= ATTN_MAX_B &&
            (long long)T_max * Hq < (1ll << 30);
 }
 
@@ -21,7 +21,7 @@ size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Offsets of the arrays in the scratch allocation.
 struct Layout {
-    size_t err, info, n_copy, copies, free_list, remap, mark, rank, hdr, ctas, works, merges, seg, part_o, part_ml,
+    size_t err, info, n_copy, copies, free_list, remap, rank, hdr, ctas, works, merges, seg, part_o, part_ml,
         total;
 };
 
@@ -39,7 +39,6 @@ Layout layout(const AttnPlan& p, int D, int n_pages, int n_rows) {
     l.copies = carve((size_t)n_pages * sizeof(KvCopy));
     l.free_list = carve((size_t)n_pages * 4);
     l.remap = carve((size_t)n_pages * 4);
-    l.mark = carve((size_t)n_rows * 4);
     l.rank = carve((size_t)n_rows * 4);
     l.hdr = carve(sizeof(AttnHdr));
     l.ctas = carve((size_t)p.n_cta * sizeof(AttnCta));
@@ -127,7 +126,6 @@ ft_status ft_kv_init(ft_kv** out, int32_t L, int32_t Hq, int32_t Hkv, int32_t D,
     kv->copies = (KvCopy*)(a + l.copies);
     kv->free_list = (int*)(a + l.free_list);
     kv->remap = (int*)(a + l.remap);
-    kv->mark = (int*)(a + l.mark);
     kv->rank = (int*)(a + l.rank);
     kv->plan.hdr = (AttnHdr*)(a + l.hdr);
     kv->plan.ctas = (AttnCta*)(a + l.ctas);

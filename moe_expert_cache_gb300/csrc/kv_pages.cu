@@ -1,6 +1,11 @@
 // Page operations of the key/value cache: one control kernel per call (one
 // CTA: it validates the whole list before it changes anything) and, where
 // pages move, a copy kernel over all layers.
+//
+// The control kernels are bound by the latency of dependent reads (lists,
+// lengths, table entries), about 0.7 us each: what does not depend on the list
+// (the first 4096 reference counts) is read beside it, rows are marked in
+// shared memory, and a table entry that was checked is read again from L1.
 #include "ft_kv.cuh"
 
 namespace {
@@ -10,14 +15,14 @@ constexpr int CT = 1024;  // threads of the control kernels
 struct KvCtl {
     int *table, *lens, *refs;
     int n_pages, n_rows, row_pages, page;
-    int *info, *n_copy, *free_list, *remap, *mark, *rank;
+    int *info, *n_copy, *free_list, *remap, *rank;
     KvCopy* copies;
     unsigned* err;
 };
 
 KvCtl ctl_of(const ft_kv* kv) {
     return KvCtl{kv->table, kv->lens, kv->refs, kv->n_pages, kv->n_rows, kv->row_pages, kv->page,
-                 kv->info, kv->n_copy, kv->free_list, kv->remap, kv->mark, kv->rank, kv->copies, kv->err};
+                 kv->info, kv->n_copy, kv->free_list, kv->remap, kv->rank, kv->copies, kv->err};
 }
 
 // Exclusive prefix sum over the CTA; total gets the sum.  ws: 33 ints.
@@ -46,22 +51,28 @@ __device__ int block_scan(int v, int* ws, int& total) {
     return x - v + (wid ? ws[wid - 1] : 0);
 }
 
+// Which of the four pages from base + 4 * thread on are free, one bit each.
+__device__ __forceinline__ unsigned free_bits(const KvCtl& c, int base) {
+    const int p = base + 4 * threadIdx.x;
+    unsigned f = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (p + j < c.n_pages && c.refs[p + j] == 0) f |= 1u << j;
+    return f;
+}
+
 // The lowest `want` free pages, ascending, to list; returns how many there are
-// (at most a few more than `want` are counted).  Four counts a thread and step.
-__device__ int take_free(const KvCtl& c, int want, int* ws) {
+// (at most a few more than `want` are counted).  first: free_bits(c, 0).
+__device__ int take_free(const KvCtl& c, int want, int* ws, unsigned first) {
     int have = 0;
     for (int base = 0; base < c.n_pages && have < want; base += 4 * CT) {
-        const int p = base + 4 * threadIdx.x;
-        unsigned f = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (p + j < c.n_pages && c.refs[p + j] == 0) f |= 1u << j;
+        const unsigned f = base ? free_bits(c, base) : first;
         int total;
         int at = have + block_scan(__popc(f), ws, total);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (f >> j & 1u) {
-                if (at < want) c.free_list[at] = p + j;
+                if (at < want) c.free_list[at] = base + 4 * threadIdx.x + j;
                 ++at;
             }
         have += total;
@@ -70,30 +81,18 @@ __device__ int take_free(const KvCtl& c, int want, int* ws) {
     return have;
 }
 
-// Rows rows[0..n) are in range and distinct, and none of others[0..n) (may be
-// null) is among them (every thread gets the answer).
-__device__ bool rows_ok(const KvCtl& c, int n, const int* rows, const int* others = nullptr) {
-    bool ok = true;
-    for (int i = threadIdx.x; i < n; i += CT) {
-        const int r = rows[i];
-        if (r < 0 || r >= c.n_rows)
-            ok = false;
-        else if (atomicExch(&c.mark[r], 1))
-            ok = false;
-    }
+// Bits of the rows that a list names.
+struct RowMarks {
+    unsigned w[KV_MAX_ROWS / 32];
+};
+__device__ __forceinline__ void clear(RowMarks& m, int n_rows) {
+    for (int i = threadIdx.x; i < (n_rows + 31) / 32; i += CT) m.w[i] = 0;
     __syncthreads();
-    if (others) {
-        for (int i = threadIdx.x; i < n; i += CT) {
-            const int r = others[i];
-            if (r < 0 || r >= c.n_rows || c.mark[r]) ok = false;
-        }
-        __syncthreads();
-    }
-    for (int i = threadIdx.x; i < n; i += CT) {
-        const int r = rows[i];
-        if (r >= 0 && r < c.n_rows) c.mark[r] = 0;
-    }
-    return __syncthreads_and(ok);
+}
+// Marks row r; false if it is out of range or marked already.
+__device__ __forceinline__ bool mark(RowMarks& m, int r, int n_rows) {
+    if (r < 0 || r >= n_rows) return false;
+    return !(atomicOr(&m.w[r >> 5], 1u << (r & 31)) >> (r & 31) & 1u);
 }
 
 __device__ void set_info(const KvCtl& c, int allocated, int copied, int live) {
@@ -112,22 +111,29 @@ __device__ void refuse(const KvCtl& c, unsigned bit) {
 
 __global__ void __launch_bounds__(CT) kv_extend_kernel(KvCtl c, int n, const int* __restrict__ rows,
                                                        const int* __restrict__ add) {
+    __shared__ int ws[33];
+    __shared__ RowMarks marks;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    clear(marks, c.n_rows);
     ft::grid_dep_launch();
     ft::grid_dep_wait();
-    __shared__ int ws[33];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    if (!rows_ok(c, n, rows)) return refuse(c, FT_DEVERR_ARG);
+    const unsigned first = free_bits(c, 0);
     int want = 0;
     bool ok = true;
     for (int base = 0; base < n; base += CT) {
         const int i = base + threadIdx.x;
         int need = 0;
         if (i < n) {
-            const long long len = c.lens[rows[i]], to = len + add[i];
-            if (len < 0 || add[i] < 0 || to > (long long)c.row_pages * c.page)
+            const int r = rows[i], a = add[i];
+            if (mark(marks, r, c.n_rows)) {
+                const long long len = c.lens[r], to = len + a;
+                if (len < 0 || a < 0 || to > (long long)c.row_pages * c.page)
+                    ok = false;
+                else
+                    need = (int)((to + c.page - 1) / c.page - (len + c.page - 1) / c.page);
+            } else {
                 ok = false;
-            else
-                need = (int)((to + c.page - 1) / c.page - (len + c.page - 1) / c.page);
+            }
         }
         int total;
         const int at = want + block_scan(need, ws, total);
@@ -135,7 +141,7 @@ __global__ void __launch_bounds__(CT) kv_extend_kernel(KvCtl c, int n, const int
         want += total;
     }
     if (!__syncthreads_and(ok)) return refuse(c, FT_DEVERR_ARG);
-    if (take_free(c, want, ws) < want) return refuse(c, FT_DEVERR_CAPACITY);
+    if (take_free(c, want, ws, first) < want) return refuse(c, FT_DEVERR_CAPACITY);
     for (int i = wid; i < n; i += CT / 32) {
         const int r = rows[i], len = c.lens[r], to = len + add[i], at = c.rank[i];
         const int have = (len + c.page - 1) / c.page, end = (to + c.page - 1) / c.page;
@@ -152,24 +158,26 @@ __global__ void __launch_bounds__(CT) kv_extend_kernel(KvCtl c, int n, const int
 
 __global__ void __launch_bounds__(CT) kv_fork_kernel(KvCtl c, int n, const int* __restrict__ parents,
                                                      const int* __restrict__ children) {
+    __shared__ int ws[33];
+    __shared__ RowMarks marks;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    clear(marks, c.n_rows);
     ft::grid_dep_launch();
     ft::grid_dep_wait();
-    __shared__ int ws[33];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    if (!rows_ok(c, n, children, parents)) return refuse(c, FT_DEVERR_ARG);
+    const unsigned first = free_bits(c, 0);
     int want = 0;
     bool ok = true;
     for (int base = 0; base < n; base += CT) {
         const int i = base + threadIdx.x;
         int need = 0;
         if (i < n) {
-            const int p = parents[i];
-            if (c.lens[children[i]] != 0) {
-                ok = false;
-            } else {
+            const int p = parents[i], ch = children[i];
+            if (mark(marks, ch, c.n_rows) && p >= 0 && p < c.n_rows) {
                 const int len = c.lens[p];
-                if (len < 0 || len > (long long)c.row_pages * c.page) ok = false;
+                if (c.lens[ch] != 0 || len < 0 || len > (long long)c.row_pages * c.page) ok = false;
                 need = ok && len % c.page ? 1 : 0;
+            } else {
+                ok = false;
             }
         }
         int total;
@@ -178,14 +186,17 @@ __global__ void __launch_bounds__(CT) kv_fork_kernel(KvCtl c, int n, const int* 
         want += total;
     }
     if (!__syncthreads_and(ok)) return refuse(c, FT_DEVERR_ARG);
+    // no parent is a child; their pages are in range
     for (int i = wid; i < n; i += CT / 32) {
-        const int* row = c.table + (size_t)parents[i] * c.row_pages;
-        const int np = (c.lens[parents[i]] + c.page - 1) / c.page;
+        const int p = parents[i];
+        if (marks.w[p >> 5] >> (p & 31) & 1u) ok = false;
+        const int* row = c.table + (size_t)p * c.row_pages;
+        const int np = (c.lens[p] + c.page - 1) / c.page;
         for (int j = lane; j < np; j += 32)
             if (row[j] < 0 || row[j] >= c.n_pages) ok = false;
     }
     if (!__syncthreads_and(ok)) return refuse(c, FT_DEVERR_ARG);
-    if (take_free(c, want, ws) < want) return refuse(c, FT_DEVERR_CAPACITY);
+    if (take_free(c, want, ws, first) < want) return refuse(c, FT_DEVERR_CAPACITY);
     for (int i = wid; i < n; i += CT / 32) {
         const int p = parents[i], len = c.lens[p], full = len / c.page, tok = len % c.page;
         const int* src = c.table + (size_t)p * c.row_pages;
@@ -208,16 +219,26 @@ __global__ void __launch_bounds__(CT) kv_fork_kernel(KvCtl c, int n, const int* 
 }
 
 __global__ void __launch_bounds__(CT) kv_free_kernel(KvCtl c, int n, const int* __restrict__ rows) {
+    __shared__ RowMarks marks;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    clear(marks, c.n_rows);
     ft::grid_dep_launch();
     ft::grid_dep_wait();
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    bool ok = rows_ok(c, n, rows);
-    if (!ok) return refuse(c, FT_DEVERR_ARG);
+    bool ok = true;
     for (int i = wid; i < n; i += CT / 32) {
         const int r = rows[i];
+        bool mine = true;
+        if (lane == 0) mine = mark(marks, r, c.n_rows);
+        if (!__all_sync(0xffffffffu, mine)) {
+            ok = false;
+            continue;
+        }
         const long long len = c.lens[r];
-        if (len < 0 || len > (long long)c.row_pages * c.page) ok = false;
-        const int np = ok ? (int)((len + c.page - 1) / c.page) : 0;
+        if (len < 0 || len > (long long)c.row_pages * c.page) {
+            ok = false;
+            continue;
+        }
+        const int np = (int)((len + c.page - 1) / c.page);
         for (int j = lane; j < np; j += 32) {
             const int p = c.table[(size_t)r * c.row_pages + j];
             if (p < 0 || p >= c.n_pages) ok = false;
@@ -320,13 +341,16 @@ __global__ void __launch_bounds__(256) kv_copy_kernel(const int* n_copy, const K
     }
 }
 
-cudaError_t launch_copy(ft_kv* kv, bool compact) {
+// at most `most` pages are copied
+cudaError_t launch_copy(ft_kv* kv, bool compact, long long most) {
     int banks = kv->L * 2 * kv->Hkv, bank_bytes = kv->page * kv->D * 2, tok_bytes = kv->D * 2;
     long long entries = compact ? (long long)kv->n_rows * kv->row_pages : 0;
     const int* live = compact ? kv->info + KV_LIVE : nullptr;
     void* args[] = {&kv->n_copy, &kv->copies, &kv->pool, &banks, &bank_bytes, &tok_bytes,
                     &kv->table, &entries, &kv->remap, &live, &kv->n_pages};
-    return launch_dependent((const void*)kv_copy_kernel, kv->num_sms * 8, 256, 0, kv->stream, args);
+    const long long ctas = (most * banks * ((bank_bytes + 4095) / 4096) + 7) / 8;  // a unit a warp
+    const int grid = (int)(ctas < kv->num_sms * 8 ? ctas : kv->num_sms * 8);
+    return launch_dependent((const void*)kv_copy_kernel, grid, 256, 0, kv->stream, args);
 }
 
 }  // namespace
@@ -341,7 +365,7 @@ cudaError_t launch_kv_fork(ft_kv* kv, int n, const int* parents, const int* chil
     KvCtl c = ctl_of(kv);
     void* args[] = {&c, &n, &parents, &children};
     const cudaError_t e = launch_dependent((const void*)kv_fork_kernel, 1, CT, 0, kv->stream, args);
-    return e == cudaSuccess ? launch_copy(kv, false) : e;
+    return e == cudaSuccess && n > 0 ? launch_copy(kv, false, n) : e;
 }
 
 cudaError_t launch_kv_free(ft_kv* kv, int n, const int* rows) {
@@ -354,5 +378,5 @@ cudaError_t launch_kv_compact(ft_kv* kv) {
     KvCtl c = ctl_of(kv);
     void* args[] = {&c};
     const cudaError_t e = launch_dependent((const void*)kv_compact_kernel, 1, CT, 0, kv->stream, args);
-    return e == cudaSuccess ? launch_copy(kv, true) : e;
+    return e == cudaSuccess ? launch_copy(kv, true, kv->n_pages) : e;
 }
