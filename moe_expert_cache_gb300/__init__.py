@@ -304,12 +304,14 @@ def kv_destroy(kv) -> None:
 
 def _ptr(a) -> int | None:
     """Address of a numpy array / torch tensor / int; None for None."""
+    try:
+        return a.data_ptr()
+    except AttributeError:
+        pass
     if a is None:
         return None
     if isinstance(a, int):
         return a
-    if hasattr(a, "data_ptr"):
-        return a.data_ptr()
     if hasattr(a, "ctypes"):
         return a.ctypes.data
     raise TypeError(type(a))
@@ -455,7 +457,7 @@ class KvCache:
         st, h = kv_init(L, Hq, Hkv, D, page, n_pages, n_rows, row_pages, dtype, T_max, B_max, _ptr(pool), _ptr(table),
                         _ptr(lens), _ptr(refs), stream or None)
         _check(st, "ft_kv_init")
-        self.h = h
+        self.h, self._lib = h, load()
         self._keep = (pool, table, lens, refs)
 
     def close(self):
@@ -470,29 +472,42 @@ class KvCache:
             pass
 
     def extend(self, n, rows, add):
-        _check(kv_extend(self.h, n, _ptr(rows), _ptr(add)), "ft_kv_extend")
+        st = self._lib.ft_kv_extend(self.h, n, _ptr(rows), _ptr(add))
+        if st:
+            _check(st, "ft_kv_extend")
 
     def fork(self, n, parents, children):
-        _check(kv_fork(self.h, n, _ptr(parents), _ptr(children)), "ft_kv_fork")
+        st = self._lib.ft_kv_fork(self.h, n, _ptr(parents), _ptr(children))
+        if st:
+            _check(st, "ft_kv_fork")
 
     def free(self, n, rows):
-        _check(kv_free(self.h, n, _ptr(rows)), "ft_kv_free")
+        st = self._lib.ft_kv_free(self.h, n, _ptr(rows))
+        if st:
+            _check(st, "ft_kv_free")
 
     def compact(self):
-        _check(kv_compact(self.h), "ft_kv_compact")
+        st = self._lib.ft_kv_compact(self.h)
+        if st:
+            _check(st, "ft_kv_compact")
 
     def qk_rope_store(self, layer, T, qkv, ld, row_of, pos, q_out, ld_q, *, q_norm=None, k_norm=None, eps=1e-6,
                       cos_sin=None, max_pos=0, rot=0, pair=False):
-        _check(qk_rope_store(self.h, layer, T, _ptr(qkv), ld, _ptr(row_of), _ptr(pos), _ptr(q_out), ld_q, _ptr(q_norm),
-                             _ptr(k_norm), eps, _ptr(cos_sin), max_pos, rot, 1 if pair else 0), "ft_qk_rope_store")
+        st = self._lib.ft_qk_rope_store(self.h, layer, T, _ptr(qkv), ld, _ptr(row_of), _ptr(pos), _ptr(q_out), ld_q,
+                                        _ptr(q_norm), _ptr(k_norm), eps, _ptr(cos_sin), max_pos, rot, 1 if pair else 0)
+        if st:
+            _check(st, "ft_qk_rope_store")
 
     def attn_plan(self, B, T, cu_q, *, rows=None, n_groups=0, group_start=None, group_tokens=None):
         """Lay out the work of a step from the lengths on the stream now; every layer's attn_forward uses it."""
-        _check(attn_plan(self.h, B, T, _ptr(cu_q), _ptr(rows), n_groups, _ptr(group_start), _ptr(group_tokens)),
-               "ft_attn_plan")
+        st = self._lib.ft_attn_plan(self.h, B, T, _ptr(cu_q), _ptr(rows), n_groups, _ptr(group_start), _ptr(group_tokens))
+        if st:
+            _check(st, "ft_attn_plan")
 
     def attn_forward(self, layer, q, ld_q, out, ld_o, scale):
-        _check(attn_forward(self.h, layer, _ptr(q), ld_q, _ptr(out), ld_o, scale), "ft_attn_forward")
+        st = self._lib.ft_attn_forward(self.h, layer, _ptr(q), ld_q, _ptr(out), ld_o, scale)
+        if st:
+            _check(st, "ft_attn_forward")
 
     def last(self) -> dict:
         """What the last page operation did (syncs)."""

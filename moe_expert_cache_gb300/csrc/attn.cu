@@ -1137,15 +1137,22 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// The kernels of a head size and type.
+struct Kernels {
+    const void *attn, *merge;
+    size_t smem;
+};
 template <int D, bool BF>
-cudaError_t launch_typed(ft_kv* kv, const AttnArgs& a, const AttnPlan& pl) {
-    cudaError_t e = ensure_dynamic_smem((const void*)attn_kernel<D, BF>, Cfg<D>::SMEM);
-    if (e != cudaSuccess) return e;
-    void* args[] = {const_cast<CUtensorMap*>(&kv->map), const_cast<AttnArgs*>(&a)};
-    e = launch_dependent((const void*)attn_kernel<D, BF>, pl.n_cta, G_THREADS, Cfg<D>::SMEM, kv->stream, args);
-    if (e != cudaSuccess) return e;
-    return launch_dependent((const void*)attn_merge_kernel<D, BF>, kv->num_sms * 4, 256, 0, kv->stream, args + 1);
+Kernels kernels() {
+    return Kernels{(const void*)attn_kernel<D, BF>, (const void*)attn_merge_kernel<D, BF>, Cfg<D>::SMEM};
 }
+Kernels kernels_of(const ft_kv* kv) {
+    const bool bf = kv->dtype == FT_KV_BF16;
+    if (kv->D == 64) return bf ? kernels<64, true>() : kernels<64, false>();
+    if (kv->D == 128) return bf ? kernels<128, true>() : kernels<128, false>();
+    return bf ? kernels<256, true>() : kernels<256, false>();
+}
+size_t plan_smem(const ft_kv* kv) { return CUM * 4 + (size_t)kv->plan.n_cta * 16; }
 
 }  // namespace
 
@@ -1183,15 +1190,18 @@ bool attn_encode_map(ft_kv* kv) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+cudaError_t attn_setup(ft_kv* kv) {
+    const Kernels k = kernels_of(kv);
+    const cudaError_t e = ensure_dynamic_smem(k.attn, k.smem);
+    return e == cudaSuccess ? ensure_dynamic_smem((const void*)attn_plan_kernel, plan_smem(kv)) : e;
+}
+
 cudaError_t launch_attn_plan(ft_kv* kv, int B, int T, const int* cu_q, const int* rows, int n_groups,
                              const int* group_start, const int* group_tokens) {
     PlanArgs a{kv->plan, B, T, n_groups, kv->Hq / kv->Hkv, kv->Hkv, kv->page, kv->n_rows, kv->row_pages,
                MERGE_NB(kv->D), kv->num_sms * 24, cu_q, rows, group_start, group_tokens, kv->lens, kv->err};
-    const size_t smem = CUM * 4 + (size_t)kv->plan.n_cta * 16;
-    const cudaError_t e = ensure_dynamic_smem((const void*)attn_plan_kernel, smem);
-    if (e != cudaSuccess) return e;
     void* args[] = {&a};
-    return launch_dependent((const void*)attn_plan_kernel, 1, PT, smem, kv->stream, args);
+    return launch_dependent((const void*)attn_plan_kernel, 1, PT, plan_smem(kv), kv->stream, args);
 }
 
 cudaError_t launch_attn_forward(ft_kv* kv, int layer, const void* q, long long ld_q, void* out, long long ld_o,
@@ -1214,8 +1224,8 @@ cudaError_t launch_attn_forward(ft_kv* kv, int layer, const void* q, long long l
     a.part_o = kv->part_o;
     a.part_ml = kv->part_ml;
     a.err = kv->err;
-    const bool bf = kv->dtype == FT_KV_BF16;
-    if (kv->D == 64) return bf ? launch_typed<64, true>(kv, a, kv->plan) : launch_typed<64, false>(kv, a, kv->plan);
-    if (kv->D == 128) return bf ? launch_typed<128, true>(kv, a, kv->plan) : launch_typed<128, false>(kv, a, kv->plan);
-    return bf ? launch_typed<256, true>(kv, a, kv->plan) : launch_typed<256, false>(kv, a, kv->plan);
+    const Kernels k = kernels_of(kv);
+    void* args[] = {&kv->map, &a};
+    const cudaError_t e = launch_dependent(k.attn, kv->plan.n_cta, G_THREADS, k.smem, kv->stream, args);
+    return e == cudaSuccess ? launch_dependent(k.merge, kv->num_sms * 4, 256, 0, kv->stream, args + 1) : e;
 }

@@ -132,6 +132,7 @@ cudaError_t launch_qk_rope_store(ft_kv* kv, const RopeArgs& a);
 void attn_plan_sizes(int Hq, int Hkv, int D, int T_max, int B_max, int num_sms, AttnPlan& p);
 size_t attn_seg_bytes(const AttnPlan& p);
 bool attn_encode_map(ft_kv* kv);
+cudaError_t attn_setup(ft_kv* kv);  // the kernels' shared-memory limits, once per handle
 cudaError_t launch_attn_plan(ft_kv* kv, int B, int T, const int* cu_q, const int* rows, int n_groups,
                              const int* group_start, const int* group_tokens);
 cudaError_t launch_attn_forward(ft_kv* kv, int layer, const void* q, long long ld_q, void* out, long long ld_o,

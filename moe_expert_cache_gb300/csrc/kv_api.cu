@@ -134,7 +134,7 @@ ft_status ft_kv_init(ft_kv** out, int32_t L, int32_t Hq, int32_t Hkv, int32_t D,
     kv->plan.seg = (int*)(a + l.seg);
     kv->part_o = (float*)(a + l.part_o);
     kv->part_ml = (float2*)(a + l.part_ml);
-    if (!attn_encode_map(kv)) return fail(FT_ERR_CUDA);
+    if (!attn_encode_map(kv) || attn_setup(kv) != cudaSuccess) return fail(FT_ERR_CUDA);
     *out = kv;
     return FT_OK;
 }
