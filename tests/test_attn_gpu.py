@@ -89,6 +89,15 @@ def test_rows_in_any_order_and_many_requests():
     c.check_attend(ns, rows=rows)
 
 
+def test_as_many_requests_as_a_plan_takes():
+    rng = np.random.default_rng(8)
+    lens = [32 + int(x) for x in rng.integers(1, 30, 1024)]
+    c = Cache(lens, D=64, page=16, Hq=2, Hkv=1, T_max=1024, shared=32, seed=8)
+    c.poison(float("nan"))
+    c.check_attend([1] * 1024, groups=([0, 400, 1024], [32, 32]))
+    c.check_attend([1] * 1024)
+
+
 def test_long_axis_split():
     # one request over many CTAs: the join of dozens of pieces, with the largest scores last and first
     for flip in (False, True):

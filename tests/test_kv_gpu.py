@@ -71,6 +71,22 @@ def test_large_pool_takes_the_lowest_free_pages():
     _apply(c, "compact")
 
 
+def test_long_lists():
+    # lists of more rows than a step of the scans; forks of whole and of partial pages, one parent many times
+    rng = np.random.default_rng(4)
+    n = 2600
+    c = Cache([0] * n, D=64, page=16, Hq=1, Hkv=1, n_pages=9000, row_pages=6)
+    a = [int(x) for x in rng.permutation(n)[:1301]]
+    _apply(c, "extend", a, [int(x) for x in rng.integers(0, 60, len(a))])
+    empty = [r for r in range(n) if c.model.lens[r] == 0]
+    held = [r for r in a[:60] if c.model.lens[r]]
+    _apply(c, "fork", [int(rng.choice(held)) if i % 2 else held[7] for i in range(len(empty) - 1)], empty[1:])
+    _apply(c, "extend", list(range(n)), [int(x) for x in rng.integers(0, 20, n)])
+    assert sum(1 for x in c.model.lens if x) > 2400
+    _apply(c, "free", [int(x) for x in rng.permutation(n)[:2001]])
+    _apply(c, "compact")
+
+
 def test_page_refusals_change_nothing():
     c = Cache([40, 0, 16, 0], D=64, page=16, Hq=1, Hkv=1, row_pages=4, spare=1)
     bad = [("extend", [0, 0], [1, 1]), ("extend", [4], [1]), ("extend", [-1], [1]), ("extend", [0], [-1]),
@@ -241,7 +257,8 @@ def test_init_refusals():
     assert st == ft.FT_OK
     ft.kv_destroy(h)
     for i, v in ((0, 0), (1, 3), (1, 0), (1, 516), (2, 0), (3, 96), (3, 32), (4, 8), (4, 256), (5, 0), (6, 0), (7, 0), (8, 2),
-                 (9, 0), (10, 0), (10, 1025), (11, 0), (11, p[0] + 64), (12, 0), (13, p[2] + 2), (14, 0), (7, 1 << 27)):
+                 (9, 0), (10, 0), (10, 1025), (11, 0), (11, p[0] + 64), (12, 0), (13, p[2] + 2), (14, 0), (7, 1 << 27),
+                 (6, 65537)):
         bad = list(good)
         bad[i] = v
         st, h = ft.kv_init(*bad)
