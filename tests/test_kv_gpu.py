@@ -75,7 +75,7 @@ def test_long_lists():
     # lists of more rows than a step of the scans; forks of whole and of partial pages, one parent many times
     rng = np.random.default_rng(4)
     n = 2600
-    c = Cache([0] * n, D=64, page=16, Hq=1, Hkv=1, n_pages=9000, row_pages=6)
+    c = Cache([0] * n, D=64, page=16, Hq=1, Hkv=1, n_pages=9000, row_pages=6, B_max=1)
     a = [int(x) for x in rng.permutation(n)[:1301]]
     _apply(c, "extend", a, [int(x) for x in rng.integers(0, 60, len(a))])
     empty = [r for r in range(n) if c.model.lens[r] == 0]
