@@ -223,6 +223,21 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 16 TMEM lanes x 32 columns.  A quad of threads holds 8 columns of a block of 8 values: r[4*b + e] is column
+// 8*b + 2*(lane % 4) + e of row lane / 4, r[4*b + 2 + e] of row lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// Partial results keep the values of a row's 32-column group in the order in which that load has them in a quad:
+// the 8 values of a thread, 32 bytes, lie together, and a store of a warp fills whole lines of 8 rows instead of a
+// sector of each of 32.  Column of place x (even; x + 1 is the next column):
+__device__ __forceinline__ int part_column(int x) { return (x & ~31) | (x & 6) << 2 | (x >> 2 & 6); }
+
 // 32 bytes to global memory in one store (a whole sector of one row).
 __device__ __forceinline__ void st_global32(void* d, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -336,16 +351,10 @@ __global__ void __launch_bounds__(256, 3) attn_merge_kernel(const AttnArgs p) {
         }
         if (on && share == 0) {
             const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
-            uint16_t* dst = p.out + (long long)tok * p.ld_o + (k.head * p.G + gh) * D + lane * V;
-            uint32_t o[V / 2];
+            uint16_t* dst = p.out + (long long)tok * p.ld_o + (k.head * p.G + gh) * D;
 #pragma unroll
-            for (int j = 0; j < V / 2; ++j) o[j] = pack2<BF>(acc[2 * j] * inv, acc[2 * j + 1] * inv);
-            if (V == 2)
-                *reinterpret_cast<uint32_t*>(dst) = o[0];
-            else if (V == 4)
-                *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1 % (V / 2)]);
-            else
-                *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1 % (V / 2)], o[2 % (V / 2)], o[3 % (V / 2)]);
+            for (int j = 0; j < V; j += 2)
+                *reinterpret_cast<uint32_t*>(dst + part_column(lane * V + j)) = pack2<BF>(acc[j] * inv, acc[j + 1] * inv);
         }
     }
 }
@@ -398,12 +407,21 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     const AttnCta mine0 = p.ctas[blockIdx.x];
     const int w0 = mine0.w0, w1 = mine0.w1;
     auto load_q = [&](const AttnWork& k) {
-        constexpr int CH = D / 8;  // 16-byte chunks of a row
-        for (int i = tid; i < k.nrows * CH; i += 128) {
-            const int rr = i / CH, ch = i % CH;
-            const int R = k.r0 + rr, tok = k.tok0 + R / p.G, gh = k.head * p.G + R % p.G;
-            ft::cp_async16(smQ + (ch >> 3) * (ATTN_BM * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
-                           p.q + (long long)tok * p.ld_q + gh * D + ch * 8);
+        constexpr int CH = D / 8, RS = 128 / CH;  // 16-byte chunks of a row, rows of a step
+        const int ch = tid % CH, rr0 = tid / CH, R = k.r0 + rr0;
+        const int dt = RS / p.G, dg = RS % p.G;   // a step in tokens and heads: no division in the loop
+        int gh = R % p.G;
+        const uint16_t* src = p.q + (long long)(k.tok0 + R / p.G) * p.ld_q + (k.head * p.G + gh) * D + ch * 8;
+        const long long step = dt * p.ld_q + dg * D, wrap = p.ld_q - p.G * D;
+        unsigned char* dst = smQ + (ch >> 3) * (ATTN_BM * 128);
+        for (int rr = rr0; rr < k.nrows; rr += RS) {
+            ft::cp_async16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), src);
+            src += step;
+            gh += dg;
+            if (gh >= p.G) {
+                gh -= p.G;
+                src += wrap;
+            }
         }
     };
     // the first item came with the range for what starts at once (its queries and pages); all arrive by a bulk copy
@@ -735,15 +753,19 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                         }
                     }
                 } else {
-                    float* dst = p.part_o + (size_t)(k.prow + r) * D;
+                    const int r4 = wid * 32 + (lane >> 2);
+                    float* dst = p.part_o + (size_t)(k.prow + r4) * D + (lane & 3) * 8;
 #pragma unroll
                     for (int cc = 0; cc < D; cc += 32) {
                         uint32_t o[32];
-                        tc::tmem_ld32(lane_base + (uint32_t)cc, o);
+                        tmem_ld_quads(lane_base + (uint32_t)cc, o);
+                        tmem_ld_quads(lane_base + (uint32_t)(cc + (16 << 16)), o + 16);
                         tc::tmem_wait_ld(o);
-                        if (in) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8) st_global32(dst + cc + j, o + j);
+                        for (int j = 0; j < 4; ++j) {  // rows r4, + 8, + 16, + 24
+                            const uint32_t* s = o + (j >> 1) * 16 + (j & 1) * 2;
+                            const uint32_t v[8] = {s[0], s[1], s[4], s[5], s[8], s[9], s[12], s[13]};
+                            if (r4 + 8 * j < k.nrows) st_global32(dst + cc + (size_t)(8 * j) * D, v);
                         }
                     }
                     if (in) p.part_ml[k.prow + r] = make_float2(m * p.c, l);
