@@ -24,6 +24,17 @@
 // the tensor core has the other's products.  At 256, where O takes half of
 // TMEM, one CTA with two score buffers.
 //
+// Requests with few rows that share nothing (up to 16 rows each on average, head
+// sizes 128 and 256) run a kernel that takes such items transposed,
+//   S^T = K Q^T, O^T = V^T P^T,
+// so that a softmax thread has a key and its few queries instead of a row and
+// 128 keys: 64 requests of 512 keys 14.8 -> 12.5 us, 76 of 640 17.8 -> 15.1
+// (13.1 -> 12.7 and 15.6 -> 14.8 at 256).  Beside a shared prefix it loses: 64
+// requests behind 8192 keys at equal time, 256 with 64 keys of their own 54 ->
+// 61 us, 6 behind 131072 keys 57 -> 58.5, and a kernel that only has both forms
+// costs the other 2-3%; head size 64, whose products have N = 64 already, 19 ->
+// 24 us.  Hence the rule on what the plan call says.
+//
 // The running maximum is a reference that may fall behind: past an item's first
 // tile the weights are taken on the present one, and only where a tile's weights
 // sum to more than 4096 is the tile done again on its own maximum and O rescaled.
@@ -40,6 +51,8 @@
 // shared tiles (prompts 4% faster, short items 1.6 times slower) or over
 // alternate tiles (the ring could not keep up), rings of half tiles (3% slower),
 // a cooperative launch with the join at its end (launch +2 us).
+#include <type_traits>
+
 #include "ft_kv.cuh"
 #include "ft_tc.cuh"
 
@@ -51,6 +64,7 @@ constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 48;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float MAX_SUM = 4096.f;    // of a tile's weights on a reference that has fallen behind (f16 holds 65504)
 constexpr int MERGE_NB(int D) { return D == 256 ? 4 : 8; }  // pieces that a warp of the join has in flight
+constexpr int NQ = 16;               // items of up to this many rows take the transposed form
 constexpr int NWORK = 16;            // work items of a CTA that are kept in shared memory
 constexpr int OV = 2;                // cost of an item's start, in tiles
 constexpr int OVP = 4;               // the same with the partial result of a prefix item
@@ -138,10 +152,11 @@ __device__ __forceinline__ uint32_t desc_v(const void* tile, uint32_t lead) {
     return (ft::smem_addr(tile) >> 4) | ((lead >> 4) << 16);
 }
 
-// kind::f16 with bf16 (1) or f16 (0) operands, fp32 accumulator; bit 16: B is
-// given with N contiguous.
-constexpr uint32_t idesc_of(bool bf, int N, bool b_mn) {
-    return (1u << 4) | ((bf ? 1u : 0u) << 7) | ((bf ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) |
+// kind::f16 with bf16 (1) or f16 (0) operands, fp32 accumulator; bits 15 and
+// 16: A is given with M, B with N contiguous.
+constexpr uint32_t idesc_of(bool bf, int N, bool a_mn, bool b_mn) {
+    return (1u << 4) | ((bf ? 1u : 0u) << 7) | ((bf ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+           ((b_mn ? 1u : 0u) << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(ATTN_BM >> 4) << 24);
 }
 
@@ -198,6 +213,12 @@ __device__ __forceinline__ void mma_values(uint32_t o, uint32_t pt, uint32_t v, 
     for (int i = 0; i < 4; ++i) mma_ts(o, pt + 8 * i, v + 128 * i, idesc, i ? 1u : accumulate);
 }
 
+// O^T (+)= V^T P^T over 64 keys, 128 values: both operands in shared memory.
+__device__ __forceinline__ void mma_values_t(uint32_t o, uint32_t v, uint32_t pt, uint32_t idesc, uint32_t accumulate) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mma_ss(o, v + 128 * i, pt + 2 * i, idesc, i ? 1u : accumulate);
+}
+
 // A place in the ring and the parity of its phase.
 struct Slot {
     int st = 0;
@@ -221,6 +242,53 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+// 32 lanes x 16 columns: one row a thread.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// x[j] of all lanes by op, for 16 j: each step hands half of the values to the partner.  Lane i gets j = i / 2; x is
+// used up.
+template <class Op>
+__device__ __forceinline__ float warp_columns(float* x, int lane, Op op) {
+#pragma unroll
+    for (int o = 16; o > 1; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int j = 0; j < o / 2; ++j) {
+            const float send = up ? x[j] : x[j + o / 2], keep = up ? x[j + o / 2] : x[j];
+            x[j] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        }
+    }
+    return op(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
+}
+// Whether a predicate holds in any of the four softmax warps, and a barrier for them.
+__device__ __forceinline__ bool any_of_128(bool x) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((int)x)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 16 TMEM lanes x 32 columns.  A quad of threads holds 8 columns of a block of 8 values: r[4*b + e] is column
@@ -235,8 +303,8 @@ __device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, uint32_t* r) {
 }
 // Partial results keep the values of a row's 32-column group in the order in which that load has them in a quad:
 // the 8 values of a thread, 32 bytes, lie together, and a store of a warp fills whole lines of 8 rows instead of a
-// sector of each of 32.  Column of place x (even; x + 1 is the next column):
-__device__ __forceinline__ int part_column(int x) { return (x & ~31) | (x & 6) << 2 | (x >> 2 & 6); }
+// sector of each of 32.  Column of place x, and place of column x:
+__device__ __forceinline__ int part_column(int x) { return (x & ~30) | (x & 6) << 2 | (x >> 2 & 6); }
 
 // 32 bytes to global memory in one store (a whole sector of one row).
 __device__ __forceinline__ void st_global32(void* d, const uint32_t* v) {
@@ -359,7 +427,7 @@ __global__ void __launch_bounds__(256, 3) attn_merge_kernel(const AttnArgs p) {
     }
 }
 
-template <int D, bool BF>
+template <int D, bool BF, bool FEW>
 __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __grid_constant__ CUtensorMap map,
                                                                        const AttnArgs p) {
     using C = Cfg<D>;
@@ -370,7 +438,9 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_fail;
     __shared__ __align__(16) AttnWork s_work[NWORK];
+    __shared__ __align__(16) float s_red[NQ][4];  // transposed form: a value of each query and softmax warp
     unsigned char *ring_k = smQ + C::QBYTES, *ring_v = ring_k + NK * C::STAGE;
+    unsigned char* smP = smQ + 64 * 128;  // transposed form: NS x 4 KB in rows of Q that its items do not have
     const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
 
     if (tid == 128) {
@@ -508,9 +578,10 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
     } else if (wid == 5) {
         // ------------------------------------------------------------ MMA warp
         {
-            constexpr uint32_t id_s = idesc_of(BF, ATTN_BN, false), id_o = idesc_of(BF, D, true);
+            constexpr uint32_t id_s = idesc_of(BF, ATTN_BN, false, false), id_o = idesc_of(BF, D, false, true);
+            constexpr uint32_t id_st = idesc_of(BF, NQ, false, false), id_ot = idesc_of(BF, NQ, true, false);
             constexpr int H = C::HALVES;
-            const uint32_t kdesc = desc_k(ring_k), vdesc = desc_v(ring_v, ATTN_BN / H * 128), qdesc = desc_k(smQ);
+            const uint32_t pdesc = desc_k(smP), kdesc = desc_k(ring_k), vdesc = desc_v(ring_v, ATTN_BN / H * 128), qdesc = desc_k(smQ);
             constexpr uint32_t SW = C::STAGE / 16, QW = (D / 64) / H * (ATTN_BM * 128 / 16);
             int g = 0, n = 0;
             Slot rk, rv;
@@ -523,41 +594,50 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                 mma_commit(&v_empty[rv.st]);
                 advance<NV>(rv);
             };
-            auto scores = [&]() {  // S = Q K^T with the next tile of the ring
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    wait(&k_full[rk.st], rk.ph);
-                    tc::fence_after_sync();
-                    mma_scores<(D / 64) / H>(tmem + (uint32_t)(D + sc.st * ATTN_BN), qdesc + h * QW, kdesc + rk.st * SW, id_s,
-                                             h ? 1u : 0u);
-                    if (h == H - 1) mma_commit(&s_full[sc.st]);
-                    mma_commit(&k_empty[rk.st]);
-                    advance<NK>(rk);
-                }
-                advance<NS>(sc);
-            };
             int sb = 0;
-            if (nw > 0) wait(&w_full, 0);
-            for (int w = w0; w < w1 && ok && !__any_sync(0xffffffffu, s_fail); ++w, ++n) {
-                const AttnWork k = work(w);
+            // an item; the two forms have loops of their own, so that neither's operands are selected at run time
+            auto item = [&](const AttnWork& k, auto form) {
+                constexpr bool few = decltype(form)::value;
                 const int nt = k.ntile, keys = k.kend - k.pos0;
+                auto scores = [&]() {  // S = Q K^T, or S^T = K Q^T, with the next tile of the ring
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        wait(&k_full[rk.st], rk.ph);
+                        tc::fence_after_sync();
+                        const uint32_t s = tmem + (uint32_t)(D + sc.st * ATTN_BN), kd = kdesc + rk.st * SW, qd = qdesc + h * QW;
+                        mma_scores<(D / 64) / H>(s, few ? kd : qd, few ? qd : kd, few ? id_st : id_s, h ? 1u : 0u);
+                        if (h == H - 1) mma_commit(&s_full[sc.st]);
+                        mma_commit(&k_empty[rk.st]);
+                        advance<NK>(rk);
+                    }
+                    advance<NS>(sc);
+                };
+                auto values = [&](int half, uint32_t v, uint32_t accumulate) {
+                    if (few) {
+#pragma unroll
+                        for (int d = 0; d < D; d += 128)
+                            mma_values_t(tmem + (uint32_t)(d / 128 * NQ), v + d / 64 * (ATTN_BN / H * 128 / 16),
+                                         pdesc + (uint32_t)(sb * 256 + half * 128), id_ot, accumulate);
+                    } else {
+                        mma_values(tmem, tmem + (uint32_t)(D + sb * ATTN_BN + 32 * half), v, id_o, accumulate);
+                    }
+                };
                 wait(&q_full, n);
                 scores();
                 for (int i = 0; i < nt && ok; ++i, ++g) {
                     if (NS == 2 && i + 1 < nt) scores();
                     if (i == 0 && n > 0) wait(&o_empty, n - 1);
                     wait(&v_full[rv.st], rv.ph);
-                    const uint32_t pt = tmem + (uint32_t)(D + sb * ATTN_BN);
                     wait(&p_full[sb], g / NS);
                     tc::fence_after_sync();
-                    mma_values(tmem, pt, vdesc + rv.st * SW, id_o, i ? 1u : 0u);
+                    values(0, vdesc + rv.st * SW, i ? 1u : 0u);
                     if (keys - i * ATTN_BN > 64) {
                         if (H == 2) {
                             release_v();
                             wait(&v_full[rv.st], rv.ph);
                             tc::fence_after_sync();
                         }
-                        mma_values(tmem, pt + 32, vdesc + rv.st * SW + (H == 2 ? 0 : 512), id_o, 1u);
+                        values(1, vdesc + rv.st * SW + (H == 2 ? 0 : 512), 1u);
                     }
                     release_v();
                     if (NS == 2) mma_commit(&pv_done[g & 1]);
@@ -565,6 +645,14 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                     if (NS == 2) sb ^= 1;
                     if (NS == 1 && i + 1 < nt) scores();
                 }
+            };
+            if (nw > 0) wait(&w_full, 0);
+            for (int w = w0; w < w1 && ok && !__any_sync(0xffffffffu, s_fail); ++w, ++n) {
+                const AttnWork k = work(w);
+                if (FEW && k.nrows <= NQ)
+                    item(k, std::true_type());
+                else
+                    item(k, std::false_type());
             }
             if (!ok) s_fail = 1;
             mma_commit(&done);
@@ -589,13 +677,202 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
         };
         int g = 0, it0 = 0, n = 0;
         bool ok = true;
+        // what the pool holds past the keys of a tile may be anything: its weights are 0, its values are made 0
+        auto clear_values = [&](int valid, int i) {
+            if (valid >= ATTN_BN || (H == 2 && valid == 64)) return;
+            const bool two = valid > 64;
+            const int vit = it0 + H * i + (H == 2 && two), st = vit % NV;
+            if (!wait(&v_full[st], vit / NV)) ok = false;
+            unsigned char* vt = ring_v + (size_t)st * C::STAGE;
+            // rows of this stage (of 64 keys, or of the whole tile) that hold no key
+            const int z0 = max(H == 2 && two ? valid - 64 : valid, 0), nz = ((H == 1 && two ? ATTN_BN : 64) - z0) * 8;
+            for (int x = tid; x < nz * (D / 64); x += 128) {
+                const int b = x / nz, y = x % nz;
+                *reinterpret_cast<uint4*>(vt + b * (ATTN_BN / H * 128) + z0 * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        };
+        auto next_item = [&](const AttnWork& k) {
+            it0 += H * k.ntile - (H == 2 && k.kend - (k.pos0 + (k.ntile - 1) * ATTN_BN) <= 64);
+        };
+        // The transposed form, for few rows: a thread has a key, its scores with all the queries, their weights on
+        // a reference of each query that the four warps agree on: the score of the item's first key, as long as no
+        // weight on it is larger than MAX_SUM.
+        auto few_rows = [&](const AttnWork& k, int w) {
+            int t = r;
+            asm volatile("" : "+r"(t));  // what follows from t stays in here: the other form needs the registers
+            float ref[NQ], l[NQ], x[NQ];  // reference of the weights (0: no key seen yet), sums of this thread's keys
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) l[j] = ref[j] = 0.f;
+            const uint32_t rows = (1u << k.nrows) - 1;
+            const bool more = w + 1 < w1;
+            unsigned unseen = 0;  // queries whose first key scored -inf
+            bool held = false;    // the next item's queries have to wait for the last product: they lie over its weights
+            for (int i = 0; i < k.ntile; ++i, ++g) {
+                if (!wait(&s_full[g % NS], g / NS)) ok = false;
+                tc::fence_after_sync();
+                tmem_ld16(lane_base + (uint32_t)(D + (g % NS) * ATTN_BN), reinterpret_cast<uint32_t*>(x));
+                if (i == k.ntile - 1 && more) {
+                    held = work(w + 1).nrows > 64;
+                    if (!held) load_q(work(w + 1));
+                }
+                const int pos = k.pos0 + i * ATTN_BN + t;
+                // the queries that see this key: all but those of tokens that it is behind
+                const int past = k.vis0 == ATTN_NOMASK ? 0 : pos - k.vis0 + 1;
+                const uint32_t vis = pos >= k.kend ? 0u : past <= 0 ? rows : rows & (0xffffffffu << min(max(past * p.G - k.r0, 0), 31));
+                if (i == 0) {
+                    if (t == 0) {
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j) s_red[j >> 2][j & 3] = vis >> j & 1 ? x[j] * p.c : 0.f;
+                    }
+                    if (any_of_128(!ok)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int j = 0; j < NQ; j += 4) *reinterpret_cast<float4*>(ref + j) = *reinterpret_cast<const float4*>(s_red[j >> 2]);
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) {
+                        if (ref[j] == -INFINITY) {
+                            unseen |= 1u << j;
+                            ref[j] = 0.f;
+                        }
+                    }
+                }
+                float e[NQ], top = 0.f;
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    const float y = ex2(fmaf(x[j], p.c, -ref[j]));
+                    e[j] = vis >> j & 1 ? y : 0.f;
+                    top = fmaxf(top, e[j]);
+                }
+                if (any_of_128(top > MAX_SUM || (unseen & vis) || !ok)) {
+                    // the maxima of the queries over the tile
+                    float y[NQ];
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) y[j] = x[j] = vis >> j & 1 ? x[j] * p.c : -INFINITY;
+                    const float m1 = warp_columns(y, t & 31, [](float a, float b) { return fmaxf(a, b); });
+                    if (!(t & 1)) s_red[(t & 31) >> 1][wid] = m1;
+                    if (any_of_128(!ok)) {
+                        ok = false;
+                        break;
+                    }
+                    if (i > 0) {
+                        if (NS == 2 && !wait(&pv_done[(g - 1) & 1], (g - 1) >> 1)) ok = false;
+                        tc::fence_after_sync();
+                    }
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) {
+                        const float4 m4 = *reinterpret_cast<const float4*>(s_red[j]);
+                        const float m = max3(fmaxf(m4.x, m4.y), m4.z, m4.w);
+                        const bool first = unseen >> j & 1;
+                        if (m != -INFINITY) unseen &= ~(1u << j);
+                        const float now = first ? (m == -INFINITY ? 0.f : m) : fmaxf(m, ref[j]);
+                        y[j] = first ? 1.f : ex2(ref[j] - now);
+                        ref[j] = now;
+                        l[j] *= y[j];
+                        e[j] = ex2(x[j] - now);
+                    }
+                    any_of_128(false);  // s_red is read
+                    if (i > 0) {
+#pragma unroll
+                        for (int d = 0; d < D; d += 128) {
+                            uint32_t o[NQ];
+                            tmem_ld16(lane_base + (uint32_t)(d / 128 * NQ), o);
+#pragma unroll
+                            for (int j = 0; j < NQ; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * y[j]);
+                            tmem_st16(lane_base + (uint32_t)(d / 128 * NQ), o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // P^T: 16 rows of 64 keys, 128 bytes each with the swizzle, a half of the tile after the other
+                const uint32_t pt = ft::smem_addr(smP) + (g % NS) * 4096 + (t >> 6) * 2048 + (t & 63) * 2;
+#pragma unroll
+                for (int j = 0; j < NQ; j += 2) {
+                    const uint32_t v = pack2<BF>(e[j], e[j + 1]);
+                    l[j] += e[j];
+                    l[j + 1] += e[j + 1];
+                    st_shared16((pt ^ ((j & 7) << 4)) + j * 128, v);
+                    st_shared16((pt ^ (((j + 1) & 7) << 4)) + (j + 1) * 128, v >> 16);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                clear_values(k.kend - (pos - t), i);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ft::mbar_arrive(&p_full[g % NS]);
+            }
+            if (more && !held) publish_q();
+            const float sum1 = warp_columns(l, t & 31, [](float a, float b) { return a + b; });
+            if (!(t & 1)) s_red[(t & 31) >> 1][wid] = sum1;
+            if (any_of_128(!ok)) {
+                ok = false;
+                return;
+            }
+            if (!wait(&o_full, n)) {
+                ok = false;
+                return;
+            }
+            tc::fence_after_sync();
+            if (more && held) {
+                load_q(work(w + 1));
+                publish_q();
+            }
+            const float4 s4 = *reinterpret_cast<const float4*>(s_red[t & 15]);
+            const float sum = (s4.x + s4.y) + (s4.z + s4.w);  // of query lane % 16
+            const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+#pragma unroll
+            for (int d = 0; d < D; d += 128) {
+                tmem_ld16(lane_base + (uint32_t)(d / 128 * NQ), reinterpret_cast<uint32_t*>(x));
+                if (k.prow < 0) {
+                    int gh = k.r0 % p.G;
+                    uint16_t* dst = p.out + (long long)(k.tok0 + k.r0 / p.G) * p.ld_o + (k.head * p.G + gh) * D + d + t;
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) {
+                        const float f = __shfl_sync(0xffffffffu, inv, j);
+                        if (j < k.nrows) *dst = (uint16_t)pack2<BF>(x[j] * f, 0.f);
+                        dst += D;
+                        if (++gh == p.G) {
+                            gh = 0;
+                            dst += p.ld_o - p.G * D;
+                        }
+                    }
+                } else {
+                    float* dst = p.part_o + (size_t)k.prow * D + part_column(d + t);
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j)
+                        if (j < k.nrows) dst[j * D] = x[j];
+                }
+            }
+            if (k.prow >= 0) {
+                float mine = ref[0];
+#pragma unroll
+                for (int j = 1; j < NQ; ++j) mine = t == j ? ref[j] : mine;
+                if (t < k.nrows) p.part_ml[k.prow + t] = make_float2(sum == 0.f ? -INFINITY : mine, sum);
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) ft::mbar_arrive(&o_empty);
+            next_item(k);
+        };
         if (w0 < w1) {
             load_q(mine0.first);
             publish_q();
             ok = wait(&w_full, 0);
         }
-        for (int w = w0; w < w1 && ok && !__any_sync(0xffffffffu, s_fail); ++w, ++n) {
+        for (int w = w0; w < w1; ++w, ++n) {
+            // the transposed form's barriers have no time limit: there the four warps go on or stop together
+            if (FEW ? any_of_128(!ok || s_fail) : !ok || __any_sync(0xffffffffu, s_fail)) {
+                ok = false;
+                break;
+            }
             const AttnWork k = work(w);
+            if constexpr (FEW) {
+                if (k.nrows <= NQ) {
+                    few_rows(k, w);
+                    continue;
+                }
+            }
             const bool rows_here = wid * 32 < k.nrows;
             const int tok = (k.r0 + min(r, k.nrows - 1)) / p.G;
             const int lim = min(k.kend, k.vis0 == ATTN_NOMASK ? k.kend : k.vis0 + tok);  // this row sees positions < lim
@@ -660,7 +937,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                             lt += weights(1);
                         }
                         // (lanes past the rows hold anything)
-                        exact = __any_sync(0xffffffffu, r < k.nrows && lt > MAX_SUM);
+                        exact = __any_sync(0xffffffffu, r < k.nrows && (lt > MAX_SUM || m == -INFINITY));
                         if (exact) load(0);
                     }
                     if (exact) {
@@ -678,7 +955,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                         if (i == 0) {
                             m = mn;
                         } else {
-                            const bool lag = r < k.nrows && lt > MAX_SUM;
+                            const bool lag = r < k.nrows && (lt > MAX_SUM || m == -INFINITY) && mn > m;
                             // with one S the scores' own barrier has told that the product before them is done
                             if (NS == 2 && !wait(&pv_done[(g - 1) & 1], (g - 1) >> 1)) ok = false;
                             tc::fence_after_sync();
@@ -703,29 +980,17 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                     tmem_st32(sa, s);
                     if (two) tmem_st32(sa + 32, s + 64);
                 }
-                if (valid < ATTN_BN && (H == 1 || valid != 64)) {
-                    // what the pool holds past the keys may be anything: its weights are 0, its values are made 0
-                    const int vit = it0 + H * i + (H == 2 && two), st = vit % NV;
-                    if (!wait(&v_full[st], vit / NV)) ok = false;
-                    unsigned char* vt = ring_v + (size_t)st * C::STAGE;
-                    // rows of this stage (of 64 keys, or of the whole tile) that hold no key
-                    const int z0 = max(H == 2 && two ? valid - 64 : valid, 0), nz = ((H == 1 && two ? ATTN_BN : 64) - z0) * 8;
-                    for (int x = tid; x < nz * (D / 64); x += 128) {
-                        const int b = x / nz, y = x % nz;
-                        *reinterpret_cast<uint4*>(vt + b * (ATTN_BN / H * 128) + z0 * 128 + y * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                }
+                clear_values(valid, i);
                 if (rows_here) tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) ft::mbar_arrive(&p_full[g % NS]);
             }
-            if (!ok) break;
+            if (!ok) continue;
             if (w + 1 < w1) publish_q();
             if (!wait(&o_full, n)) {
                 ok = false;
-                break;
+                continue;
             }
             tc::fence_after_sync();
             if (rows_here) {
@@ -774,7 +1039,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) ft::mbar_arrive(&o_empty);
-            it0 += H * k.ntile - (H == 2 && k.kend - (k.pos0 + (k.ntile - 1) * ATTN_BN) <= 64);
+            next_item(k);
         }
         if (!ok) s_fail = 1;
         ft::cp_async_wait_all();
@@ -1168,12 +1433,13 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
 
 // The kernels of a head size and type.
 struct Kernels {
-    const void *attn, *merge;
+    const void *attn, *attn_few, *merge;
     size_t smem;
 };
 template <int D, bool BF>
 Kernels kernels() {
-    return Kernels{(const void*)attn_kernel<D, BF>, (const void*)attn_merge_kernel<D, BF>, Cfg<D>::SMEM};
+    return Kernels{(const void*)attn_kernel<D, BF, false>, (const void*)attn_kernel<D, BF, D != 64>,
+                   (const void*)attn_merge_kernel<D, BF>, Cfg<D>::SMEM};
 }
 Kernels kernels_of(const ft_kv* kv) {
     const bool bf = kv->dtype == FT_KV_BF16;
@@ -1221,12 +1487,14 @@ bool attn_encode_map(ft_kv* kv) {
 
 cudaError_t attn_setup(ft_kv* kv) {
     const Kernels k = kernels_of(kv);
-    const cudaError_t e = ensure_dynamic_smem(k.attn, k.smem);
+    cudaError_t e = ensure_dynamic_smem(k.attn, k.smem);
+    if (e == cudaSuccess) e = ensure_dynamic_smem(k.attn_few, k.smem);
     return e == cudaSuccess ? ensure_dynamic_smem((const void*)attn_plan_kernel, plan_smem(kv)) : e;
 }
 
 cudaError_t launch_attn_plan(ft_kv* kv, int B, int T, const int* cu_q, const int* rows, int n_groups,
                              const int* group_start, const int* group_tokens) {
+    kv->few_rows = n_groups == 0 && (long long)T * (kv->Hq / kv->Hkv) <= (long long)NQ * B;
     PlanArgs a{kv->plan, B, T, n_groups, kv->Hq / kv->Hkv, kv->Hkv, kv->page, kv->n_rows, kv->row_pages,
                MERGE_NB(kv->D), kv->num_sms * 24, kv->plan.n_cta / kv->num_sms, cu_q, rows, group_start, group_tokens, kv->lens, kv->err};
     void* args[] = {&a};
@@ -1255,6 +1523,6 @@ cudaError_t launch_attn_forward(ft_kv* kv, int layer, const void* q, long long l
     a.err = kv->err;
     const Kernels k = kernels_of(kv);
     void* args[] = {&kv->map, &a};
-    const cudaError_t e = launch_dependent(k.attn, kv->plan.n_cta, G_THREADS, k.smem, kv->stream, args);
+    const cudaError_t e = launch_dependent(kv->few_rows ? k.attn_few : k.attn, kv->plan.n_cta, G_THREADS, k.smem, kv->stream, args);
     return e == cudaSuccess ? launch_dependent(k.merge, kv->num_sms * 4, 256, 0, kv->stream, args + 1) : e;
 }

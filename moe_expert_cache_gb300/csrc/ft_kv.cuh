@@ -35,7 +35,7 @@ struct KvCopy {
 constexpr int ATTN_BM = 128;        // rows of a work item (TMEM lanes)
 constexpr int ATTN_BN = 128;        // keys of a tile
 constexpr int ATTN_MAX_B = 1024;    // requests of a plan (one thread each)
-constexpr int ATTN_NOMASK = 1 << 30;
+constexpr int ATTN_NOMASK = 0x7fffffff;
 
 struct __align__(16) AttnWork {
     int head;     // key/value head
@@ -104,6 +104,7 @@ struct ft_kv {
     float* part_o;     // [part_rows, D] unnormalised partial outputs
     float2* part_ml;   // [part_rows] running maximum (log2 units) and sum
     bool have_plan;
+    bool few_rows;     // the plan's requests have few rows each on average and share nothing
     int plan_T;
     CUtensorMap map;   // [n_pages*L*2*Hkv][page][D] of the pool
 };

@@ -98,6 +98,43 @@ def test_as_many_requests_as_a_plan_takes():
     c.check_attend([1] * 1024)
 
 
+@pytest.mark.parametrize("D,page,kind,Hq,Hkv", [(128, 64, "bf16", 8, 2), (128, 16, "f16", 9, 3), (256, 32, "bf16", 16, 1),
+                                                (256, 128, "f16", 4, 4)])
+def test_requests_of_few_rows_and_some_of_many(D, page, kind, Hq, Hkv):
+    # ungrouped requests of one token or a few, several tokens' causal edge inside a tile, rows without a key, and
+    # now and then one of many rows between them
+    rng = np.random.default_rng(D + page)
+    B = 400 // Hkv
+    lens = [int(x) for x in rng.integers(0, 400, B)]
+    ns = [int(x) for x in rng.integers(0, 3, B)]
+    most = 16 * Hkv // Hq
+    for i in range(0, B, 9):
+        ns[i], lens[i] = most + 1, lens[i] + most  # just too many rows
+    for i in range(5, B, 37):
+        ns[i], lens[i] = 100 * Hkv // Hq, lens[i] + 60
+    while sum(ns) * (Hq // Hkv) > 16 * B:
+        ns[int(rng.integers(0, B))] = 0
+    c = Cache(lens, D=D, page=page, Hq=Hq, Hkv=Hkv, kind=kind, T_max=sum(ns), seed=D)
+    c.poison(float("nan"))
+    c.check_attend(ns)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 9])
+def test_keys_of_minus_infinity_and_growing_scores(D, n):
+    # the first key, or all of the first tile's, score -inf; after them scores that grow from tile to tile
+    for dead in (1, 130):
+        c = Cache([700], D=D, page=64, Hq=4, Hkv=1, T_max=16)
+        t = c.torch.arange(700, device="cuda")
+        pg = c.table[0].long()[t // 64]
+        up = c.torch.linspace(0.05, 4.0, 700, device="cuda")[:, None]
+        c.pool[pg, 0, 0, 0, t % 64] = (c.pool[pg, 0, 0, 0, t % 64].float() * up).to(c.dt)
+        c.pool[pg[:dead], 0, 0, 0, t[:dead] % 64, 0] = float("-inf")
+        q = c.randn(n, 4 * D, scale=1.5)
+        q.view(n, 4, D)[:, :, 0] = 1.0
+        c.check_attend([n], q=q)
+
+
 def test_long_axis_split():
     # one request over many CTAs: the join of dozens of pieces, with the largest scores last and first
     for flip in (False, True):
