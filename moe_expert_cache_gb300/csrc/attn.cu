@@ -63,7 +63,11 @@ constexpr int G_THREADS = 256;        // 4 softmax warps, two TMA warps, an MMA 
 constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 48;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float MAX_SUM = 4096.f;    // of a tile's weights on a reference that has fallen behind (f16 holds 65504)
-constexpr int MERGE_NB(int D) { return D == 256 ? 4 : 8; }  // pieces that a warp of the join has in flight
+// pieces that a warp of the join has in flight, and the join's CTAs on an SM.  More pieces need registers that the
+// loads' addresses want (64 requests behind 8192 keys at head size 128: 6 pieces 28.6 us, 12 30.1, 16 31.3; with 3 CTAs
+// an SM 30.5; 130 behind 16384 at 256, 2 CTAs: 4 pieces 58.7 us, 6 58.1, 8 58.9, 4 with 3 CTAs 61.8)
+constexpr int MERGE_NB(int D) { return D == 64 ? 8 : 6; }
+constexpr int MERGE_CTAS(int D) { return D == 64 ? 3 : 2; }
 constexpr int NQ = 16;               // items of up to this many rows take the transposed form
 constexpr int NWORK = 16;            // work items of a CTA that are kept in shared memory
 constexpr int OV = 2;                // cost of an item's start, in tiles
@@ -324,7 +328,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // order of the sums.  Rows with many pieces (a long sequence has one per CTA
 // that worked on it) have several warps, which share the pieces.
 template <int D, bool BF>
-__global__ void __launch_bounds__(256, 3) attn_merge_kernel(const AttnArgs p) {
+__global__ void __launch_bounds__(256, MERGE_CTAS(D)) attn_merge_kernel(const AttnArgs p) {
     constexpr int V = D / 32, NB = MERGE_NB(D);
     __shared__ float s_acc[8 * D];
     __shared__ float2 s_md[8];
@@ -1496,7 +1500,7 @@ cudaError_t launch_attn_plan(ft_kv* kv, int B, int T, const int* cu_q, const int
                              const int* group_start, const int* group_tokens) {
     kv->few_rows = n_groups == 0 && (long long)T * (kv->Hq / kv->Hkv) <= (long long)NQ * B;
     PlanArgs a{kv->plan, B, T, n_groups, kv->Hq / kv->Hkv, kv->Hkv, kv->page, kv->n_rows, kv->row_pages,
-               MERGE_NB(kv->D), kv->num_sms * 24, kv->plan.n_cta / kv->num_sms, cu_q, rows, group_start, group_tokens, kv->lens, kv->err};
+               MERGE_NB(kv->D), kv->num_sms * 8 * MERGE_CTAS(kv->D), kv->plan.n_cta / kv->num_sms, cu_q, rows, group_start, group_tokens, kv->lens, kv->err};
     void* args[] = {&a};
     return launch_dependent((const void*)attn_plan_kernel, 1, PT, plan_smem(kv), kv->stream, args);
 }
