@@ -71,7 +71,7 @@ constexpr int MERGE_CTAS(int D) { return D == 64 ? 3 : 2; }
 constexpr int NQ = 16;               // items of up to this many rows take the transposed form
 constexpr int NWORK = 16;            // work items of a CTA that are kept in shared memory
 constexpr int OV = 2;                // cost of an item's start, in tiles
-constexpr int OVP = 4;               // the same with the partial result of a prefix item
+constexpr int OVP = 3;               // the same with the partial result of a prefix item
 
 template <int D>
 struct Cfg {

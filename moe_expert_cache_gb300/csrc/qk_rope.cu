@@ -13,6 +13,11 @@
 // token, y = (x r) C + (partner r) S with r = rsqrt(...), and kept in registers
 // over all the heads of one kind that the warp works on; the arithmetic runs two
 // values an instruction.
+//
+// Measured: 8191 tokens of 32 + 2*4 heads of 128, 33.7 us, 5.1 TB/s (75% of the
+// copy rate; DRAM sees 86 MB in and 33 MB out, the rest of the writes stays in
+// L2); one token 2.4 us, the latency of three dependent reads (token, page,
+// values) and a launch.
 #include "ft_kv.cuh"
 
 namespace {
@@ -84,7 +89,9 @@ __device__ __forceinline__ uint4 pack8(const f32x2* f) {
     return v;
 }
 
-constexpr int U = 3;  // heads whose loads a lane has in flight
+// heads whose loads a lane has in flight, at 128 threads and 4 CTAs an SM (8191 tokens: 33.7 us; 2 at 256 threads 35.8,
+// 4 46.4, whose registers spill)
+constexpr int U = 3;
 
 template <int D, bool BF, bool PAIR>
 __global__ void __launch_bounds__(128, 4) qk_rope_store_kernel(const RopeParams p) {
