@@ -20,6 +20,8 @@ Modules:
               conversion.
   fp8      -- E4M3 decoding of block-FP8 records (fp32 scale per 128 x 128
               block) and the block quantiser.
+  kv       -- the paged key/value cache (extend, fork, free, compact), the norm
+              and rotation of heads, causal attention.
 
 Readings of the pages that these modules take where the pages are silent are
 listed in each function's docstring.  Parity unpinned: none of the functions
