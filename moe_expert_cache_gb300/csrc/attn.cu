@@ -1118,7 +1118,8 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
     __shared__ int g_min[PT], g_rows[PT], g_solo[PT], g_first[PT];               // per group
     __shared__ int q_g[PT / 2], q_off[PT / 2];  // per group taken together (it has two requests at least)
     __shared__ int ws[33];
-    __shared__ int s_c, s_iph;
+    __shared__ long long s_end[5];  // per choice of the chunk: when the last CTA ends
+    __shared__ int s_c[5], s_iph;
     extern __shared__ __align__(16) int s_cum[];                   // [CUM]
     int4* s_cta = reinterpret_cast<int4*>(s_cum + CUM);            // [n_cta] first item, first and last segment
     ft::grid_dep_launch();
@@ -1217,44 +1218,41 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         cost += total;
     }
     const long long S = (long long)cost * p.Hkv;
-    if (wid == 0) {
-        int best_c = 1;
-        long long best = 0x7fffffffffffffffll;
-        if (n_pre > 0) {
-            int rts = 0, mt = 1;
-            for (int i = lane; i < n_pre; i += 32) {
-                rts += cdiv(g_rows[q_g[i]], ATTN_BM);
-                mt = max(mt, cdiv(g_min[q_g[i]], ATTN_BN));
-            }
-            rts = __reduce_add_sync(0xffffffffu, rts);
-            mt = __reduce_max_sync(0xffffffffu, mt);
-            auto items = [&](int c) {
-                int x = 0;
-                for (int i = lane; i < n_pre; i += 32)
-                    x += cdiv(g_rows[q_g[i]], ATTN_BM) * cdiv(cdiv(g_min[q_g[i]], ATTN_BN), c);
-                return (int)__reduce_add_sync(0xffffffffu, x) * p.Hkv;
-            };
-            // a half or a quarter of the CTAs, the rest left to the other work, or up to four rounds over all
-            for (int rounds = 1; rounds <= 16; rounds *= 2) {
-                const int cap = max(rounds * n_cta / 4, rts * p.Hkv);
-                int lo = 1, hi = mt;  // smallest c with items(c) <= cap
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (items(mid) <= cap) hi = mid; else lo = mid + 1;
-                }
-                const int ni = items(lo);
-                const long long each = lo + OVP;
-                const long long end = max((S + ni * each + n_cta - 1) / n_cta, (long long)cdiv(ni, n_cta) * each);
-                if (end < best) {
-                    best = end;
-                    best_c = lo;
-                }
-            }
+    // a half or a quarter of the CTAs, the rest left to the other work, or up to four rounds over all: a warp each
+    if (wid < 5 && n_pre > 0) {
+        int rts = 0, mt = 1;
+        for (int i = lane; i < n_pre; i += 32) {
+            rts += cdiv(g_rows[q_g[i]], ATTN_BM);
+            mt = max(mt, cdiv(g_min[q_g[i]], ATTN_BN));
         }
-        if (lane == 0) s_c = best_c;
+        rts = __reduce_add_sync(0xffffffffu, rts);
+        mt = __reduce_max_sync(0xffffffffu, mt);
+        auto items = [&](int c) {
+            int x = 0;
+            for (int i = lane; i < n_pre; i += 32) x += cdiv(g_rows[q_g[i]], ATTN_BM) * cdiv(cdiv(g_min[q_g[i]], ATTN_BN), c);
+            return (int)__reduce_add_sync(0xffffffffu, x) * p.Hkv;
+        };
+        const int cap = max((1 << wid) * n_cta / 4, rts * p.Hkv);
+        int lo = 1, hi = mt;  // smallest c with items(c) <= cap
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (items(mid) <= cap) hi = mid; else lo = mid + 1;
+        }
+        const int ni = items(lo);
+        const long long each = lo + OVP;
+        if (lane == 0) {
+            s_end[wid] = max((S + ni * each + n_cta - 1) / n_cta, (long long)cdiv(ni, n_cta) * each);
+            s_c[wid] = lo;
+        }
     }
     __syncthreads();
-    const int c = s_c;
+    int c = 1;
+    if (n_pre > 0) {
+        int best = 0;
+        for (int i = 1; i < 5; ++i)
+            if (s_end[i] < s_end[best]) best = i;
+        c = s_c[best];
+    }
     {
         int x = 0;
         if (tid < n_pre) x = cdiv(g_rows[q_g[tid]], ATTN_BM) * cdiv(cdiv(g_min[q_g[tid]], ATTN_BN), c);
