@@ -1060,6 +1060,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
 
 constexpr int PT = ATTN_MAX_B;  // threads: one per request
 
+constexpr int CHOICES = PT / 32;  // chunk sizes that are looked at, one a warp
 constexpr int CUM = 2048;       // segments whose running cost is kept in shared memory
 
 struct PlanArgs {
@@ -1118,8 +1119,8 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
     __shared__ int g_min[PT], g_rows[PT], g_solo[PT], g_first[PT];               // per group
     __shared__ int q_g[PT / 2], q_off[PT / 2];  // per group taken together (it has two requests at least)
     __shared__ int ws[33];
-    __shared__ long long s_end[5];  // per choice of the chunk: when the last CTA ends
-    __shared__ int s_c[5], s_iph;
+    __shared__ long long s_end[CHOICES];  // per choice of the chunk: what it costs
+    __shared__ int s_c[CHOICES], s_iph;
     extern __shared__ __align__(16) int s_cum[];                   // [CUM]
     int4* s_cta = reinterpret_cast<int4*>(s_cum + CUM);            // [n_cta] first item, first and last segment
     ft::grid_dep_launch();
@@ -1218,8 +1219,13 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         cost += total;
     }
     const long long S = (long long)cost * p.Hkv;
-    // a half or a quarter of the CTAs, the rest left to the other work, or up to four rounds over all: a warp each
-    if (wid < 5 && n_pre > 0) {
+    // Items for so many sixteenths of the CTAs, the rest left to the other work, up to four rounds over all of them: a
+    // warp looks at each choice.  What it costs, in eighths of a tile's time: the end of an even share or of the longest
+    // chain of prefix items (1.3 times that where an SM has two such CTAs), and the join, 20000 pieces of a row in a
+    // tile's time.  Against the five choices 1/4, 1/2, 1, 2, 4 by the end alone: 64 requests behind 8192 keys 28.1 ->
+    // 26.6 us, with 64 keys of their own at head size 256 22.3 -> 20.5, 130 behind 16384 58.0 -> 56.4, 65 of one head a
+    // row 38.4 -> 36.6; the worst of 24 others 256 behind 8192 at 256, 45.5 -> 47.7.
+    if (n_pre > 0) {
         int rts = 0, mt = 1;
         for (int i = lane; i < n_pre; i += 32) {
             rts += cdiv(g_rows[q_g[i]], ATTN_BM);
@@ -1227,29 +1233,33 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         }
         rts = __reduce_add_sync(0xffffffffu, rts);
         mt = __reduce_max_sync(0xffffffffu, mt);
-        auto items = [&](int c) {
+        auto total = [&](int c, auto rows) {  // of the row tiles, or the rows, times the chunks that they run over
             int x = 0;
-            for (int i = lane; i < n_pre; i += 32) x += cdiv(g_rows[q_g[i]], ATTN_BM) * cdiv(cdiv(g_min[q_g[i]], ATTN_BN), c);
+            for (int i = lane; i < n_pre; i += 32) x += rows(g_rows[q_g[i]]) * cdiv(cdiv(g_min[q_g[i]], ATTN_BN), c);
             return (int)__reduce_add_sync(0xffffffffu, x) * p.Hkv;
         };
-        const int cap = max((1 << wid) * n_cta / 4, rts * p.Hkv);
-        int lo = 1, hi = mt;  // smallest c with items(c) <= cap
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (items(mid) <= cap) hi = mid; else lo = mid + 1;
-        }
-        const int ni = items(lo);
-        const long long each = lo + OVP;
-        if (lane == 0) {
-            s_end[wid] = max((S + ni * each + n_cta - 1) / n_cta, (long long)cdiv(ni, n_cta) * each);
-            s_c[wid] = lo;
+        auto items = [&](int c) { return total(c, [](int r) { return cdiv(r, ATTN_BM); }); };
+        {
+            const int k = wid, cap = max((k < 16 ? k + 1 : 16 + 3 * (k - 15)) * n_cta / 16, rts * p.Hkv);
+            int lo = 1, hi = mt;  // smallest c with items(c) <= cap
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (items(mid) <= cap) hi = mid; else lo = mid + 1;
+            }
+            const int ni = items(lo), pieces = total(lo, [](int r) { return r; });
+            const long long each = lo + OVP, chain = 8 * cdiv(ni, n_cta) * each;
+            const bool beside = p.per_sm == 2 && ni > n_cta / 2 * 17 / 16;
+            if (lane == 0) {
+                s_end[k] = max((S + ni * each) * 8 / n_cta, beside ? chain * 13 / 10 : chain) + pieces / 2500;
+                s_c[k] = lo;
+            }
         }
     }
     __syncthreads();
     int c = 1;
     if (n_pre > 0) {
         int best = 0;
-        for (int i = 1; i < 5; ++i)
+        for (int i = 1; i < CHOICES; ++i)
             if (s_end[i] < s_end[best]) best = i;
         c = s_c[best];
     }
