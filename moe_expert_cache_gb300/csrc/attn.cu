@@ -41,15 +41,16 @@
 // The weights stay as exact (they are floating-point numbers on any scale), no
 // maxima are taken, and almost no tile touches O.
 //
-// What bounds it: few rows, HBM (8 rows over 262144 keys: 537 MB in 88 us with
-// the join, 90% of the copy rate); many rows, the chain scores -> weights ->
+// What bounds it: few rows, HBM (8 rows over 262144 keys: 537 MB in 85 us with
+// the join, 93% of the copy rate); many rows, the chain scores -> weights ->
 // product of a CTA beside the other CTA's (a prompt of 4096 tokens behind 8192
-// at head size 128: 512 us, 1340 TFLOP/s, 70% of cuBLAS; 411 us at head size
+// at head size 128: 490 us, 1400 TFLOP/s, 73% of cuBLAS; 391 us at head size
 // 256); short items, the latency of their start (about 3 us).
 // Tried at head size 128 and left: tiles of 64 keys (the products of 128 x 64
 // wait for Q's reads; 4% slower), one CTA with two streams of 128 rows over
 // shared tiles (prompts 4% faster, short items 1.6 times slower) or over
 // alternate tiles (the ring could not keep up), rings of half tiles (3% slower),
+// the weights of half a tile handed over before the other half's (14% slower),
 // a cooperative launch with the join at its end (launch +2 us).
 #include <type_traits>
 
