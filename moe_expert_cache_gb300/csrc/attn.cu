@@ -54,6 +54,7 @@
 // a cooperative launch with the join at its end (launch +2 us).
 #include <type_traits>
 
+#include "attn_line.cuh"
 #include "ft_kv.cuh"
 #include "ft_tc.cuh"
 
@@ -71,8 +72,8 @@ constexpr int MERGE_NB(int D) { return D == 64 ? 8 : 6; }
 constexpr int MERGE_CTAS(int D) { return D == 64 ? 3 : 2; }
 constexpr int NQ = 16;               // items of up to this many rows take the transposed form
 constexpr int NWORK = 16;            // work items of a CTA that are kept in shared memory
-constexpr int OV = 2;                // cost of an item's start, in tiles
-constexpr int OVP = 3;               // the same with the partial result of a prefix item
+using attnline::OVP;
+using attnline::upper;
 
 template <int D>
 struct Cfg {
@@ -1074,44 +1075,8 @@ struct PlanArgs {
 // What the plan kernel keeps of a segment.
 struct SegRec {
     int b, r0, nrows, ntile, kend;
-    int cum;  // cost of the segments before it
+    attnline::cost_t cum;  // cost of the segments before it
 };
-
-__device__ int scan_excl(int v, int* ws, int& total) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) ws[wid] = x;
-    __syncthreads();
-    if (wid == 0) {
-        int s = ws[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
-        }
-        ws[lane] = s;
-    }
-    __syncthreads();
-    total = ws[31];
-    return x - v + (wid ? ws[wid - 1] : 0);
-}
-
-// largest i in [0, n) with a[i] <= x (a ascending, a[0] <= x)
-template <class F>
-__device__ __forceinline__ int upper(int n, long long x, F a) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((long long)a(mid) <= x) lo = mid; else hi = mid;
-    }
-    return lo;
-}
 
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
@@ -1119,10 +1084,11 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
     __shared__ int s_n[PT], s_len[PT], s_row[PT], s_P[PT], s_pre[PT], s_sb[PT];  // per request
     __shared__ int g_min[PT], g_rows[PT], g_solo[PT], g_first[PT];               // per group
     __shared__ int q_g[PT / 2], q_off[PT / 2];  // per group taken together (it has two requests at least)
-    __shared__ int ws[33];
+    __shared__ int ws[32];
+    __shared__ attnline::cost_t wl[32];
     __shared__ long long s_end[CHOICES];  // per choice of the chunk: what it costs
     __shared__ int s_c[CHOICES], s_iph;
-    extern __shared__ __align__(16) int s_cum[];                   // [CUM]
+    extern __shared__ __align__(16) attnline::cost_t s_cum[];      // [CUM]
     int4* s_cta = reinterpret_cast<int4*>(s_cum + CUM);            // [n_cta] first item, first and last segment
     ft::grid_dep_launch();
     ft::grid_dep_wait();
@@ -1184,7 +1150,7 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         if (5 * cdiv(g_rows[tid], ATTN_BM) > 4 * g_solo[tid]) P = 0;
     }
     int n_pre;
-    const int my_pre = scan_excl(P > 0, ws, n_pre);
+    const int my_pre = ft::block_scan(P > 0 ? 1 : 0, ws, n_pre);
     g_min[tid] = P;  // from here on: the shared tokens taken
     if (P > 0) q_g[my_pre] = tid;
     g_solo[tid] = my_pre;
@@ -1195,9 +1161,9 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
     // ---- chunks of the shared ranges: of up to four rounds over the CTAs, the one that ends first
     int n_seg;
     const int my_segs = cdiv(n * G, ATTN_BM);
-    s_sb[tid] = scan_excl(my_segs, ws, n_seg);
+    s_sb[tid] = ft::block_scan(my_segs, ws, n_seg);
     __syncthreads();
-    int cost = 0;
+    attnline::cost_t cost = 0;
     for (int base = 0; base < n_seg; base += PT) {
         const int s = base + tid;
         SegRec r{};
@@ -1211,15 +1177,15 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
             r.kend = max(0, min(s_len[r.b], s_len[r.b] - s_n[r.b] + 1 + last));
             r.ntile = max(1, cdiv(r.kend - s_P[r.b], ATTN_BN));
         }
-        int total;
-        r.cum = cost + scan_excl(s < n_seg ? r.ntile + OV : 0, ws, total);
+        attnline::cost_t total;
+        r.cum = cost + ft::block_scan(s < n_seg ? attnline::segment_cost(r.ntile) : 0, wl, total);
         if (s < n_seg) {
             seg[s] = r;
             if (s < CUM) s_cum[s] = r.cum;
         }
         cost += total;
     }
-    const long long S = (long long)cost * p.Hkv;
+    const long long S = cost * p.Hkv;
     // Items for so many sixteenths of the CTAs, the rest left to the other work, up to four rounds over all of them: a
     // warp looks at each choice.  What it costs, in eighths of a tile's time: the end of an even share or of the longest
     // chain of prefix items (1.3 times that where an SM has two such CTAs), and the join, 20000 pieces of a row in a
@@ -1268,7 +1234,7 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         int x = 0;
         if (tid < n_pre) x = cdiv(g_rows[q_g[tid]], ATTN_BM) * cdiv(cdiv(g_min[q_g[tid]], ATTN_BN), c);
         int iph;
-        const int off = scan_excl(x, ws, iph);
+        const int off = ft::block_scan(x, ws, iph);
         if (tid < n_pre) q_off[tid] = off;
         if (tid == 0) s_iph = iph;
     }
@@ -1276,25 +1242,9 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
     const int iph = s_iph, n_items = iph * p.Hkv;
 
     // ---- parts of the line of tiles: CTAs with one prefix item more get less
-    const int k0 = n_items / n_cta, n1 = n_items % n_cta, n0 = n_cta - n1;
-    const long long p0 = (long long)k0 * (c + OVP), p1 = p0 + (n1 ? c + OVP : 0);
-    const long long W = (S + n1 * p1 + n0 * p0 + n_cta - 1) / n_cta;
-    long long q1 = 0, q0;
-    if (n1 && W <= p1) {
-        q0 = (S + n0 - 1) / n0;
-    } else {
-        q1 = n1 ? W - p1 : 0;
-        q0 = W - p0;
-    }
-    if (q0 < 1) q0 = 1;
-    auto start_of = [&](int i) { return min(S, i < n1 ? i * q1 : n1 * q1 + (i - n1) * q0); };
-    auto cta_of = [&](long long x) { return x < n1 * q1 ? (int)(x / q1) : n1 + (int)((x - n1 * q1) / q0); };
+    const attnline::Line line(cost, p.Hkv, n_seg, n_cta, n_items, c);
+    const int k0 = line.k0, n1 = line.n1;
     auto cum_of = [&](int i) { return i < CUM ? s_cum[i] : seg[i].cum; };
-    auto linear = [&](long long x) {  // head * n_seg + segment that holds cost position x
-        const int h = (int)(x / cost);
-        return h * n_seg + upper(n_seg, x - (long long)h * cost, [&](int i) { return cum_of(i); });
-    };
-    auto begin_of = [&](int l) { return (long long)(l / n_seg) * cost + cum_of(l % n_seg); };
     __syncthreads();  // seg is complete
 
     int n_works = 0;
@@ -1303,17 +1253,16 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         int cnt = 0;
         if (i < n_cta) {
             cnt = k0 + (i < n1 ? 1 : 0);
-            const long long x0 = start_of(i), x1 = start_of(i + 1);
+            const long long x0 = line.start_of(i), x1 = line.start_of(i + 1);
             if (x1 > x0) {
-                const int l0 = linear(x0), l1 = linear(x1 - 1);
-                cnt += l1 - l0 + 1;
-                if (x1 - begin_of(l1) <= OV) --cnt;  // only the start cost of the last one: its tiles are the next CTA's
+                const int l0 = line.at(x0, cum_of), l1 = line.at(x1 - 1, cum_of);
+                cnt += attnline::Line::items(l0, l1, line.begin_of(l1, cum_of), x1);
                 s_cta[i].y = l0;
                 s_cta[i].z = l1;
             }
         }
         int total;
-        const int at = n_works + scan_excl(cnt, ws, total);
+        const int at = n_works + ft::block_scan(cnt, ws, total);
         if (i < n_cta) {
             p.pl.ctas[i].w0 = s_cta[i].x = at;
             p.pl.ctas[i].w1 = at + cnt;
@@ -1354,13 +1303,13 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
             w.prow = idx * ATTN_BM;
             put(jp + j, w);
         }
-        const long long x0 = start_of(i), x1 = start_of(i + 1);
+        const long long x0 = line.start_of(i), x1 = line.start_of(i + 1);
         if (x1 <= x0) continue;
         const int l0 = mine.y, l1 = mine.z;
         for (int l = l0 + sl; l <= l1; l += 8) {
-            const long long b0 = begin_of(l);
             const SegRec r = seg[l % n_seg];
-            const int t0 = (int)max(0ll, x0 - b0 - OV), t1 = (int)min((long long)r.ntile, max(0ll, x1 - b0 - OV));
+            int t0, t1;
+            attnline::Line::tiles(line.begin_of(l, cum_of), r.ntile, x0, x1, t0, t1);
             if (t0 >= t1) continue;  // (only ever the last one)
             AttnWork w;
             w.head = l / n_seg;
@@ -1381,9 +1330,7 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
     }
     // ---- rows with more than one piece
     auto pieces_of = [&](int l, const SegRec& r, int& c0, int& c1) {  // the CTAs that have some of its tiles
-        const long long b0 = begin_of(l) + OV;
-        c0 = cta_of(b0);
-        c1 = cta_of(b0 + r.ntile - 1);
+        line.holders(line.begin_of(l, cum_of), r.ntile, c0, c1);
         return c0 != c1 || s_pre[r.b] >= 0;
     };
     int rows = 0;
@@ -1392,7 +1339,7 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         int c0, c1;
         if (pieces_of(l, r, c0, c1)) rows += r.nrows;
     }
-    scan_excl(rows, ws, rows);
+    ft::block_scan(rows, ws, rows);
     // several warps share a row's pieces as long as all warps run at once
     const int warps = max(1, p.merge_warps / max(1, rows));
     int n_merge = 0;
@@ -1425,7 +1372,7 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
             }
         }
         int total;
-        const int at = n_merge + scan_excl(cnt, ws, total);
+        const int at = n_merge + ft::block_scan(cnt, ws, total);
         const int step = cnt ? 8 / m.wpr : 0, brow = m.brow;
         for (int j = 0; j < cnt; ++j) {
             m.r0 = r.r0 + j * step;
@@ -1460,7 +1407,7 @@ Kernels kernels_of(const ft_kv* kv) {
     if (kv->D == 128) return bf ? kernels<128, true>() : kernels<128, false>();
     return bf ? kernels<256, true>() : kernels<256, false>();
 }
-size_t plan_smem(const ft_kv* kv) { return CUM * 4 + (size_t)kv->plan.n_cta * 16; }
+size_t plan_smem(const ft_kv* kv) { return CUM * sizeof(attnline::cost_t) + (size_t)kv->plan.n_cta * 16; }
 
 }  // namespace
 

@@ -159,4 +159,31 @@ inline cudaError_t launch_dependent(const void* k, int grid, int block, size_t s
 namespace ft {
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Exclusive prefix sum over a CTA of 1024 threads; total gets the sum.
+template <class V>
+__device__ __forceinline__ V block_scan(V v, V (&ws)[32], V& total) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    V x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const V y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // the previous call's reads of ws are over
+    if (lane == 31) ws[wid] = x;
+    __syncthreads();
+    if (wid == 0) {
+        V s = ws[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const V y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        ws[lane] = s;
+    }
+    __syncthreads();
+    total = ws[31];
+    return x - v + (wid ? ws[wid - 1] : 0);
+}
 }  // namespace ft

@@ -28,32 +28,6 @@ KvCtl ctl_of(const ft_kv* kv) {
                  kv->info, kv->n_copy, kv->free_list, kv->remap, kv->rank, kv->copies, kv->err};
 }
 
-// Exclusive prefix sum over the CTA; total gets the sum.  ws: 33 ints.
-__device__ int block_scan(int v, int* ws, int& total) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    __syncthreads();  // the previous call's reads of ws are over
-    if (lane == 31) ws[wid] = x;
-    __syncthreads();
-    if (wid == 0) {
-        int s = ws[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
-        }
-        ws[lane] = s;
-    }
-    __syncthreads();
-    total = ws[31];
-    return x - v + (wid ? ws[wid - 1] : 0);
-}
-
 // Which of the four pages from base + 4 * thread on are free, one bit each.
 __device__ __forceinline__ unsigned free_bits(const KvCtl& c, int base) {
     const int p = base + 4 * threadIdx.x;
@@ -66,12 +40,12 @@ __device__ __forceinline__ unsigned free_bits(const KvCtl& c, int base) {
 
 // The lowest `want` free pages, ascending, to list; returns how many there are
 // (at most a few more than `want` are counted).  first: free_bits(c, 0).
-__device__ int take_free(const KvCtl& c, int want, int* ws, unsigned first) {
+__device__ int take_free(const KvCtl& c, int want, int (&ws)[32], unsigned first) {
     int have = 0;
     for (int base = 0; base < c.n_pages && have < want; base += 4 * CT) {
         const unsigned f = base ? free_bits(c, base) : first;
         int total;
-        int at = have + block_scan(__popc(f), ws, total);
+        int at = have + ft::block_scan(__popc(f), ws, total);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (f >> j & 1u) {
@@ -114,7 +88,7 @@ __device__ void refuse(const KvCtl& c, unsigned bit) {
 
 __global__ void __launch_bounds__(CT) kv_extend_kernel(KvCtl c, int n, const int* __restrict__ rows,
                                                        const int* __restrict__ add) {
-    __shared__ int ws[33];
+    __shared__ int ws[32];
     __shared__ RowMarks marks;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     clear(marks, c.n_rows);
@@ -139,7 +113,7 @@ __global__ void __launch_bounds__(CT) kv_extend_kernel(KvCtl c, int n, const int
             }
         }
         int total;
-        const int at = want + block_scan(need, ws, total);
+        const int at = want + ft::block_scan(need, ws, total);
         if (i < n) c.rank[i] = at;
         want += total;
     }
@@ -161,7 +135,7 @@ __global__ void __launch_bounds__(CT) kv_extend_kernel(KvCtl c, int n, const int
 
 __global__ void __launch_bounds__(CT) kv_fork_kernel(KvCtl c, int n, const int* __restrict__ parents,
                                                      const int* __restrict__ children) {
-    __shared__ int ws[33];
+    __shared__ int ws[32];
     __shared__ RowMarks marks;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     clear(marks, c.n_rows);
@@ -184,7 +158,7 @@ __global__ void __launch_bounds__(CT) kv_fork_kernel(KvCtl c, int n, const int* 
             }
         }
         int total;
-        const int at = want + block_scan(need, ws, total);
+        const int at = want + ft::block_scan(need, ws, total);
         if (i < n) c.rank[i] = at;
         want += total;
     }
@@ -273,10 +247,10 @@ __global__ void __launch_bounds__(CT) kv_free_kernel(KvCtl c, int n, const int* 
 __global__ void __launch_bounds__(CT) kv_compact_kernel(KvCtl c) {
     ft::grid_dep_launch();
     ft::grid_dep_wait();
-    __shared__ int ws[33];
+    __shared__ int ws[32];
     int live = 0;
     for (int p = threadIdx.x; p < c.n_pages; p += CT) live += c.refs[p] > 0;
-    block_scan(live, ws, live);
+    ft::block_scan(live, ws, live);
     int holes = 0, movers = 0;
     for (int base = 0; base < c.n_pages; base += CT) {
         const int p = base + threadIdx.x;
@@ -284,7 +258,7 @@ __global__ void __launch_bounds__(CT) kv_compact_kernel(KvCtl c) {
         const bool hole = in && p < live && !used, mover = used && p >= live;
         // at most 2^10 of each kind in a step: both counts in one word
         int total;
-        const int at = block_scan((hole ? 1 : 0) | (mover ? 1 << 16 : 0), ws, total);
+        const int at = ft::block_scan((hole ? 1 : 0) | (mover ? 1 << 16 : 0), ws, total);
         if (hole) c.copies[holes + (at & 0xffff)].dst = p;
         if (mover) c.copies[movers + (at >> 16)].src = p;
         holes += total & 0xffff;
