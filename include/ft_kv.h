@@ -69,7 +69,8 @@ size_t ft_kv_scratch_bytes(int32_t Hq, int32_t Hkv, int32_t D, int32_t n_pages, 
  *   dtype          FT_KV_BF16 or FT_KV_F16: type of the pool, the queries and
  *                  the outputs.
  *   T_max, B_max   largest number of query tokens and of requests of an
- *                  ft_attn_plan; 1 <= B_max <= 1024, T_max >= 1.
+ *                  ft_attn_plan; 1 <= B_max <= 1024, T_max >= 1, T_max*Hq below
+ *                  2^30, 2*T_max*Hq + 128*Hkv*(B_max + 1) below 2^31 - 2^23.
  *   pool           DEVICE, 128-byte aligned;  table, lens, refs DEVICE, 4-byte
  *                  aligned.  All four stay valid until ft_kv_destroy.
  *   stream         cudaStream_t that every call runs on (NULL = legacy default

@@ -1421,7 +1421,7 @@ void attn_plan_sizes(int Hq, int Hkv, int D, int T_max, int B_max, int num_sms, 
     // a row each, a short last record of a segment, and what each CTA of the join reads first
     p.cap_merges = T_max * Hq + Hkv * p.cap_segs + 4 * num_sms;
     p.b_row = (long long)p.cap_items * ATTN_BM;
-    p.c_row = p.b_row + (long long)T_max * Hq;
+    p.c_row = p.b_row + (long long)T_max * Hq;  // (kv_api.cu refuses sizes whose rows pass 2^31)
     p.part_rows = p.c_row + (long long)p.n_cta * ATTN_BM;
 }
 

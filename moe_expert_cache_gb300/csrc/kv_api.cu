@@ -12,9 +12,14 @@
 namespace {
 
 bool sizes_ok(int Hq, int Hkv, int D, int n_pages, int n_rows, int T_max, int B_max) {
-    return Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq / Hkv <= ATTN_BM && (D == 64 || D == 128 || D == 256) &&
-           n_pages >= 1 && n_rows >= 1 && n_rows <= KV_MAX_ROWS && T_max >= 1 && B_max >= 1 && B_max <= ATTN_MAX_B &&
-           (long long)T_max * Hq < (1ll << 30);
+    if (!(Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq / Hkv <= ATTN_BM && (D == 64 || D == 128 || D == 256) &&
+          n_pages >= 1 && n_rows >= 1 && n_rows <= KV_MAX_ROWS && T_max >= 1 && B_max >= 1 && B_max <= ATTN_MAX_B &&
+          (long long)T_max * Hq < (1ll << 30)))
+        return false;
+    // the plan numbers rows of partial results in 32 bits (attn_plan_sizes; at least 256 bytes a row, so more of them
+    // would not fit the card either).  2^23 are kept for the CTAs' own: five items of 128 rows each for 13107 CTAs
+    const long long tiles = ((long long)T_max * (Hq / Hkv) + ATTN_BM - 1) / ATTN_BM;
+    return Hkv * (tiles + B_max) * ATTN_BM + (long long)T_max * Hq < (1ll << 31) - (1ll << 23);
 }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -64,7 +69,7 @@ bool misaligned(const void* p, size_t a) { return (uintptr_t)p % a != 0; }
 extern "C" {
 
 size_t ft_kv_page_bytes(int32_t L, int32_t Hkv, int32_t D, int32_t page) {
-    if (L < 1 || Hkv < 1 || (D != 64 && D != 128 && D != 256) ||
+    if (L < 1 || Hkv < 1 || (long long)L * 2 * Hkv >= (1ll << 31) - 1 || (D != 64 && D != 128 && D != 256) ||
         (page != 16 && page != 32 && page != 64 && page != 128))
         return 0;
     return (size_t)L * 2 * Hkv * page * D * 2;
