@@ -170,7 +170,8 @@ ft_status ft_attn_plan(ft_kv* kv, int32_t B, int32_t T, const int32_t* cu_q, con
  * seeing its row's keys 0 .. len - n + i (the new tokens are the last of the
  * row).  A query that sees no key gives zeros.  Scores, softmax statistics
  * and sums are fp32; the softmax weights are rounded to the cache's type for
- * the product with V.  Values at places that a query of the same tile does not
+ * the product with V (f16: to its 11 bits down to 2^-22 of a row's largest
+ * weight, and to multiples of 2^-32 of it below).  Values at places that a query of the same tile does not
  * see but that lie within the row's length must be finite.
  *   q        DEVICE [T, >= Hq*D], row stride ld_q;  out the same with ld_o;
  *            out must not overlap q.  ld_q, ld_o multiples of 8, both pointers

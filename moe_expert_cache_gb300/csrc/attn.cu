@@ -37,9 +37,9 @@
 //
 // The running maximum is a reference that may fall behind: past an item's first
 // tile the weights are taken on the present one, and only where a tile's weights
-// sum to more than 4096 is the tile done again on its own maximum and O rescaled.
-// The weights stay as exact (they are floating-point numbers on any scale), no
-// maxima are taken, and almost no tile touches O.
+// sum to more than 4096 (f16: 254) is the tile done again on its own maximum and O
+// rescaled.  The weights stay as exact (they are floating-point numbers on any
+// scale), no maxima are taken, and almost no tile touches O.
 //
 // What bounds it: few rows, HBM (8 rows over 262144 keys: 537 MB in 85 us with
 // the join, 93% of the copy rate); many rows, the chain scores -> weights ->
@@ -64,7 +64,15 @@ constexpr int G_THREADS = 256;        // 4 softmax warps, two TMA warps, an MMA 
 // with two CTAs an SM: 128 registers a thread at launch; 128 x 208 + 128 x 48 = 256 x 128
 constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 48;
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float MAX_SUM = 4096.f;    // of a tile's weights on a reference that has fallen behind (f16 holds 65504)
+// f16 weights are taken on a reference 2^8 below the row's own: 2^-24, the smallest f16 number, is then 2^-32 of the
+// largest weight, and a strong first key does not drown a long context (4096 keys of 2^-26 to 2^-30 of its weight each
+// lost all of their 2^-15 of the result).  bf16 has the range without.  MAX_SUM is the most that a tile's weights may
+// sum to on a reference that has fallen behind, 254 and 4096 of the reference's own weight (f16 holds 65504; a tile's
+// 128 weights sum to 128 of it at most while the reference is the largest score).
+template <bool BF>
+constexpr float SHIFT = BF ? 0.f : 8.f;
+template <bool BF>
+constexpr float MAX_SUM = BF ? 4096.f : 65024.f;
 // pieces that a warp of the join has in flight, and the join's CTAs on an SM.  More pieces need registers that the
 // loads' addresses want (64 requests behind 8192 keys at head size 128: 6 pieces 28.6 us, 12 30.1, 16 31.3; with 3 CTAs
 // an SM 30.5; 130 behind 16384 at 256, 2 CTAs: 4 pieces 58.7 us, 6 58.1, 8 58.9, 4 with 3 CTAs 61.8)
@@ -702,8 +710,9 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
             it0 += H * k.ntile - (H == 2 && k.kend - (k.pos0 + (k.ntile - 1) * ATTN_BN) <= 64);
         };
         // The transposed form, for few rows: a thread has a key, its scores with all the queries, their weights on
-        // a reference of each query that the four warps agree on: the score of the item's first key, as long as no
-        // weight on it is larger than MAX_SUM.
+        // a reference of each query that the four warps agree on, as long as no weight on it is larger than MAX_SUM: the
+        // score of the item's first key or, in f16, whose weights have room for less, the largest of the first 32 (64
+        // requests of up to 512 keys 14.2 us; with the first key's 15.1).
         auto few_rows = [&](const AttnWork& k, int w) {
             int t = r;
             asm volatile("" : "+r"(t));  // what follows from t stays in here: the other form needs the registers
@@ -727,9 +736,17 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                 const int past = k.vis0 == ATTN_NOMASK ? 0 : pos - k.vis0 + 1;
                 const uint32_t vis = pos >= k.kend ? 0u : past <= 0 ? rows : rows & (0xffffffffu << min(max(past * p.G - k.r0, 0), 31));
                 if (i == 0) {
-                    if (t == 0) {
+                    if constexpr (BF) {
+                        if (t == 0) {
 #pragma unroll
-                        for (int j = 0; j < NQ; ++j) s_red[j >> 2][j & 3] = vis >> j & 1 ? x[j] * p.c : 0.f;
+                            for (int j = 0; j < NQ; ++j) s_red[j >> 2][j & 3] = vis >> j & 1 ? x[j] * p.c : 0.f;
+                        }
+                    } else if (wid == 0) {
+                        float y[NQ];
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j) y[j] = vis >> j & 1 ? x[j] * p.c : -INFINITY;
+                        const float m0 = warp_columns(y, t, [](float a, float b) { return fmaxf(a, b); });
+                        if (!(t & 1)) s_red[t >> 3][(t >> 1) & 3] = m0 - SHIFT<BF>;
                     }
                     if (any_of_128(!ok)) {
                         ok = false;
@@ -752,7 +769,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                     e[j] = vis >> j & 1 ? y : 0.f;
                     top = fmaxf(top, e[j]);
                 }
-                if (any_of_128(top > MAX_SUM || (unseen & vis) || !ok)) {
+                if (any_of_128(top > MAX_SUM<BF> || (unseen & vis) || !ok)) {
                     // the maxima of the queries over the tile
                     float y[NQ];
 #pragma unroll
@@ -770,7 +787,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
 #pragma unroll
                     for (int j = 0; j < NQ; ++j) {
                         const float4 m4 = *reinterpret_cast<const float4*>(s_red[j]);
-                        const float m = max3(fmaxf(m4.x, m4.y), m4.z, m4.w);
+                        const float m = max3(fmaxf(m4.x, m4.y), m4.z, m4.w) - SHIFT<BF>;
                         const bool first = unseen >> j & 1;
                         if (m != -INFINITY) unseen &= ~(1u << j);
                         const float now = first ? (m == -INFINITY ? 0.f : m) : fmaxf(m, ref[j]);
@@ -928,7 +945,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                     const float2 ls = unf2(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])));
                     return ls.x + ls.y;
                 };
-                auto reference = [&]() { mc = m == -INFINITY ? 0.f : m * p.c; };  // -inf: a row that has seen no key yet
+                auto reference = [&]() { mc = m == -INFINITY ? 0.f : m * p.c - SHIFT<BF>; };  // -inf: a row that has seen no key yet
                 if (rows_here) {
                     load(0);
                     bool exact = i == 0;
@@ -943,7 +960,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                             lt += weights(1);
                         }
                         // (lanes past the rows hold anything)
-                        exact = __any_sync(0xffffffffu, r < k.nrows && (lt > MAX_SUM || m == -INFINITY));
+                        exact = __any_sync(0xffffffffu, r < k.nrows && (lt > MAX_SUM<BF> || m == -INFINITY));
                         if (exact) load(0);
                     }
                     if (exact) {
@@ -961,7 +978,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                         if (i == 0) {
                             m = mn;
                         } else {
-                            const bool lag = r < k.nrows && (lt > MAX_SUM || m == -INFINITY) && mn > m;
+                            const bool lag = r < k.nrows && (lt > MAX_SUM<BF> || m == -INFINITY) && mn > m;
                             // with one S the scores' own barrier has told that the product before them is done
                             if (NS == 2 && !wait(&pv_done[(g - 1) & 1], (g - 1) >> 1)) ok = false;
                             tc::fence_after_sync();
@@ -1039,7 +1056,7 @@ __global__ void __launch_bounds__(G_THREADS, Cfg<D>::CTAS) attn_kernel(const __g
                             if (r4 + 8 * j < k.nrows) st_global32(dst + cc + (size_t)(8 * j) * D, v);
                         }
                     }
-                    if (in) p.part_ml[k.prow + r] = make_float2(m * p.c, l);
+                    if (in) p.part_ml[k.prow + r] = make_float2(m * p.c - SHIFT<BF>, l);
                 }
             }
             tc::fence_before_sync();
