@@ -132,8 +132,8 @@ ft_status ft_kv_compact(ft_kv* kv);
  *            their sines.  rot is 0..D, a multiple of 16 (0: no rotation,
  *            cos_sin and max_pos are ignored).
  *   pair     0: value i turns with value i + rot/2; 1: 2i with 2i+1.
- *   q_out    DEVICE [T, >= Hq*D], row stride ld_q; may be qkv itself (same
- *            stride).
+ *   q_out    DEVICE [T, >= Hq*D], row stride ld_q; may be qkv itself, or other
+ *            columns of its rows (same stride); must not overlap it otherwise.
  * ld, ld_q multiples of 8; qkv, q_out, norms and cos_sin 16-byte aligned.
  */
 ft_status ft_qk_rope_store(ft_kv* kv, int32_t layer, int32_t T, const void* qkv, int64_t ld, const int32_t* row_of,

@@ -64,6 +64,17 @@ ft_status launched(cudaError_t e) {
 
 bool misaligned(const void* p, size_t a) { return (uintptr_t)p % a != 0; }
 
+// Whether rows [n] of w values of 2 bytes at a, ld values apart, and of v values at b, ld_b apart, may touch: their spans
+// overlap, and they are not different columns of the rows of one buffer.
+bool may_touch(const void* a, int64_t ld, int64_t w, const void* b, int64_t ld_b, int64_t v, int64_t n) {
+    const uintptr_t a0 = (uintptr_t)a, a1 = a0 + ((size_t)(n - 1) * ld + w) * 2;
+    const uintptr_t b0 = (uintptr_t)b, b1 = b0 + ((size_t)(n - 1) * ld_b + v) * 2;
+    if (!(a0 < b1 && b0 < a1)) return false;
+    if (ld != ld_b) return true;
+    const uintptr_t row = (uintptr_t)ld * 2, off = b0 >= a0 ? (b0 - a0) % row : (row - (a0 - b0) % row) % row;
+    return off < (uintptr_t)w * 2 || off + (uintptr_t)v * 2 > row;
+}
+
 }  // namespace
 
 extern "C" {
@@ -171,10 +182,10 @@ ft_status ft_qk_rope_store(ft_kv* kv, int32_t layer, int32_t T, const void* qkv,
         !(eps >= 0.f) || !std::isfinite(eps))
         return FT_ERR_ARG;
     if (T == 0) return FT_OK;
-    if (!qkv || !row_of || !pos || !q_out || ld < (int64_t)(kv->Hq + 2 * kv->Hkv) * kv->D || ld % 8 ||
-        ld_q < (int64_t)kv->Hq * kv->D || ld_q % 8 || misaligned(qkv, 16) || misaligned(q_out, 16) ||
+    const int64_t w = ((int64_t)kv->Hq + 2 * (int64_t)kv->Hkv) * kv->D, wq = (int64_t)kv->Hq * kv->D;
+    if (!qkv || !row_of || !pos || !q_out || ld < w || ld % 8 || ld_q < wq || ld_q % 8 || misaligned(qkv, 16) || misaligned(q_out, 16) ||
         misaligned(q_norm, 16) || misaligned(k_norm, 16) || (rot && (!cos_sin || max_pos < 1 || misaligned(cos_sin, 16))) ||
-        (q_out == qkv && ld != ld_q))
+        (q_out == qkv ? ld != ld_q : may_touch(qkv, ld, w, q_out, ld_q, wq, T)))
         return FT_ERR_ARG;
     RopeArgs a{qkv, ld, row_of, pos, q_out, ld_q, q_norm, k_norm, eps, cos_sin, rot ? max_pos : 0x7fffffff, rot, pair,
                layer, T};
