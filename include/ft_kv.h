@@ -153,11 +153,14 @@ ft_status ft_qk_rope_store(ft_kv* kv, int32_t layer, int32_t T, const void* qkv,
  *            DEVICE int32 [n_groups+1] and [n_groups]: the requests
  *            group_start[g]..group_start[g+1]-1 share their first
  *            group_tokens[g] tokens, that is, their rows start with the same
- *            pages.  Only whole pages that precede every query of the group
- *            are taken as shared; a claim that is too large is cut to that.
- *            n_groups = 0 (then both may be NULL): nothing is shared.
- *            n_groups <= B.  What is claimed changes the speed, never the result,
- *            as long as the rows hold the same pages there.
+ *            pages.  Taken as shared are the whole pages that precede every
+ *            query of the group and that the rows of all its requests with
+ *            queries have in common; a claim that is too large is cut to that,
+ *            so what is claimed changes the speed, never the result.
+ *            n_groups = 0 (then both may be NULL): nothing is shared; requests
+ *            of few tokens then run a form of their own, which is the faster
+ *            one for them, so a caller without a shared prefix passes 0.
+ *            n_groups <= B.
  * Errors found on the device (cu_q or groups not ascending or out of range, a
  * row out of range, a length out of range): FT_ERR_DEVICE; the plan is empty.
  */

@@ -52,6 +52,7 @@
 // alternate tiles (the ring could not keep up), rings of half tiles (3% slower),
 // the weights of half a tile handed over before the other half's (14% slower),
 // a cooperative launch with the join at its end (launch +2 us).
+#include <climits>
 #include <type_traits>
 
 #include "attn_line.cuh"
@@ -1085,7 +1086,7 @@ constexpr int CUM = 2048;       // segments whose running cost is kept in shared
 struct PlanArgs {
     AttnPlan pl;
     int B, T, n_groups, G, Hkv, page, n_rows, row_pages, merge_nb, merge_warps, per_sm;
-    const int *cu_q, *rows, *group_start, *group_tokens, *lens;
+    const int *cu_q, *rows, *group_start, *group_tokens, *lens, *table;
     unsigned* err;
 };
 
@@ -1096,6 +1097,51 @@ struct SegRec {
 };
 
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ int block_max(int v, int (&ws)[32]) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if ((threadIdx.x & 31) == 0) ws[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = __reduce_max_sync(0xffffffffu, ws[threadIdx.x & 31]);
+    __syncthreads();
+    return v;
+}
+
+// Lowers cut[g] to the tokens of the whole pages that the rows of group g share, of the claim[g] that are claimed: a warp
+// compares 256 pages of a request with those of the group's first at a time.  Bound by what one SM reads from L2 once
+// there are many rows, by latency else: 64 requests of 128 claimed pages 1.8 us, 6 of 1024 1.3, 130 of 512 6.0 (7.1 page
+// by page, which is left for rows that do not start on 16 bytes; with the loads of two requests under way 6.8).
+template <class V>
+__device__ __forceinline__ void cut_claims(const PlanArgs& p, int most, const int* group, const int* row, const int* first,
+                                           const int* claim, int* cut) {
+    constexpr int W = sizeof(V) / 4, N = 8 / W;
+    const int lane = threadIdx.x & 31, plog = __ffs(p.page) - 1;
+    for (int u = threadIdx.x >> 5; u < p.B * cdiv(most, 256); u += PT / 32) {
+        const int b = u % p.B, g = group[b], j0 = u / p.B * 256 + lane * W;
+        if (g < 0 || b == first[g]) continue;
+        const int pages = claim[g] >> plog;
+        const int *mine = p.table + (size_t)row[b] * p.row_pages, *ref = p.table + (size_t)row[first[g]] * p.row_pages;
+        V x[N], y[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int j = j0 + i * 32 * W;
+            if (j < pages) {
+                x[i] = *reinterpret_cast<const V*>(mine + j);
+                y[i] = *reinterpret_cast<const V*>(ref + j);
+            }
+        }
+        int bad = INT_MAX;
+#pragma unroll
+        for (int i = N - 1; i >= 0; --i) {
+            const int j = j0 + i * 32 * W;
+#pragma unroll
+            for (int k = W - 1; k >= 0; --k)
+                if (j + k < pages && reinterpret_cast<const int*>(&x[i])[k] != reinterpret_cast<const int*>(&y[i])[k]) bad = j + k;
+        }
+        bad = __reduce_min_sync(0xffffffffu, bad);
+        if (lane == 0 && bad != INT_MAX) atomicMin(&cut[g], bad << plog);
+    }
+}
 
 __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
     __shared__ int s_n[PT], s_len[PT], s_row[PT], s_P[PT], s_pre[PT], s_sb[PT];  // per request
@@ -1166,6 +1212,16 @@ __global__ void __launch_bounds__(PT) attn_plan_kernel(const PlanArgs p) {
         P = min(p.group_tokens[tid], g_min[tid]) / p.page * p.page;
         if (5 * cdiv(g_rows[tid], ATTN_BM) > 4 * g_solo[tid]) P = 0;
     }
+    // ... and cut to the pages that all its rows really share
+    g_min[tid] = g_solo[tid] = P;
+    s_pre[tid] = gi;
+    const int most = __syncthreads_or(P) ? block_max(P / p.page, ws) : 0;
+    if (p.row_pages % 4 == 0 && (uintptr_t)p.table % 16 == 0)
+        cut_claims<int4>(p, most, s_pre, s_row, g_first, g_min, g_solo);
+    else
+        cut_claims<int>(p, most, s_pre, s_row, g_first, g_min, g_solo);
+    __syncthreads();
+    P = g_solo[tid];
     int n_pre;
     const int my_pre = ft::block_scan(P > 0 ? 1 : 0, ws, n_pre);
     g_min[tid] = P;  // from here on: the shared tokens taken
@@ -1473,7 +1529,7 @@ cudaError_t launch_attn_plan(ft_kv* kv, int B, int T, const int* cu_q, const int
                              const int* group_start, const int* group_tokens) {
     kv->few_rows = n_groups == 0 && (long long)T * (kv->Hq / kv->Hkv) <= (long long)NQ * B;
     PlanArgs a{kv->plan, B, T, n_groups, kv->Hq / kv->Hkv, kv->Hkv, kv->page, kv->n_rows, kv->row_pages,
-               MERGE_NB(kv->D), kv->num_sms * 8 * MERGE_CTAS(kv->D), kv->plan.n_cta / kv->num_sms, cu_q, rows, group_start, group_tokens, kv->lens, kv->err};
+               MERGE_NB(kv->D), kv->num_sms * 8 * MERGE_CTAS(kv->D), kv->plan.n_cta / kv->num_sms, cu_q, rows, group_start, group_tokens, kv->lens, kv->table, kv->err};
     void* args[] = {&a};
     return launch_dependent((const void*)attn_plan_kernel, 1, PT, plan_smem(kv), kv->stream, args);
 }

@@ -152,3 +152,37 @@ def test_what_a_bad_number_reaches(D, Hq, n):
         fine[:n, Hq // 2:, 3] = True
         assert bool(fine.all())
         assert c.kv.status() == c.ft.FT_OK
+
+
+@pytest.mark.parametrize("D,page,Hq", [(64, 16, 16), (128, 64, 32), (256, 32, 16)])
+def test_claims_that_the_pages_do_not_bear_out(D, page, Hq):
+    # rows that share fewer pages than is claimed, down to none: the pages that they do share are taken
+    import torch
+    shared, own = 40 * page, 5 * page
+    for differs in ({3: 39}, {1: 17, 6: 30}, {7: 0}, {0: 25}, {i: 9 for i in range(1, 8)}):
+        c = Cache([shared + own + i for i in range(8)], D=D, page=page, Hq=Hq, Hkv=2, shared=shared, T_max=16,
+                  spare=8 * len(differs), seed=page)
+        free = [p for p in range(c.n_pages) if c.model.refs[p] == 0]
+        for i, (r, j) in enumerate(differs.items()):
+            c.model.refs[c.model.rows[r][j]] -= 1
+            c.model.rows[r][j] = free[i]
+            c.model.refs[free[i]] = 1
+        c.table.copy_(torch.from_numpy(c.model.table()))
+        for ns in ([1] * 8, [1, 0, 2, 3, 1, 2, 1, 0]):
+            for groups in (([0, 8], [shared]), ([0, 8], [10 ** 6]), ([0, 4, 8], [shared, shared - 1]), ([1, 7], [shared])):
+                out, q = c.attend(ns, groups=groups)
+                assert c.kv.status() == c.ft.FT_OK
+                check_dense(c, ns, out, q)
+
+
+def test_claims_over_long_prefixes_and_many_requests():
+    # more pages than a warp compares at a time, more requests than there are warps; one page in the middle differs
+    import torch
+    shared, page, B = 700 * 16, 16, 50
+    for row, j in ((49, 699), (13, 300), (30, 256), (7, 255)):
+        c = Cache([shared + 1 + 3 * i for i in range(B)], D=64, page=page, Hq=16, Hkv=1, shared=shared, T_max=B, spare=3, seed=j)
+        c.model.rows[row][j] = next(p for p in range(c.n_pages) if c.model.refs[p] == 0)
+        c.table.copy_(torch.from_numpy(c.model.table()))
+        out, q = c.attend([1] * B, groups=([0, B], [shared]))
+        assert c.kv.status() == c.ft.FT_OK
+        check_dense(c, [1] * B, out, q)
