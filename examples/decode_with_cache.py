@@ -83,8 +83,10 @@ class Model:
         pos = self.ints(s + i for s, c in zip(starts, n) for i in range(c))
         cu = self.ints(np.concatenate([[0], np.cumsum(n)]).tolist())
         self.kv.extend(len(rows), row_ids, self.ints(n))
-        group = (self.ints([0, len(rows)]), self.ints([shared]))
-        self.kv.attn_plan(len(rows), T, cu, rows=row_ids, n_groups=1, group_start=group[0], group_tokens=group[1])
+        group = {}
+        if shared and len(rows) > 1:  # (without a claim requests of few tokens run the faster form)
+            group = dict(n_groups=1, group_start=self.ints([0, len(rows)]), group_tokens=self.ints([shared]))
+        self.kv.attn_plan(len(rows), T, cu, rows=row_ids, **group)
         h = self.embed[ids].clone()
         q = torch.empty(T, w, dtype=BF16, device="cuda")
         o = torch.empty_like(q)
