@@ -107,10 +107,12 @@ ft_status ft_kv_fork(ft_kv* kv, int32_t n, const int32_t* parents, const int32_t
  * all the same). */
 ft_status ft_kv_free(ft_kv* kv, int32_t n, const int32_t* rows);
 
-/* The pages in use become pages 0..live-1, so that the upper part of the pool
- * can be given back (for instance to a larger expert cache,
- * ft_cache_resize): the pages in use at index >= live move to the free ones
- * below live, the lowest first into the lowest, and table and refs follow. */
+/* The pages in use become pages 0..live-1: the pages in use at index >= live
+ * move to the free ones below live, the lowest first into the lowest, and table
+ * and refs follow.  The upper part of the pool then holds nothing, but a handle
+ * keeps its n_pages and may take those pages again.  To use that memory for
+ * something else: ft_kv_destroy, then ft_kv_init with a smaller n_pages >= live
+ * on the same pool, table, lens and refs, which goes on with the same rows. */
 ft_status ft_kv_compact(ft_kv* kv);
 
 /*

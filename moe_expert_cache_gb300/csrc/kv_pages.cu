@@ -280,8 +280,9 @@ __global__ void __launch_bounds__(CT) kv_compact_kernel(KvCtl c) {
 // is copied in part have their first tok*D values copied.  With `live` set,
 // the table's entries past the live pages are replaced too.  HBM bound: 601
 // pages of 1 MB moved by a compaction take 201 us with its control pass, 6.26
-// TB/s, 92% of the copy rate.  Reads and writes bypass L1 and leave L2 first
-// (no page is read twice).
+// TB/s, 92% of the copy rate.  Reads and writes bypass L1 and leave L2 first: a
+// compaction reads no page twice (forks of one parent read its last page once a
+// child, a few KB of it).
 __global__ void __launch_bounds__(256) kv_copy_kernel(const int* n_copy, const KvCopy* __restrict__ copies, uint8_t* pool,
                                                       int banks, int bank_bytes, int tok_bytes, int* table,
                                                       long long entries, const int* __restrict__ remap,

@@ -272,7 +272,7 @@ cudaError_t launch_qk_rope_store(ft_kv* kv, const RopeArgs& a) {
     p.steps = (kv->Hq + 2 * kv->Hkv + hpw - 1) / hpw;
     // few tokens: a warp per step, so that the whole call is one round of
     // loads; many: a warp keeps its token's angles over as many steps as leave
-    // every SM 32 warps
+    // 32 warps for every SM, two rounds of the 16 that its registers hold
     const long long per = (long long)a.T * p.steps / ((long long)kv->num_sms * 32);
     p.spw = per < 1 ? 1 : per > p.steps ? p.steps : (int)per;
     p.parts = (p.steps + p.spw - 1) / p.spw;
