@@ -176,8 +176,10 @@ ft_status ft_attn_plan(ft_kv* kv, int32_t B, int32_t T, const int32_t* cu_q, con
  * row).  A query that sees no key gives zeros.  Scores, softmax statistics
  * and sums are fp32; the softmax weights are rounded to the cache's type for
  * the product with V (f16: to its 11 bits down to 2^-22 of a row's largest
- * weight, and to multiples of 2^-32 of it below).  Values at places that a query of the same tile does not
- * see but that lie within the row's length must be finite.
+ * weight, and to multiples of 2^-32 of it below).  Keys that a query does not
+ * see may hold anything.  Values must be finite at places within the row's
+ * length that some query of the same tile of 128 rows does not see: one that is
+ * not reaches the queries of the tile that precede it.
  *   q        DEVICE [T, >= Hq*D], row stride ld_q;  out the same with ld_o;
  *            out must not overlap q.  ld_q, ld_o multiples of 8, both pointers
  *            16-byte aligned.

@@ -44,8 +44,12 @@
 // What bounds it: few rows, HBM (8 rows over 262144 keys: 537 MB in 85 us with
 // the join, 93% of the copy rate); many rows, the chain scores -> weights ->
 // product of a CTA beside the other CTA's (a prompt of 4096 tokens behind 8192
-// at head size 128: 490 us, 1400 TFLOP/s, 73% of cuBLAS; 391 us at head size
+// at head size 128: 490 us, 1400 TFLOP/s, 73% of cuBLAS; 387 us at head size
 // 256); short items, the latency of their start (about 3 us).
+//
+// The weights are rounded to the cache's type, as the tensor core takes both
+// operands in one: against 64 bits 2.3e-3 in bf16 and 2.8e-4 in f16, where the
+// rounding of the output alone gives 1.7e-3 and 2.1e-4.
 // Tried at head size 128 and left: tiles of 64 keys (the products of 128 x 64
 // wait for Q's reads; 4% slower), one CTA with two streams of 128 rows over
 // shared tiles (prompts 4% faster, short items 1.6 times slower) or over
