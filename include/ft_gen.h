@@ -1,0 +1,139 @@
+/*
+ * ft_gen.h -- C ABI of what a generation step needs around the two halves of
+ * its layers (ft.h: experts, ft_kv.h: attention): the norms before and after a
+ * block with its gate and the residual sum, and beam search's choice of the
+ * next tokens.  The reordering of the cache's rows after that choice and the
+ * layout of the next batch are ft_kv_reorder and ft_kv_batch of ft_kv.h.
+ *
+ * Conventions: those of ft.h.  ft_block_norm and ft_beam_select are async,
+ * allocate nothing, do not synchronise and can be captured in a CUDA graph.
+ * Nothing here has a backward pass: the library serves, it does not train.
+ */
+#ifndef FT_GEN_H
+#define FT_GEN_H
+
+#include "ft.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Types of values (the first two are FT_KV_BF16 and FT_KV_F16). */
+#define FT_T_BF16 0
+#define FT_T_F16  1
+#define FT_T_F32  2
+
+/* What a block's output is multiplied by. */
+#define FT_GATE_NONE    0
+#define FT_GATE_CHANNEL 1   /* [H], one factor a channel     */
+#define FT_GATE_TOKEN   2   /* [T], one factor a token       */
+#define FT_GATE_FULL    3   /* [T, >= H], one factor a value */
+
+/* What one place of a model fixes (plain data of the caller, read during the call only). */
+typedef struct {
+    int32_t H;            /* channels: 8..16384, a multiple of 8                               */
+    int32_t block_type;   /* FT_T_* of block, of resid and resid_out, of out, of the weights,  */
+    int32_t resid_type;   /* of the gate.  Of those that a call has the ones that are not      */
+    int32_t out_type;     /* FT_T_F32 are all FT_T_BF16 or all FT_T_F16.                       */
+    int32_t w_type;
+    int32_t gate_type;
+    int32_t gate;         /* FT_GATE_*                                                         */
+    int32_t post_norm;    /* 1: the block's output is normalised before gate and sum           */
+    const void* post;     /* DEVICE [H] weights of that norm; NULL: all one                    */
+    const void* pre;      /* DEVICE [H] weights of the norm of out; NULL: all one              */
+    float eps;            /* finite, >= 0; added to the mean square                            */
+    float resid_scale;    /* finite                                                            */
+    float block_scale;    /* finite                                                            */
+} ft_norm_desc;
+
+/*
+ * ft_block_norm -- what lies between two blocks of a layer, in one pass over T
+ * tokens of H channels:
+ *   z  = norm(block) * post                          (post_norm = 0: z = block)
+ *   h  = resid_scale * resid + block_scale * gate * z
+ *   out = norm(h) * pre            norm(x) = x / sqrt(mean(x^2) + eps)
+ * All arithmetic in fp32, one rounding where h and out are stored; out is made
+ * from the h that is not rounded.  Squares are summed in fp32: values from
+ * about 1e19 on overflow there, as the formula does in fp32.
+ *   block     DEVICE [T, >= H], row stride ld_b elements; NULL: no block (z = 0;
+ *             gate and post_norm must be 0): the norm before the first block.
+ *   gate      DEVICE, layout by desc->gate; ld_g is its row stride for
+ *             FT_GATE_FULL and ignored otherwise.
+ *   resid     DEVICE [T, >= H], row stride ld_r.
+ *   resid_out DEVICE [T, >= H], row stride ld_ro: h.  NULL: h is not stored.
+ *   out       DEVICE [T, >= H], row stride ld_o.  NULL: only h is wanted; one of
+ *             the two must be given.
+ * Row strides are multiples of 8 elements; all pointers 16-byte aligned, a gate
+ * of FT_GATE_TOKEN by its type.  resid_out and out may each be resid or block
+ * itself (same type and stride) or other columns of its rows; an output that
+ * overlaps an input otherwise, or the other output, is refused.
+ * stream: cudaStream_t (NULL: legacy default stream).
+ * Errors: FT_ERR_ARG, FT_ERR_CUDA.  T = 0 is allowed and does nothing.
+ */
+ft_status ft_block_norm(const ft_norm_desc* desc, int32_t T, const void* block, int64_t ld_b, const void* gate,
+                        int64_t ld_g, const void* resid, int64_t ld_r, void* resid_out, int64_t ld_ro, void* out,
+                        int64_t ld_o, void* stream);
+
+typedef struct ft_beam ft_beam;   /* opaque; created by ft_beam_init, freed by ft_beam_destroy */
+
+/* Bytes of device scratch that ft_beam_init allocates for these sizes on the
+ * current device; 0 where it refuses the sizes or there is no device. */
+size_t ft_beam_scratch_bytes(int32_t V, int32_t dtype, int32_t R_max, int32_t N_max);
+
+/*
+ * ft_beam_init -- a handle for choices over a vocabulary; syncs.
+ *   V       vocabulary, 1..2^24.
+ *   dtype   FT_T_* of the logits.
+ *   R_max   largest number of rows (requests x beams) of a call, 1..65536.
+ *   N_max   largest number of candidates that a call asks of a request, 1..64.
+ *           R_max * ceil(V / 8192) * N_max below 2^31.
+ *   stream  cudaStream_t that every call runs on; it must outlive the handle.
+ * Errors: FT_ERR_ARG, FT_ERR_OOM, FT_ERR_CUDA.
+ */
+ft_status ft_beam_init(ft_beam** out, int32_t V, int32_t dtype, int32_t R_max, int32_t N_max, void* stream);
+
+/*
+ * ft_beam_select -- the N best continuations of each of B requests of K beams.
+ * Beam k of request b is row b*K + k.  Its candidates are all tokens v, of
+ *   scores[row] + logits[row, v] - log(sum over u of exp(logits[row, u])),
+ * or, where the beam has ended, the token eos alone at scores[row].  The N best
+ * of all beams of the request are given in order, equal ones by beam, then by
+ * token.  Scores are compared in 64 bits (the sum over the vocabulary is taken
+ * in fp32), and rounded once when they are stored.  With K = 1 and scores of 0
+ * these are a row's N likeliest tokens with their log-probabilities.
+ *   B, K, N  B*K <= R_max, 1 <= K <= 64, 1 <= N <= N_max; B = 0 does nothing.
+ *   logits   DEVICE [B*K, >= V], row stride ld elements, aligned to its type.  A
+ *            logit of -inf is a token that may not be chosen; any finite value,
+ *            the type's lowest too, is a logit.  A row of a beam that has ended
+ *            is not read.
+ *   scores   DEVICE fp32 [B*K]; -inf: the beam has no candidates (its logits
+ *            are not read), as all but the first have before the first step.
+ *   rows     DEVICE int32 [B*K] or NULL: what out_parents holds for a row
+ *            (its row of the cache's table); NULL: the row's own number.
+ *   done     DEVICE int32 [B*K] or NULL: not 0 where the beam has ended.
+ *   eos      the token that ends a beam, -1: none; 0..V-1 where done is given.
+ *   out_scores, out_parents, out_tokens   DEVICE fp32, int32, int32 [B*N].  Where
+ *            a request has fewer than N candidates: -inf, -1, -1.
+ *   out_done DEVICE int32 [B*N] or NULL: 1 where the candidate's beam had ended
+ *            or its token is eos, else 0.
+ * out_scores may be scores and out_done may be done if N = K; outputs must not
+ * overlap anything else.
+ * A row with a NaN or a logit of +inf, and a score that is NaN or +inf, latch
+ * FT_ERR_DEVICE; that beam has no candidates.
+ * Errors: FT_ERR_ARG, FT_ERR_CUDA.
+ */
+ft_status ft_beam_select(ft_beam* bm, int32_t B, int32_t K, int32_t N, const void* logits, int64_t ld,
+                         const float* scores, const int32_t* rows, const int32_t* done, int32_t eos, float* out_scores,
+                         int32_t* out_parents, int32_t* out_tokens, int32_t* out_done);
+
+/* Synchronise the stream and return, then clear, what the device latched since
+ * the last call: FT_OK or FT_ERR_DEVICE. */
+ft_status ft_beam_status(ft_beam* bm);
+
+/* Free the handle and its scratch.  Syncs.  bm may be NULL. */
+void ft_beam_destroy(ft_beam* bm);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* FT_GEN_H */

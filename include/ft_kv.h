@@ -102,6 +102,32 @@ ft_status ft_kv_extend(ft_kv* kv, int32_t n, const int32_t* rows, const int32_t*
  * more than once. */
 ft_status ft_kv_fork(ft_kv* kv, int32_t n, const int32_t* parents, const int32_t* children);
 
+/* Row rows[i] becomes what row parents[i] was before the call, all rows at once
+ * (the beams of a search after a step): its length and its complete pages,
+ * shared.  A last page that is not complete is kept by one child if the parent's
+ * own row is in the list, by that row if it is its own child, else by the first
+ * in the list; every other child gets a copy of its tokens on a new page.
+ * parents[i] = -1: the row becomes empty.  A parent need not be in the list and
+ * may be listed more than once.  Pages that no row holds any more are free, for
+ * the new pages of this call too.  rows NULL: row i.  n is at most 1024. */
+ft_status ft_kv_reorder(ft_kv* kv, int32_t n, const int32_t* rows, const int32_t* parents);
+
+/* Lay out a step: row rows[b] of each of B requests grows by add[b] >= 0 tokens
+ * as by ft_kv_extend, and the new tokens of all requests, in order, are listed
+ * for ft_attn_plan and ft_qk_rope_store.
+ *   B, T    0..n_rows; T >= the sum of add, the size of the lists.
+ *   rows    DEVICE int32 [B]; NULL: row b.   add  DEVICE int32 [B].
+ *   cu_q    DEVICE int32 [B+1]: request b has the tokens cu_q[b]..cu_q[b+1]-1.
+ *   row_of, pos  DEVICE int32 [T]: row and position of each token; from cu_q[B]
+ *           on -1 and 0 (padding: nothing is computed or stored for it).
+ *   slots   DEVICE int64 [T] or NULL: page * (tokens of a page) + place in the
+ *           page, -1 for padding.
+ * A call that is refused on the device lists no tokens: cu_q is 0 and all T are
+ * padding.  More tokens than T latch FT_ERR_DEVICE.  The outputs must not
+ * overlap the inputs or each other. */
+ft_status ft_kv_batch(ft_kv* kv, int32_t B, const int32_t* rows, const int32_t* add, int32_t T, int32_t* cu_q,
+                      int32_t* row_of, int32_t* pos, int64_t* slots);
+
 /* Rows rows[i] become empty; pages that no row holds any more are free.  A
  * page whose count is already 0 latches FT_ERR_DEVICE (the row is emptied
  * all the same). */

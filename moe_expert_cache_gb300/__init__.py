@@ -1,4 +1,4 @@
-"""Python binding of libft (the C ABI in include/ft.h and include/ft_kv.h): argument marshalling only.
+"""Python binding of libft (the C ABI in include/ft.h, ft_kv.h and ft_gen.h): argument marshalling only.
 
 Every function here has the name of the C entry point without its ``ft_``
 prefix and takes plain integers for pointers (device or host addresses, e.g.
@@ -6,8 +6,9 @@ prefix and takes plain integers for pointers (device or host addresses, e.g.
 step of the hot path runs in the CUDA library; there is no Python or CPU
 fallback: if libft.so is missing this module raises on first use.
 
-``Context`` and ``KvCache`` are small convenience owners of an ``ft_ctx*`` and
-an ``ft_kv*`` that raise ``FtError`` on a non-zero status.
+``Context``, ``KvCache`` and ``Beams`` are small convenience owners of an
+``ft_ctx*``, an ``ft_kv*`` and an ``ft_beam*``, ``BlockNorm`` holds an
+``ft_norm_desc``; they raise ``FtError`` on a non-zero status.
 """
 from __future__ import annotations
 
@@ -31,6 +32,13 @@ FT_FMT_MXFP4 = 2
 FT_FMT_FP8 = 3
 FT_KV_BF16 = 0
 FT_KV_F16 = 1
+FT_T_BF16 = 0
+FT_T_F16 = 1
+FT_T_F32 = 2
+FT_GATE_NONE = 0
+FT_GATE_CHANNEL = 1
+FT_GATE_TOKEN = 2
+FT_GATE_FULL = 3
 
 _c_int = ctypes.c_int32
 _c_i64 = ctypes.c_int64
@@ -46,6 +54,13 @@ class CtlInfo(ctypes.Structure):
 
 class KvInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("allocated", "copied", "live")]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("H", "block_type", "resid_type", "out_type", "w_type", "gate_type", "gate", "post_norm")] + \
+               [(n, ctypes.c_void_p) for n in ("post", "pre")] + \
+               [(n, ctypes.c_float) for n in ("eps", "resid_scale", "block_scale")]
 
 
 class Counters(ctypes.Structure):
@@ -102,6 +117,14 @@ _SIGS = {
     "ft_kv_last": (_c_int, [_c_p, ctypes.POINTER(KvInfo)]),
     "ft_kv_status": (_c_int, [_c_p]),
     "ft_kv_destroy": (None, [_c_p]),
+    "ft_kv_reorder": (_c_int, [_c_p, _c_int, _c_p, _c_p]),
+    "ft_kv_batch": (_c_int, [_c_p, _c_int, _c_p, _c_p, _c_int, _c_p, _c_p, _c_p, _c_p]),
+    "ft_block_norm": (_c_int, [_c_p, _c_int] + [_c_p, _c_i64] * 5 + [_c_p]),
+    "ft_beam_scratch_bytes": (ctypes.c_size_t, [_c_int] * 4),
+    "ft_beam_init": (_c_int, [ctypes.POINTER(_c_p)] + [_c_int] * 4 + [_c_p]),
+    "ft_beam_select": (_c_int, [_c_p, _c_int, _c_int, _c_int, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_int] + [_c_p] * 4),
+    "ft_beam_status": (_c_int, [_c_p]),
+    "ft_beam_destroy": (None, [_c_p]),
 }
 
 _lib = None
@@ -274,6 +297,14 @@ def kv_compact(kv) -> int:
     return load().ft_kv_compact(kv)
 
 
+def kv_reorder(kv, n, rows, parents) -> int:
+    return load().ft_kv_reorder(kv, n, rows, parents)
+
+
+def kv_batch(kv, B, rows, add, T, cu_q, row_of, pos, slots) -> int:
+    return load().ft_kv_batch(kv, B, rows, add, T, cu_q, row_of, pos, slots)
+
+
 def qk_rope_store(kv, layer, T, qkv, ld, row_of, pos, q_out, ld_q, q_norm, k_norm, eps, cos_sin, max_pos, rot,
                   pair) -> int:
     return load().ft_qk_rope_store(kv, layer, T, qkv, ld, row_of, pos, q_out, ld_q, q_norm, k_norm, eps, cos_sin,
@@ -298,6 +329,35 @@ def kv_status(kv) -> int:
 
 def kv_destroy(kv) -> None:
     load().ft_kv_destroy(kv)
+
+
+def block_norm(desc, T, block, ld_b, gate, ld_g, resid, ld_r, resid_out, ld_ro, out, ld_o, stream=None) -> int:
+    """``desc`` is a NormDesc; the norms, gate and residual sum between two blocks (see include/ft_gen.h)."""
+    return load().ft_block_norm(ctypes.addressof(desc), T, block, ld_b, gate, ld_g, resid, ld_r, resid_out, ld_ro, out, ld_o,
+                                stream)
+
+
+def beam_scratch_bytes(V, dtype, R_max, N_max) -> int:
+    return load().ft_beam_scratch_bytes(V, dtype, R_max, N_max)
+
+
+def beam_init(V, dtype, R_max, N_max, stream):
+    h = _c_p()
+    st = load().ft_beam_init(ctypes.byref(h), V, dtype, R_max, N_max, stream)
+    return st, h.value
+
+
+def beam_select(bm, B, K, N, logits, ld, scores, rows, done, eos, out_scores, out_parents, out_tokens, out_done) -> int:
+    return load().ft_beam_select(bm, B, K, N, logits, ld, scores, rows, done, eos, out_scores, out_parents, out_tokens,
+                                 out_done)
+
+
+def beam_status(bm) -> int:
+    return load().ft_beam_status(bm)
+
+
+def beam_destroy(bm) -> None:
+    load().ft_beam_destroy(bm)
 
 
 # ------------------------------------------------------------ convenience
@@ -486,6 +546,18 @@ class KvCache:
         if st:
             _check(st, "ft_kv_free")
 
+    def reorder(self, n, parents, *, rows=None):
+        """Row rows[i] (None: row i) becomes what row parents[i] was, all at once; -1 empties it."""
+        st = self._lib.ft_kv_reorder(self.h, n, _ptr(rows), _ptr(parents))
+        if st:
+            _check(st, "ft_kv_reorder")
+
+    def batch(self, B, add, T, cu_q, row_of, pos, *, rows=None, slots=None):
+        """Grow the rows by add[b] tokens and list the new tokens for attn_plan and qk_rope_store, padded to T."""
+        st = self._lib.ft_kv_batch(self.h, B, _ptr(rows), _ptr(add), T, _ptr(cu_q), _ptr(row_of), _ptr(pos), _ptr(slots))
+        if st:
+            _check(st, "ft_kv_batch")
+
     def compact(self):
         st = self._lib.ft_kv_compact(self.h)
         if st:
@@ -517,3 +589,63 @@ class KvCache:
 
     def status(self) -> int:
         return kv_status(self.h)
+
+
+class BlockNorm:
+    """The norms around a block at one place of a model, with its gate and residual sum (include/ft_gen.h).
+
+    ``pre`` and ``post`` are weight tensors [H] (or addresses) of type ``w_type``; None: all one.
+    ``post_norm`` says whether the block's output is normalised (None: where ``post`` is given).
+    Types are FT_T_*, ``gate`` is FT_GATE_*.  Calls run on ``stream``.
+    """
+
+    def __init__(self, H, *, pre=None, post=None, post_norm=None, block_type=FT_T_BF16, resid_type=FT_T_F32,
+                 out_type=FT_T_BF16, w_type=FT_T_BF16, gate=FT_GATE_NONE, gate_type=FT_T_BF16, eps=1e-6, resid_scale=1.0,
+                 block_scale=1.0, stream=0):
+        norm = post is not None if post_norm is None else bool(post_norm)
+        self.desc = NormDesc(H, block_type, resid_type, out_type, w_type, gate_type, gate, 1 if norm else 0, _ptr(post),
+                             _ptr(pre), eps, resid_scale, block_scale)
+        self.stream = stream or None
+        self._at, self._lib = ctypes.addressof(self.desc), load()
+        self._keep = (pre, post)
+
+    def forward(self, T, resid, ld_r, *, block=None, ld_b=0, gate=None, ld_g=0, resid_out=None, ld_ro=0, out=None, ld_o=0):
+        st = self._lib.ft_block_norm(self._at, T, _ptr(block), ld_b, _ptr(gate), ld_g, _ptr(resid), ld_r, _ptr(resid_out),
+                                     ld_ro, _ptr(out), ld_o, self.stream)
+        if st:
+            _check(st, "ft_block_norm")
+
+
+class Beams:
+    """Owner of one ft_beam*: the choice of the next tokens of beams over a vocabulary of V (include/ft_gen.h).
+
+    All calls run on ``stream``; every method raises FtError on a non-zero status.
+    """
+
+    def __init__(self, V, R_max, N_max, *, dtype=FT_T_F32, stream=0):
+        self.h = None
+        st, h = beam_init(V, dtype, R_max, N_max, stream or None)
+        _check(st, "ft_beam_init")
+        self.h, self._lib = h, load()
+
+    def close(self):
+        if self.h:
+            beam_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def select(self, B, K, N, logits, ld, scores, out_scores, out_parents, out_tokens, *, rows=None, done=None, eos=-1,
+               out_done=None):
+        """The N best continuations of each of B requests of K beams, best first."""
+        st = self._lib.ft_beam_select(self.h, B, K, N, _ptr(logits), ld, _ptr(scores), _ptr(rows), _ptr(done), eos,
+                                      _ptr(out_scores), _ptr(out_parents), _ptr(out_tokens), _ptr(out_done))
+        if st:
+            _check(st, "ft_beam_select")
+
+    def status(self) -> int:
+        return beam_status(self.h)

@@ -113,6 +113,10 @@ cudaError_t launch_kv_extend(ft_kv* kv, int n, const int* rows, const int* add);
 cudaError_t launch_kv_fork(ft_kv* kv, int n, const int* parents, const int* children);
 cudaError_t launch_kv_free(ft_kv* kv, int n, const int* rows);
 cudaError_t launch_kv_compact(ft_kv* kv);
+cudaError_t launch_kv_reorder(ft_kv* kv, int n, const int* rows, const int* parents);
+cudaError_t launch_kv_batch(ft_kv* kv, int B, const int* rows, const int* add, int T, int* cu_q, int* row_of, int* pos,
+                            long long* slots);
+cudaError_t kv_pages_setup();  // the kernels' shared-memory limits, once per handle
 
 struct RopeArgs {
     const void* qkv;

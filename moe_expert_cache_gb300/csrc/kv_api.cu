@@ -150,7 +150,7 @@ ft_status ft_kv_init(ft_kv** out, int32_t L, int32_t Hq, int32_t Hkv, int32_t D,
     kv->plan.seg = (int*)(a + l.seg);
     kv->part_o = (float*)(a + l.part_o);
     kv->part_ml = (float2*)(a + l.part_ml);
-    if (!attn_encode_map(kv) || attn_setup(kv) != cudaSuccess) return fail(FT_ERR_CUDA);
+    if (!attn_encode_map(kv) || attn_setup(kv) != cudaSuccess || kv_pages_setup() != cudaSuccess) return fail(FT_ERR_CUDA);
     *out = kv;
     return FT_OK;
 }
@@ -173,6 +173,28 @@ ft_status ft_kv_free(ft_kv* kv, int32_t n, const int32_t* rows) {
 ft_status ft_kv_compact(ft_kv* kv) {
     if (!kv) return FT_ERR_ARG;
     return launched(launch_kv_compact(kv));
+}
+
+ft_status ft_kv_reorder(ft_kv* kv, int32_t n, const int32_t* rows, const int32_t* parents) {
+    if (!kv || n < 0 || n > kv->n_rows || n > 1024 || (n > 0 && !parents)) return FT_ERR_ARG;
+    return launched(launch_kv_reorder(kv, n, rows, parents));
+}
+
+ft_status ft_kv_batch(ft_kv* kv, int32_t B, const int32_t* rows, const int32_t* add, int32_t T, int32_t* cu_q,
+                      int32_t* row_of, int32_t* pos, int64_t* slots) {
+    if (!kv || B < 0 || B > kv->n_rows || T < 0 || !cu_q || (B > 0 && !add) || (T > 0 && (!row_of || !pos)) ||
+        misaligned(cu_q, 4) || misaligned(row_of, 4) || misaligned(pos, 4) || misaligned(slots, 8) || misaligned(rows, 4) ||
+        misaligned(add, 4))
+        return FT_ERR_ARG;
+    // outputs, then what must not overlap them
+    const struct { const void* p; size_t n; } m[] = {{cu_q, ((size_t)B + 1) * 4}, {row_of, (size_t)T * 4}, {pos, (size_t)T * 4},
+                                                     {slots, (size_t)T * 8}, {rows, (size_t)B * 4}, {add, (size_t)B * 4}};
+    for (int a = 0; a < 4; ++a)
+        for (int b = a + 1; b < 6; ++b)
+            if (m[a].p && m[b].p && m[a].n && m[b].n && (uintptr_t)m[a].p < (uintptr_t)m[b].p + m[b].n &&
+                (uintptr_t)m[b].p < (uintptr_t)m[a].p + m[a].n)
+                return FT_ERR_ARG;
+    return launched(launch_kv_batch(kv, B, rows, add, T, cu_q, row_of, pos, (long long*)slots));
 }
 
 ft_status ft_qk_rope_store(ft_kv* kv, int32_t layer, int32_t T, const void* qkv, int64_t ld, const int32_t* row_of,

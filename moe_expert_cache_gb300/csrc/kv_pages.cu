@@ -241,6 +241,261 @@ __global__ void __launch_bounds__(CT) kv_free_kernel(KvCtl c, int n, const int* 
     set_info(c, 0, 0, -1);
 }
 
+// ---- layout of a step
+
+// Largest i in [0, n) with start[i] <= x (start ascending from 0, x >= 0).
+__device__ __forceinline__ int owner_of(const int* start, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+struct BatchOut {
+    int *cu_q, *row_of, *pos;
+    long long* slots;
+    int T;
+};
+
+// Lists the tokens t0, t0 + step, ... of the requests whose first tokens are start[0..B) and whose rows have their
+// new lengths (old_lens: still the old ones).
+__device__ void list_tokens(const KvCtl& c, const BatchOut& o, int B, const int* rows, const int* add, const int* start,
+                            int total, bool old_lens, int t0, int step) {
+    for (long long t = t0; t < o.T; t += step) {
+        int r = -1, p = 0;
+        long long slot = -1;
+        if (t < total) {
+            const int b = owner_of(start, B, (int)t);
+            r = rows ? rows[b] : b;
+            p = c.lens[r] - (old_lens ? 0 : add[b]) + ((int)t - start[b]);
+            if (o.slots) slot = (long long)c.table[(size_t)r * c.row_pages + p / c.page] * c.page + p % c.page;
+        }
+        o.row_of[t] = r;
+        o.pos[t] = p;
+        if (o.slots) o.slots[t] = slot;
+    }
+}
+
+constexpr int BATCH_SMEM = 2048;  // requests whose first tokens and pages are kept in shared memory
+
+// Rows grow as in kv_extend_kernel; then, with list_here, one thread a token lists them.
+__global__ void __launch_bounds__(CT) kv_batch_kernel(KvCtl c, int B, const int* __restrict__ rows,
+                                                      const int* __restrict__ add, BatchOut o, int list_here) {
+    __shared__ int ws[32];
+    __shared__ long long wl[32];
+    __shared__ RowMarks marks;
+    __shared__ int s_tok[BATCH_SMEM], s_page[BATCH_SMEM];
+    clear(marks, c.n_rows);
+    ft::grid_dep_launch();
+    ft::grid_dep_wait();
+    const unsigned first = free_bits(c, 0);
+    const bool small = B <= BATCH_SMEM;
+    int* tok = small ? s_tok : o.cu_q;
+    int* pg = small ? s_page : c.rank;
+    int want = 0;
+    long long tokens = 0;
+    bool ok = true;
+    for (int base = 0; base < B; base += CT) {
+        const int i = base + threadIdx.x;
+        int need = 0, n = 0;
+        if (i < B) {
+            const int r = rows ? rows[i] : i, a = add[i];
+            if (mark(marks, r, c.n_rows)) {
+                const long long len = c.lens[r], to = len + a;
+                if (len < 0 || a < 0 || to > (long long)c.row_pages * c.page) {
+                    ok = false;
+                } else {
+                    n = a;
+                    need = (int)((to + c.page - 1) / c.page - (len + c.page - 1) / c.page);
+                }
+            } else {
+                ok = false;
+            }
+        }
+        long long tot_n;
+        int total;
+        const long long at_n = tokens + ft::block_scan((long long)n, wl, tot_n);
+        const int at = want + ft::block_scan(need, ws, total);
+        if (i < B) {
+            tok[i] = (int)min(at_n, (long long)o.T);
+            pg[i] = at;
+        }
+        tokens += tot_n;
+        want += total;
+        if (tokens > o.T) {  // (the same in all threads; the sum of pages stays in its range)
+            ok = false;
+            break;
+        }
+    }
+    unsigned bad = 0;
+    if (!__syncthreads_and(ok)) bad = FT_DEVERR_ARG;
+    else if (take_free(c, want, ws, first) < want) bad = FT_DEVERR_CAPACITY;
+    if (bad) {
+        refuse(c, bad);
+        tokens = 0;
+        for (int i = threadIdx.x; i <= B; i += CT) o.cu_q[i] = 0;
+    } else {
+        for (int w = threadIdx.x; w < want; w += CT) {
+            const int i = owner_of(pg, B, w);
+            const int r = rows ? rows[i] : i, p = c.free_list[w];
+            c.table[(size_t)r * c.row_pages + (c.lens[r] + c.page - 1) / c.page + (w - pg[i])] = p;
+            c.refs[p] = 1;
+        }
+        if (small)
+            for (int i = threadIdx.x; i < B; i += CT) o.cu_q[i] = tok[i];
+        if (threadIdx.x == 0) o.cu_q[B] = (int)tokens;
+        set_info(c, want, 0, -1);
+        __syncthreads();
+    }
+    if (list_here) list_tokens(c, o, B, rows, add, tok, (int)tokens, true, threadIdx.x, CT);
+    if (bad) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < B; i += CT) c.lens[rows ? rows[i] : i] += add[i];
+}
+
+__global__ void __launch_bounds__(256) kv_list_kernel(KvCtl c, int B, const int* __restrict__ rows,
+                                                      const int* __restrict__ add, BatchOut o) {
+    ft::grid_dep_launch();
+    ft::grid_dep_wait();
+    list_tokens(c, o, B, rows, add, o.cu_q, o.cu_q[B], false, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+}
+
+// ---- reordering
+
+constexpr int RO_MAX = 1024;           // rows of a call, one thread each
+constexpr int RO_STAGE = 40 * 1024;    // table entries staged at a time (160 KB)
+
+__global__ void __launch_bounds__(CT) kv_reorder_kernel(KvCtl c, int n, const int* __restrict__ rows,
+                                                        const int* __restrict__ parents) {
+    extern __shared__ int stage[];
+    __shared__ int ws[32];
+    __shared__ RowMarks marks;
+    // of each item: row, parent, pages it held, complete pages it gets, its last page (0: none, 1: kept, 2 + rank: new)
+    __shared__ int s_row[RO_MAX], s_par[RO_MAX], s_old[RO_MAX], s_full[RO_MAX], s_last[RO_MAX], s_keep[RO_MAX];
+    __shared__ int s_cols;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    clear(marks, c.n_rows);
+    ft::grid_dep_launch();
+    ft::grid_dep_wait();
+    const int i = threadIdx.x;
+    int r = -1, p = -1, len = 0;
+    bool ok = true;
+    if (threadIdx.x == 0) s_cols = 0;
+    __syncthreads();
+    if (i < n) {
+        r = rows ? rows[i] : i;
+        p = parents[i];
+        if (!mark(marks, r, c.n_rows) || p < -1 || p >= c.n_rows) {
+            ok = false;
+        } else {
+            const int old = c.lens[r];
+            len = p < 0 ? 0 : c.lens[p];
+            const long long most = (long long)c.row_pages * c.page;
+            if (old < 0 || old > most || len < 0 || len > most) {
+                ok = false;
+            } else {
+                s_row[i] = r;
+                s_par[i] = p;
+                s_old[i] = (old + c.page - 1) / c.page;
+                s_full[i] = len / c.page;
+                s_keep[i] = 0x7fffffff;
+                atomicMax(&s_cols, max(s_old[i], (len + c.page - 1) / c.page));
+                c.rank[r] = i;
+            }
+        }
+    }
+    if (!__syncthreads_and(ok)) return refuse(c, FT_DEVERR_ARG);
+    // the child that keeps the last page of a parent whose own row is in the list
+    int j = -1;
+    if (i < n && p >= 0 && (marks.w[p >> 5] >> (p & 31) & 1u)) {
+        j = c.rank[p];
+        atomicMin(&s_keep[j], p == r ? -1 : i);
+    }
+    __syncthreads();
+    const bool part = i < n && len % c.page != 0;
+    const bool keeps = j >= 0 && s_keep[j] == (p == r ? -1 : i);
+    int want;
+    const int at = ft::block_scan(part && !keeps ? 1 : 0, ws, want);
+    if (i < n) s_last[i] = !part ? 0 : keeps ? 1 : 2 + at;
+    __syncthreads();
+    // counts of the pages: those that the rows get, less those that they held.  A row that stays as it is is left out.
+    auto count = [&](int sign) {
+        for (int k = wid; k < n; k += CT / 32) {
+            if (s_row[k] == s_par[k]) continue;
+            const int got = s_full[k] + (s_last[k] == 1), held = s_old[k];
+            const int* from = c.table + (size_t)max(s_par[k], 0) * c.row_pages;
+            const int* mine = c.table + (size_t)s_row[k] * c.row_pages;
+            for (int q = lane; q < max(got, held); q += 32) {
+                if (q < got) atomicAdd(&c.refs[from[q]], sign);
+                if (q < held) atomicAdd(&c.refs[mine[q]], -sign);
+            }
+        }
+        __syncthreads();
+    };
+    for (int k = wid; k < n; k += CT / 32) {
+        if (s_row[k] == s_par[k]) continue;
+        const int got = s_full[k] + (s_last[k] != 0), held = s_old[k];
+        const int* from = c.table + (size_t)max(s_par[k], 0) * c.row_pages;
+        const int* mine = c.table + (size_t)s_row[k] * c.row_pages;
+        for (int q = lane; q < max(got, held); q += 32) {
+            if (q < got && (unsigned)from[q] >= (unsigned)c.n_pages) ok = false;
+            if (q < held && (unsigned)mine[q] >= (unsigned)c.n_pages) ok = false;
+        }
+    }
+    if (!__syncthreads_and(ok)) return refuse(c, FT_DEVERR_ARG);
+    count(1);
+    // a page that a row held without being counted
+    for (int k = wid; k < n; k += CT / 32) {
+        if (s_row[k] == s_par[k]) continue;
+        for (int q = lane; q < s_old[k]; q += 32)
+            if (__ldcg(&c.refs[c.table[(size_t)s_row[k] * c.row_pages + q]]) < 0) ok = false;
+    }
+    if (!__syncthreads_and(ok)) {
+        count(-1);
+        return refuse(c, FT_DEVERR_ARG);
+    }
+    if (want > 0 && take_free(c, want, ws, free_bits(c, 0)) < want) {
+        count(-1);
+        return refuse(c, FT_DEVERR_CAPACITY);
+    }
+    // the rows, some columns at a time: all are read before one is written
+    const int cols = s_cols;
+    int tile = RO_STAGE / max(n, 1);
+    if (tile > cols) tile = cols;
+    for (int c0 = 0; c0 < cols; c0 += tile) {
+        const int w = min(tile, cols - c0);
+        for (int k = wid; k < n; k += CT / 32) {
+            if (s_row[k] == s_par[k]) continue;
+            const int* from = c.table + (size_t)max(s_par[k], 0) * c.row_pages + c0;
+            const int got = s_full[k] + (s_last[k] != 0) - c0;
+            for (int q = lane; q < min(w, got); q += 32) stage[k * tile + q] = from[q];
+        }
+        __syncthreads();
+        for (int k = wid; k < n; k += CT / 32) {
+            if (s_row[k] == s_par[k]) continue;
+            int* to = c.table + (size_t)s_row[k] * c.row_pages + c0;
+            const int full = s_full[k] - c0, last = s_last[k], end = max(s_old[k], s_full[k] + (last != 0)) - c0;
+            for (int q = lane; q < min(w, end); q += 32) {
+                int v = -1;
+                if (q < full || (q == full && last == 1)) {
+                    v = stage[k * tile + q];
+                } else if (q == full && last >= 2) {
+                    v = c.free_list[last - 2];
+                    c.refs[v] = 1;
+                    c.copies[last - 2] = KvCopy{stage[k * tile + q], v, c.lens[s_par[k]] % c.page};
+                }
+                to[q] = v;
+            }
+        }
+        __syncthreads();
+    }
+    if (i < n) c.lens[r] = len;
+    set_info(c, want, want, -1);
+}
+
 // live = pages in use; the k-th page in use at index >= live pairs with the
 // k-th free page below it (there are equally many).  The two lists fill the
 // copy list's ends independently, so both scans are one pass over refs.
@@ -353,6 +608,31 @@ cudaError_t launch_kv_free(ft_kv* kv, int n, const int* rows) {
     KvCtl c = ctl_of(kv);
     void* args[] = {&c, &n, &rows};
     return launch_dependent((const void*)kv_free_kernel, 1, CT, 0, kv->stream, args);
+}
+
+cudaError_t launch_kv_batch(ft_kv* kv, int B, const int* rows, const int* add, int T, int* cu_q, int* row_of, int* pos,
+                            long long* slots) {
+    KvCtl c = ctl_of(kv);
+    BatchOut o{cu_q, row_of, pos, slots, T};
+    int here = T <= 4096;
+    void* args[] = {&c, &B, &rows, &add, &o, &here};
+    const cudaError_t e = launch_dependent((const void*)kv_batch_kernel, 1, CT, 0, kv->stream, args);
+    if (e != cudaSuccess || here) return e;
+    void* list[] = {&c, &B, &rows, &add, &o};
+    const int ctas = (T + 255) / 256;
+    return launch_dependent((const void*)kv_list_kernel, ctas < kv->num_sms * 8 ? ctas : kv->num_sms * 8, 256, 0, kv->stream,
+                            list);
+}
+
+cudaError_t launch_kv_reorder(ft_kv* kv, int n, const int* rows, const int* parents) {
+    KvCtl c = ctl_of(kv);
+    void* args[] = {&c, &n, &rows, &parents};
+    const cudaError_t e = launch_dependent((const void*)kv_reorder_kernel, 1, CT, RO_STAGE * 4, kv->stream, args);
+    return e == cudaSuccess && n > 0 ? launch_copy(kv, false, n) : e;
+}
+
+cudaError_t kv_pages_setup() {
+    return cudaFuncSetAttribute((const void*)kv_reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RO_STAGE * 4);
 }
 
 cudaError_t launch_kv_compact(ft_kv* kv) {

@@ -1,0 +1,55 @@
+"""The norms around a block and beam search's selection in fp64.
+
+Written from the definitions, one row at a time, on numpy arrays; shares no code
+with the library.
+"""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+
+
+def unit(x, eps):
+    """A row over its root mean square."""
+    x = np.asarray(x, dtype=np.float64)
+    return x / math.sqrt(math.fsum(x * x) / len(x) + eps)
+
+
+def block_norm(block, resid, *, gate=None, post_norm=False, post=None, pre=None, eps=1e-6, resid_scale=1.0,
+               block_scale=1.0):
+    """One token: (h, out) of rows block (None: no block) and resid; gate is None, a number or a row."""
+    h = resid_scale * np.asarray(resid, dtype=np.float64)
+    if block is not None:
+        z = unit(block, eps) if post_norm else np.asarray(block, dtype=np.float64)
+        if post_norm and post is not None:
+            z = z * np.asarray(post, dtype=np.float64)
+        if gate is not None:
+            z = z * np.asarray(gate, dtype=np.float64)
+        h = h + block_scale * z
+    out = unit(h, eps)
+    return h, out if pre is None else out * np.asarray(pre, dtype=np.float64)
+
+
+def beam_select(logits, scores, N, *, done=None, eos=-1, rows=None, first_row=0):
+    """One request of K beams: logits [K, V], scores [K].  Returns a list of N tuples (score, parent, token, done),
+    (-inf, -1, -1, 0) where there are no more candidates."""
+    found = []
+    for k, (x, s) in enumerate(zip(np.asarray(logits, dtype=np.float64), scores)):
+        s = float(s)
+        if s == -math.inf or math.isnan(s) or s == math.inf:
+            continue
+        if done is not None and done[k]:
+            found.append((-s, k, eos))
+            continue
+        if np.isnan(x).any() or (x == math.inf).any() or not (x > -math.inf).any():
+            continue
+        m = x.max()
+        total = math.log(math.fsum(np.exp(x - m)))
+        # only a beam's N best can be among the request's N best
+        for v in np.argsort(-x, kind="stable")[:N]:
+            if x[v] > -math.inf:
+                found.append((-(s + ((x[v] - m) - total)), k, int(v)))
+    found.sort()
+    out = [(-s, first_row + k if rows is None else int(rows[k]), v, int(v == eos)) for s, k, v in found[:N]]
+    return out + [(-math.inf, -1, -1, 0)] * (N - len(out))

@@ -67,6 +67,61 @@ class Pages:
             self.rows[c], self.lens[c] = new, self.lens[p]
         return copies
 
+    def reorder(self, rows, parents):
+        self._check_rows(rows)
+        if any(p < -1 or p >= self.n_rows for p in parents):
+            raise Refused("device")
+        old_rows, old_lens, old_refs = [list(r) for r in self.rows], list(self.lens), list(self.refs)
+        # which item keeps its parent's incomplete page: the parent's own row, else the first in the list
+        keeper = {}
+        for i, (r, p) in enumerate(zip(rows, parents)):
+            if p in rows and (p == r or p not in keeper):
+                keeper[p] = i
+        new, wanting = [], []
+        for i, p in enumerate(parents):
+            full, part = divmod(old_lens[p], self.page) if p >= 0 else (0, 0)
+            pages = list(old_rows[p][:full]) if p >= 0 else []
+            if part and keeper.get(p) == i:
+                pages.append(old_rows[p][full])
+            elif part:
+                wanting.append((i, old_rows[p][full], part))
+            new.append(pages)
+        for r in rows:
+            for x in old_rows[r]:
+                self.refs[x] -= 1
+        for pages in new:
+            for x in pages:
+                self.refs[x] += 1
+        try:
+            got = self._free_pages(len(wanting))
+        except Refused:
+            self.refs = old_refs
+            raise
+        copies = []
+        for (i, src, part), x in zip(wanting, got):
+            new[i].append(x)
+            self.refs[x] = 1
+            copies.append((src, x, part))
+        for r, p, pages in zip(rows, parents, new):
+            self.rows[r], self.lens[r] = pages, old_lens[p] if p >= 0 else 0
+        return copies
+
+    def batch(self, rows, add, T):
+        """extend, and the lists of its new tokens: (cu_q, row_of, pos, slots), padded to T."""
+        if any(a < 0 for a in add) or sum(add) > T:
+            raise Refused("device")
+        old = [self.lens[r] if 0 <= r < self.n_rows else 0 for r in rows]
+        self.extend(rows, add)
+        cu, row_of, pos, slots = [0], [], [], []
+        for r, a, n in zip(rows, add, old):
+            cu.append(cu[-1] + a)
+            for i in range(n, n + a):
+                row_of.append(r)
+                pos.append(i)
+                slots.append(self.rows[r][i // self.page] * self.page + i % self.page)
+        pad = T - len(pos)
+        return cu, row_of + [-1] * pad, pos + [0] * pad, slots + [-1] * pad
+
     def free(self, rows):
         self._check_rows(rows)
         for r in rows:

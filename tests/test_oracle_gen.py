@@ -1,0 +1,138 @@
+"""Pins of the oracle of norms, beam selection, row reordering and batch layout."""
+import itertools
+import math
+import random
+
+import numpy as np
+import pytest
+
+from oracle import gen, kv as okv
+
+
+def test_block_norm_by_hand():
+    h, y = gen.block_norm([3.0, 4.0], [1.0, -1.0], eps=0.0, block_scale=2.0, resid_scale=3.0)
+    assert h.tolist() == [9.0, 5.0]
+    r = math.sqrt((81 + 25) / 2)
+    assert np.allclose(y, [9 / r, 5 / r], rtol=1e-15)
+    # root mean square of (3, 4) is sqrt(12.5)
+    h, _ = gen.block_norm([3.0, 4.0], [0.0, 0.0], eps=0.0, post_norm=True, post=[1.0, 2.0], gate=[0.5, 0.25])
+    assert np.allclose(h, [1.5 / math.sqrt(12.5), 2 / math.sqrt(12.5)], rtol=1e-15)
+    h, y = gen.block_norm(None, [0.0, 0.0], eps=1e-6, pre=[5.0, 5.0])
+    assert h.tolist() == [0, 0] and y.tolist() == [0, 0]
+    # scale does not change a norm without eps
+    a, b = gen.unit([1.0, 2.0, -2.0], 0.0), gen.unit([1e3, 2e3, -2e3], 0.0)
+    assert np.allclose(a, b, rtol=1e-15) and abs((a * a).mean() - 1) < 1e-15
+
+
+def _all_candidates(x, s, done, eos):
+    out = []
+    for k in range(len(s)):
+        if s[k] == -math.inf:
+            continue
+        if done and done[k]:
+            out.append((s[k], k, eos))
+            continue
+        p = [math.exp(v) if v > -math.inf else 0.0 for v in x[k]]
+        for v, q in enumerate(p):
+            if q:
+                out.append((s[k] + math.log(q / sum(p)), k, v))
+    return out
+
+
+def test_beam_select_against_all_candidates():
+    r = random.Random(1)
+    for _ in range(200):
+        K, V, N = r.randint(1, 4), r.randint(1, 7), r.randint(1, 9)
+        x = [[r.choice([-math.inf, r.gauss(0, 2)]) for _ in range(V)] for _ in range(K)]
+        s = [r.choice([-math.inf, -r.random(), -r.random()]) for _ in range(K)]
+        eos = r.randrange(V)
+        done = r.choice([None, [r.random() < 0.4 for _ in range(K)]])
+        want = sorted(_all_candidates(x, s, done, eos), key=lambda c: -c[0])[:N]
+        got = gen.beam_select(x, s, N, done=done, eos=eos)
+        assert len(got) == N
+        assert [(p, v) for _, p, v, _ in got[:len(want)]] == [(k, v) for _, k, v in want]
+        assert all(abs(a[0] - b[0]) < 1e-12 for a, b in zip(got, want))
+        assert all(g == (-math.inf, -1, -1, 0) for g in got[len(want):])
+        assert all(d == (v == eos) for _, _, v, d in got[:len(want)])
+
+
+def test_beam_select_ties_and_bad_rows():
+    x = [[0.0, 1.0, 1.0], [1.0, 0.0, 1.0]]
+    assert [g[1:3] for g in gen.beam_select(x, [0.0, 0.0], 4)] == [(0, 1), (0, 2), (1, 0), (1, 2)]
+    assert [g[1:3] for g in gen.beam_select([[math.nan, 1.0], [math.inf, 0.0], [0.0, 1.0]], [0.0] * 3, 3)] == \
+        [(2, 1), (2, 0), (-1, -1)]
+    assert [g[1] for g in gen.beam_select(x, [0.0, 0.0], 2, rows=[7, 5])] == [7, 7]
+
+
+def test_reorder_by_hand():
+    m = okv.Pages(8, 4, 3, 4)
+    m.extend([0, 1], [6, 5])          # row 0: pages 0, 1; row 1: pages 2, 3
+    assert m.rows[:2] == [[0, 1], [2, 3]]
+    # both go on from row 1: row 1 keeps its last page, row 0 gets a copy on the lowest page that is now free
+    assert m.reorder([0, 1], [1, 1]) == [(3, 0, 1)]
+    assert m.rows[:2] == [[2, 0], [2, 3]] and m.lens[:2] == [5, 5] and m.refs == [1, 0, 2, 1, 0, 0, 0, 0]
+    # they change places: each keeps the other's last page
+    assert m.reorder([0, 1], [1, 0]) == []
+    assert m.rows[:2] == [[2, 3], [2, 0]]
+    # a parent that is not in the list keeps its own; -1 empties
+    assert m.reorder([2, 1], [0, -1]) == [(3, 0, 1)]
+    assert m.rows == [[2, 3], [], [2, 0], []] and m.lens == [5, 0, 5, 0]
+    for bad in (([0, 0], [1, 1]), ([0], [4]), ([0], [-2]), ([4], [0])):
+        with pytest.raises(okv.Refused):
+            m.reorder(*bad)
+
+
+def test_reorder_keeps_every_token():
+    """Each row's tokens, as the pages hold them, are its parent's tokens."""
+    r = random.Random(3)
+    for _ in range(60):
+        page, rows, n_pages = r.choice([2, 4]), 5, 24
+        m = okv.Pages(n_pages, rows, 6, page)
+        pool = np.full((n_pages, 1, 1, 1, page, 1), -1)
+        fresh = itertools.count()
+        for _ in range(12):
+            who = r.sample(range(rows), r.randint(0, rows))
+            try:
+                add = [r.randint(0, 3) for _ in who]
+                old = list(m.lens)
+                m.extend(who, add)
+                for w, a in zip(who, add):
+                    for t in range(old[w], old[w] + a):
+                        pool[m.rows[w][t // page], 0, 0, 0, t % page, 0] = next(fresh)
+            except okv.Refused:
+                pass
+
+            def text(i):
+                return [int(pool[m.rows[i][t // page], 0, 0, 0, t % page, 0]) for t in range(m.lens[i])]
+            before = [text(i) for i in range(rows)]
+            who = r.sample(range(rows), r.randint(0, rows))
+            par = [r.randint(-1, rows - 1) for _ in who]
+            try:
+                copies = m.reorder(who, par)
+            except okv.Refused:
+                assert [text(i) for i in range(rows)] == before
+                continue
+            okv.copy_pages(pool, copies)
+            for i in range(rows):
+                want = before[i] if i not in who else [] if par[who.index(i)] < 0 else before[par[who.index(i)]]
+                assert text(i) == want
+            count = [0] * n_pages
+            for pages in m.rows:
+                for p in pages:
+                    count[p] += 1
+            assert count == m.refs
+            # no two rows share a page that is still written
+            last = [m.rows[i][-1] for i in range(rows) if m.lens[i] % page]
+            assert len(set(last)) == len(last) and all(m.refs[p] == 1 for p in last)
+
+
+def test_batch_by_hand():
+    m = okv.Pages(8, 3, 3, 4)
+    m.extend([2], [3])
+    assert m.batch([2, 0, 1], [2, 0, 5], 9) == ([0, 2, 2, 7], [2, 2, 1, 1, 1, 1, 1, -1, -1], [3, 4, 0, 1, 2, 3, 4, 0, 0],
+                                                [3, 4, 8, 9, 10, 11, 12, -1, -1])
+    assert m.lens == [0, 5, 5]
+    for bad in (([0, 1], [1, 1], 1), ([0], [-1], 4), ([0, 0], [1, 1], 4), ([0], [13], 20)):
+        with pytest.raises(okv.Refused):
+            m.batch(*bad)
+    assert m.lens == [0, 5, 5]
