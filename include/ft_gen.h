@@ -86,7 +86,6 @@ size_t ft_beam_scratch_bytes(int32_t V, int32_t dtype, int32_t R_max, int32_t N_
  *   dtype   FT_T_* of the logits.
  *   R_max   largest number of rows (requests x beams) of a call, 1..65536.
  *   N_max   largest number of candidates that a call asks of a request, 1..64.
- *           R_max * ceil(V / 8192) * N_max below 2^31.
  *   stream  cudaStream_t that every call runs on; it must outlive the handle.
  * Errors: FT_ERR_ARG, FT_ERR_OOM, FT_ERR_CUDA.
  */
@@ -127,7 +126,8 @@ ft_status ft_beam_select(ft_beam* bm, int32_t B, int32_t K, int32_t N, const voi
                          int32_t* out_parents, int32_t* out_tokens, int32_t* out_done);
 
 /* Synchronise the stream and return, then clear, what the device latched since
- * the last call: FT_OK or FT_ERR_DEVICE. */
+ * the last call: FT_OK, FT_ERR_DEVICE or FT_ERR_TIMEOUT (a bounded wait gave up;
+ * outputs since the last status are not valid). */
 ft_status ft_beam_status(ft_beam* bm);
 
 /* Free the handle and its scratch.  Syncs.  bm may be NULL. */

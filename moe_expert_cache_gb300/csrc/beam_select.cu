@@ -3,17 +3,19 @@
 //   score(k, v) = s_k + x_kv - lse_k,   lse_k = log(sum over u of exp x_ku)
 //
 // Bound: HBM for large batches (the logits are read once), latency for small
-// ones.  One kernel.  A CTA takes a chunk of one row into registers, sums the
-// exponentials and finds the chunk's N largest logits; the CTA of a request
-// that finishes last joins the chunks' sums to lse_k and takes the N best of the
-// K * chunks * N that are left.
+// ones.  Two kernels.  In the first every warp takes a chunk of one row by itself:
+// in one pass it sums the exponentials and finds, of the chunk's 16-byte vectors,
+// the N with the largest maxima.  The N largest values lie in those: each of N
+// vectors that come before another one has a value that comes before all of its.
+// In the second kernel a CTA a request joins the chunks' sums to lse_k, takes the N
+// best of the K * chunks * N vectors that are left, and of their values the N best.
 //
-// N largest without a sort: the N-th largest of the maxima of 64 groups of a
-// chunk is at most the N-th largest value of the chunk, and few values reach it.
-// Those are collected and ranked by counting, on keys that no two values share
-// (value, then place), so the order does not depend on timing.  Within a row
-// logits are compared as they are; scores of different rows are compared in 64
-// bits.
+// N largest without a sort: the N-th largest of the maxima of 32 or 128 groups is
+// at most the N-th largest of all, and few reach it.  Those are collected, the bar
+// is raised to the N-th of them now and then, and what is left is ranked by
+// counting, on keys that no two share (value, then place), so the order does not
+// depend on timing.  Within a row logits are compared as they are; scores of
+// different rows are compared in 64 bits.
 #include "ft_kv.cuh"
 #include "../../include/ft_gen.h"
 
@@ -28,25 +30,32 @@ struct ft_beam {
     cudaStream_t stream;
     void* arena;
     unsigned* err;
-    unsigned* arrived;     // [R_max] CTAs of a request that have finished; 0 at rest
     struct BeamSum* sums;  // [lists]
     uint64_t* keys;        // [lists][N_max]
     long long lists;       // chunks of all rows
 };
 
-// Sum over a chunk: l * e^m.
-struct BeamSum {
-    double m;
-    float l;
-    int pad;
+// Sum of exponentials over a part of a row: l * 2^ref, or l * e^ref where far.
+struct __align__(16) BeamSum {
+    float ref, l;
+    int far, pad;
 };
 
 namespace {
 
-constexpr int CT = 256;     // threads of a CTA
-constexpr int GROUPS = 64;  // quads of lanes
-constexpr int CAP = 1024;   // candidates that are ranked at once
+constexpr int SCAN_CT = 128;       // threads of a CTA of the first kernel
+constexpr int SCAN_WARPS = SCAN_CT / 32;
+constexpr int PER_SM = 7;          // its CTAs of an SM
+constexpr int NJ = 4;              // vectors of a lane in a tile
+constexpr int TILE = 32 * NJ;      // vectors of a tile
+constexpr int STAGES = 3;          // tiles of a warp in shared memory
+constexpr int WCAP = 128;          // candidates of a warp
+constexpr int CT = 512;            // threads of a CTA of the second kernel
+constexpr int WARPS = CT / 32;
+constexpr int CAP = 1024;          // candidates that it ranks at once
+constexpr int HELD = 8;            // vectors' keys that a thread of it holds
 constexpr int MAX_N = 64, MAX_K = 64;
+constexpr int MAX_V = 2 * MAX_N;   // vectors whose values it looks at
 constexpr float LOG2E = 1.44269504088896340736f;  // rounded to fp32; used in both directions, so its error cancels
 
 struct SelParams {
@@ -58,9 +67,10 @@ struct SelParams {
     float* out_scores;
     int *out_parents, *out_tokens, *out_done;
     int V, K, N, C, eos;
+    int vpc, items;        // vectors of a chunk; chunks of all rows
+    int raise;             // candidates of a warp beyond which it raises its bar
     BeamSum* sums;
     uint64_t* keys;
-    unsigned* arrived;
     unsigned* err;
 };
 
@@ -76,6 +86,28 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Pairs of fp32 values in 64-bit registers.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 // Values of a 16-byte vector.
@@ -95,6 +127,22 @@ __device__ __forceinline__ void unpack(const uint4& v, float* f) {
             f[2 * i + 1] = t.y;
         }
     }
+}
+
+// Their largest (a NaN counts for nothing).
+template <int TYPE>
+__device__ __forceinline__ float max_of(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (TYPE == FT_T_F32)
+        return fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])), fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
+    if (TYPE == FT_T_BF16) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(w);
+        const float2 t = __bfloat1622float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+        return fmaxf(t.x, t.y);
+    }
+    const __half2* h = reinterpret_cast<const __half2*>(w);
+    const float2 t = __half22float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+    return fmaxf(t.x, t.y);
 }
 
 // The vector of values i..i+VEC-1 of a row of V, of which some are outside it: those are -inf.
@@ -119,283 +167,430 @@ __device__ uint4 load_edge(const void* row, long long i, int V) {
     return v;
 }
 
-struct ScanSmem {
-    float group[GROUPS];
-    double wm[CT / 32];
-    float wl[CT / 32];
-    float bar;
-    int n;
-    uint64_t list[CAP];
-};
 struct JoinSmem {
     // score = base + (x - top) with lse = top + log l, base = s - log l, so that logits of any size keep their
     // differences; of an ended beam s and 0; base -inf: no candidates
     double base[MAX_K], top[MAX_K];
+    float fbase[MAX_K], ftop[MAX_K];  // the same in fp32
     bool ended[MAX_K];
-    float group[GROUPS];
+    alignas(16) float group[CT];
     float bar;
-    int n;
-    double score[CAP];
-    uint64_t at[CAP];    // beam << 32 | token
+    int n, m;
+    uint64_t score[CAP + MAX_K];  // order of the score
+    uint64_t at[CAP + MAX_K];     // beam << 32 | place
+    uint64_t vec[MAX_V];  // vectors whose values are taken: beam << 32 | place
 };
 
-// The N-th largest of the groups' maxima (N <= GROUPS), by counting; call by whole warps 0 and 1.
-__device__ __forceinline__ void nth_of_groups(const float* group, int N, float* bar) {
+// Order of doubles as unsigned integers, and back.
+__device__ __forceinline__ uint64_t ord64(double d) {
+    const uint64_t u = (uint64_t)__double_as_longlong(d);
+    return u ^ (u >> 63 ? ~0ull : 1ull << 63);
+}
+__device__ __forceinline__ double unord64(uint64_t o) {
+    return __longlong_as_double((long long)(o ^ (o >> 63 ? 1ull << 63 : ~0ull)));
+}
+
+// The N-th largest of the maxima of G groups (N <= G, a multiple of 32), by counting; call by the first G threads.
+__device__ __forceinline__ void nth_of_groups(const float* group, int G, int N, float* bar) {
     const int g = threadIdx.x;
     const float mine = group[g];
     int rank = 0;
-#pragma unroll 8
-    for (int j = 0; j < GROUPS; ++j) {
-        const float o = group[j];
-        rank += o > mine || (o == mine && j < g);
+#pragma unroll 4
+    for (int j = 0; j < G; j += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(group + j);
+        rank += o.x > mine || (o.x == mine && j < g);
+        rank += o.y > mine || (o.y == mine && j + 1 < g);
+        rank += o.z > mine || (o.z == mine && j + 2 < g);
+        rank += o.w > mine || (o.w == mine && j + 3 < g);
     }
     if (rank == N - 1) *bar = mine;
 }
 
-// The chunk's sum and its N largest values to the workspace.
-template <int TYPE, int NJ>
-__device__ void scan_chunk(const SelParams& p, const void* row, int chunk, long long list, ScanSmem& s) {
-    constexpr int VEC = TYPE == FT_T_F32 ? 4 : 8, SIZE = TYPE == FT_T_F32 ? 4 : 2;
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    // vectors are aligned in memory: the first of a row may start before it
-    const int shift = (int)((uintptr_t)row % 16) / SIZE;
-    const long long i0 = (long long)chunk * (CT * VEC * NJ) + threadIdx.x * VEC - shift;
-    uint4 v[NJ];
+// The same within a warp: of the lanes' maxima m, or, for many, of their vectors' maxima g.
+__device__ __forceinline__ float nth_of_warp(const float (&g)[NJ], float m, int N, float* sh) {
+    const int lane = threadIdx.x & 31;
+    const bool all = N > 16;
+    sh[lane] = all ? g[0] : m;
+    if (all)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        const long long i = i0 + (long long)j * (CT * VEC);
-        if (i >= 0 && i + VEC <= p.V) v[j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + i * SIZE));
-        else v[j] = load_edge<TYPE>(row, i, p.V);
+        for (int j = 1; j < NJ; ++j) sh[32 * j + lane] = g[j];
+    __syncwarp();
+    float bar = -INFINITY;
+#pragma unroll 1
+    for (int j = 0; j < (all ? NJ : 1); ++j) {
+        const float mine = sh[32 * j + lane];
+        const int at = 32 * j + lane;
+        int rank = 0;
+#pragma unroll 2
+        for (int i = 0; i < (all ? 32 * NJ : 32); i += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(sh + i);
+            rank += o.x > mine || (o.x == mine && i < at);
+            rank += o.y > mine || (o.y == mine && i + 1 < at);
+            rank += o.z > mine || (o.z == mine && i + 2 < at);
+            rank += o.w > mine || (o.w == mine && i + 3 < at);
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, rank == N - 1);
+        if (who) bar = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
     }
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        float f[VEC];
-        unpack<TYPE>(v[j], f);
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) m = fmaxf(m, f[k]);
+    __syncwarp();
+    return bar;
+}
+
+// The maxima of groups of threads of a CTA, of each thread's m: so many groups that there are four and more for each of
+// the N (fewer let many more reach the bar).  Returns their number.
+__device__ __forceinline__ int store_groups(float* group, float m, int N) {
+    const int G = N <= 16 ? 64 : N <= 32 ? 128 : 256, per = CT / G;
+    for (int o = 1; o < per; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (threadIdx.x % per == 0) group[threadIdx.x / per] = m;
+    return G;
+}
+
+// The sum of n parts, by a warp; of `step` lanes each takes parts lane, lane + step, ...  A part that is 0 (it has no value)
+// has no say in the reference.  Differences of references are exact in fp32 but where a far part meets one that is not.
+// (fp64 runs at a 64th of fp32's rate or less here, so it is kept out of what every CTA does.)
+template <int STEP, class F>
+__device__ __forceinline__ BeamSum join_sums(F part, int n) {
+    const int lane = threadIdx.x & 31;
+    float cf = -INFINITY, cn = -INFINITY;  // largest reference of each kind
+    for (int i = lane % STEP; i < n; i += STEP) {
+        const BeamSum t = part(i);
+        if (t.l != 0.f) (t.far ? cf : cn) = fmaxf(t.far ? cf : cn, t.ref);
     }
-    float g = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-    if ((lane & 3) == 0) s.group[threadIdx.x >> 2] = g;
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-    if (threadIdx.x == 0) s.n = 0;
-    // Sum of exponentials on the warp's reference: 2^(x log2(e) - c) with c a whole number near the largest exponent, so
-    // that each exponent is rounded once.  The reference in x is c / log2(e) with the same constant.  Values whose
-    // exponents an fp32 cannot hold to a fraction are taken by differences from the largest.
-    double ref = 0.;
+    for (int o = 1; o < STEP; o <<= 1) {
+        cf = fmaxf(cf, __shfl_xor_sync(0xffffffffu, cf, o));
+        cn = fmaxf(cn, __shfl_xor_sync(0xffffffffu, cn, o));
+    }
+    // a far reference of 2^20 and more decides, one below -2^20 only where there is no other
+    const bool far = cf > 0.f || (cf > -INFINITY && cn == -INFINITY);
+    const float ref = far ? cf : cn == -INFINITY ? 0.f : cn;
     float l = 0.f;
-    if (fabsf(g) <= 1048576.f || g == -INFINITY) {
-        const float c = g == -INFINITY ? 0.f : rintf(g * LOG2E);
-        float l1 = 0.f;
+    for (int i = lane % STEP; i < n; i += STEP) {
+        const BeamSum t = part(i);
+        if (t.l == 0.f) continue;
+        float d;
+        if (t.far == (int)far) d = far ? (t.ref - ref) * LOG2E : t.ref - ref;
+        else if (far) d = (float)(t.ref - (double)ref * (double)LOG2E);
+        else d = (float)((double)t.ref * (double)LOG2E - ref);
+        l += t.l * ex2(d);
+    }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            float f[VEC];
-            unpack<TYPE>(v[j], f);
+    for (int o = 1; o < STEP; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    return BeamSum{ref, l, far, 0};
+}
+
+// A warp's list shrinks to its N best, in order; returns their number.
+__device__ __noinline__ int compact_list(uint64_t* list, int cnt, int N) {
+    const int lane = threadIdx.x & 31;
+    uint64_t k[WCAP / 32];
+    int rank[WCAP / 32] = {};
+    __syncwarp();
 #pragma unroll
-            for (int k = 0; k < VEC; k += 2) {
-                l += ex2(fmaf(f[k], LOG2E, -c));
-                l1 += ex2(fmaf(f[k + 1], LOG2E, -c));
+    for (int u = 0; u < WCAP / 32; ++u) k[u] = u * 32 + lane < cnt ? list[u * 32 + lane] : 0;
+    if (cnt <= 32) {
+#pragma unroll 4
+        for (int i = 0; i < cnt; ++i) rank[0] += list[i] > k[0];
+    } else {
+        for (int i = 0; i < cnt; ++i) {
+            const uint64_t o = list[i];
+#pragma unroll
+            for (int u = 0; u < WCAP / 32; ++u) rank[u] += o > k[u];
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < WCAP / 32; ++u)
+        if (u * 32 + lane < cnt && rank[u] < N) list[rank[u]] = k[u];
+    __syncwarp();
+    return min(cnt, N);
+}
+
+__device__ __forceinline__ uint64_t key_of(float f, int i) {
+    return (uint64_t)ord(f + 0.f) << 32 | (0xffffffffu - (uint32_t)i);  // (-0 equals 0)
+}
+
+// Vector q of a row, counted from the aligned address at or before its start, `shift` values before it.
+template <int TYPE>
+__device__ __forceinline__ uint4 load_vector(const uint8_t* row, int q, int shift, int V) {
+    constexpr int VEC = TYPE == FT_T_F32 ? 4 : 8, SIZE = TYPE == FT_T_F32 ? 4 : 2;
+    const int i = q * VEC - shift;
+    if (i >= 0 && i + VEC <= V) return __ldcs(reinterpret_cast<const uint4*>(row + (long long)i * SIZE));
+    return load_edge<TYPE>(row, i, V);
+}
+
+struct ScanSmem {
+    uint8_t ring[SCAN_WARPS][STAGES][TILE * 16];
+    uint64_t list[SCAN_WARPS][WCAP];
+    alignas(16) float group[SCAN_WARPS][TILE];
+    uint64_t bars[SCAN_WARPS][STAGES];
+};
+
+// Each warp: a chunk's sum and its N best vectors to the workspace.  Tiles that lie within the chunk and the row come by
+// bulk copies into STAGES places in shared memory, the next ones in flight while one is worked on; the few others (a
+// row's first and last) are loaded when their turn comes.
+template <int TYPE>
+__global__ void __launch_bounds__(SCAN_CT, PER_SM) beam_scan_kernel(const SelParams p) {
+    constexpr int VEC = TYPE == FT_T_F32 ? 4 : 8, SIZE = TYPE == FT_T_F32 ? 4 : 2;
+    extern __shared__ __align__(128) uint8_t smem[];
+    ScanSmem& s = *reinterpret_cast<ScanSmem*>(smem);
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    uint64_t* bars = s.bars[wid];
+    uint64_t* list = s.list[wid];
+    if (lane == 0) {
+        for (int i = 0; i < STAGES; ++i) ft::mbar_init(bars + i, 1);
+        ft::mbar_fence_init();
+    }
+    __syncwarp();
+    ft::grid_dep_launch();
+    ft::grid_dep_wait();
+    const int item = blockIdx.x * SCAN_WARPS + wid;
+    if (item >= p.items) return;
+    const int r = item / p.C;
+    const float score = p.scores[r];
+    const int ended = p.done ? p.done[r] : 0;
+    if (!(score > -INFINITY) || ended) return;  // no candidates, or one that is not in the logits
+    // vectors q..q1-1, counted from the aligned address at or before the row's start, `shift` values before it
+    const uint8_t* row = static_cast<const uint8_t*>(p.logits) + r * p.ld * SIZE;
+    const int shift = (int)((uintptr_t)row % 16) / SIZE;
+    int q = (item - r * p.C) * p.vpc;
+    const int q1 = min(q + p.vpc, (p.V + shift + VEC - 1) / VEC);
+    // tiles at q < w0 or >= w1 are not whole
+    const int w0 = shift ? 1 : 0, w1 = min(q1, (p.V + shift) / VEC) - TILE + 1;
+    int ahead = q, asked = 0, got = 0;
+    auto ask = [&] {  // for the next whole tile, if there is one
+        if (ahead < w0) ahead += TILE;
+        if (ahead < w1) {
+            if (lane == 0) {
+                const int st = asked % STAGES;
+                ft::mbar_arrive_expect_tx(bars + st, TILE * 16);
+                ft::bulk_g2s(s.ring[wid][st], row + (long long)ahead * 16 - shift * SIZE, TILE * 16, bars + st);
+            }
+            ++asked;
+            ahead += TILE;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) ask();
+
+    // Sum of exponentials, 2^(x log2(e) - c) with c a whole number near the first tile's largest exponent, so that each
+    // exponent is rounded once; the reference in x is c / log2(e) with the same constant.  Beyond 2^20 an fp32 does not
+    // hold an exponent to a fraction, and terms are taken by their difference from the largest value g.
+    // A value above `limit` asks for a new reference: any value at first, later those whose terms would grow too large.
+    bool set = false, far = false;
+    float c = 0.f, g = 0.f, l0 = 0.f, l1 = 0.f, limit = -INFINITY;
+    // Candidates: values from `bar` on whose key is above `own`.
+    float bar = 0.f;
+    uint64_t own = 0;
+    int cnt = 0;
+    bool barred = false;
+    for (; q < q1; q += TILE) {
+        uint4 v[NJ];
+        if (q >= w0 && q < w1) {
+            const int st = got % STAGES;
+            ft::mbar_wait(bars + st, (got / STAGES) & 1, p.err);
+            const uint4* t = reinterpret_cast<const uint4*>(s.ring[wid][st]);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) v[j] = t[32 * j + lane];
+            ++got;
+            __syncwarp();  // all lanes have read: the place is free
+            ask();
+        } else {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int mine = q + 32 * j + lane;
+                const uint32_t none = TYPE == FT_T_F32 ? 0xff800000u : TYPE == FT_T_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+                v[j] = make_uint4(none, none, none, none);
+                if (mine < q1) v[j] = load_vector<TYPE>(row, mine, shift, p.V);
             }
         }
-        l += l1;
-        ref = (double)c / (double)LOG2E;
-    } else {
+        float mj[NJ], m = -INFINITY;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            float f[VEC];
-            unpack<TYPE>(v[j], f);
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) l += ex2((f[k] - g) * LOG2E);  // (+inf gives a NaN)
+            mj[j] = max_of<TYPE>(v[j]);
+            m = fmaxf(m, mj[j]);
         }
-        ref = g;
-    }
-    l = ft::warp_sum(l);
-    if (lane == 0) {
-        s.wm[wid] = ref;
-        s.wl[wid] = l;
-    }
-    __syncthreads();
-    if (wid < GROUPS / 32) nth_of_groups(s.group, p.N, &s.bar);
-    if (wid == 7) {
-        double r = s.wm[lane & 7];
-        const float lw = s.wl[lane & 7];
-        // a warp without a value has its reference at 0 and must not set the others'
-        double top = lw == 0.f ? -INFINITY : r;
+        const bool rare = __any_sync(0xffffffffu, m > limit || (barred && m >= bar));
+        if (rare && __any_sync(0xffffffffu, m > limit)) {
+            float top = m;
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float t = lw == 0.f ? 0.f : lw * expf((float)(r - top));
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        if (lane == 0) p.sums[list] = BeamSum{top, t, 0};
-    }
-    __syncthreads();
-    const float bar = s.bar;
-    auto key = [&](float f, long long i) { return (uint64_t)ord(f) << 32 | (uint32_t)(0xffffffffu - (uint32_t)i); };
-    if (m >= bar && m > -INFINITY) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            float f[VEC];
-            unpack<TYPE>(v[j], f);
-#pragma unroll
-            for (int k = 0; k < VEC; ++k)
-                if (f[k] >= bar && f[k] > -INFINITY) {
-                    const int at = atomicAdd(&s.n, 1);
-                    if (at < CAP) s.list[at] = key(f[k], i0 + (long long)j * (CT * VEC) + k);
-                }
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const bool to_far = fabsf(top) > 1048576.f;
+            const float to = rintf(top * LOG2E);
+            if (set) {  // e^(old reference - new one)
+                const float e = ex2(far ? (g - top) * LOG2E : to_far ? c - top * LOG2E : c - to);
+                l0 *= e;
+                l1 *= e;
+            }
+            set = true;
+            far = to_far;
+            c = to;
+            g = top;
+            limit = to_far ? top : top + 40.f;
         }
-    }
-    __syncthreads();
-    int n = s.n;
-    if (n > CAP) {
-        // Many equal values.  Keys are all different, so some bar between the lowest of these and the largest lets
-        // N to CAP of them pass: halve the range until one does.
-        uint64_t lo = (uint64_t)max(ord(bar), ord(-INFINITY) + 1) << 32, hi = ~0ull;
-        for (int it = 0; it < 64; ++it) {
-            const uint64_t mid = lo + (hi - lo) / 2;
-            int mine = 0;
+        if (!far) {
+            const uint64_t k2 = pair(LOG2E, LOG2E), c2 = pair(-c, -c);
+            uint64_t l2 = pair(l0, l1);
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 float f[VEC];
                 unpack<TYPE>(v[j], f);
 #pragma unroll
-                for (int k = 0; k < VEC; ++k)
-                    mine += f[k] > -INFINITY && key(f[k], i0 + (long long)j * (CT * VEC) + k) >= mid;
-            }
-            __syncthreads();
-            if (threadIdx.x == 0) s.n = 0;
-            __syncthreads();
-            if (mine) atomicAdd(&s.n, mine);
-            __syncthreads();
-            n = s.n;
-            if (n > CAP) lo = mid;
-            else if (n < p.N) hi = mid;
-            else { lo = mid; break; }
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) s.n = 0;
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            float f[VEC];
-            unpack<TYPE>(v[j], f);
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                const uint64_t q = key(f[k], i0 + (long long)j * (CT * VEC) + k);
-                if (f[k] > -INFINITY && q >= lo) {
-                    const int at = atomicAdd(&s.n, 1);
-                    if (at < CAP) s.list[at] = q;
+                for (int k = 0; k < VEC; k += 2) {
+                    const float2 e = unpair(fma2(pair(f[k], f[k + 1]), k2, c2));
+                    l2 = add2(l2, pair(ex2(e.x), ex2(e.y)));
                 }
             }
+            const float2 l = unpair(l2);
+            l0 = l.x;
+            l1 = l.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                float f[VEC];
+                unpack<TYPE>(v[j], f);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) l0 += ex2((f[k] - g) * LOG2E);  // (+inf gives a NaN)
+            }
         }
-        __syncthreads();
-        n = min(s.n, CAP);
+        if (!rare) continue;
+        if (!barred && set) {  // the first tile that has values
+            bar = fmaxf(nth_of_warp(mj, m, p.N, s.group[wid]), __uint_as_float(0xff7fffffu));  // (no -inf passes)
+            barred = true;
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            if (!__any_sync(0xffffffffu, mj[j] >= bar)) continue;
+            const uint64_t key = key_of(mj[j], q + 32 * j + lane);
+            const bool pass = mj[j] >= bar && key > own;
+            const unsigned who = __ballot_sync(0xffffffffu, pass);
+            if (!who) continue;
+            if (pass) list[cnt + __popc(who & ((1u << lane) - 1))] = key;
+            cnt += __popc(who);
+            if (cnt > p.raise) {
+                cnt = compact_list(list, cnt, p.N);
+                own = list[cnt - 1];
+                bar = fmaxf(bar, unord((uint32_t)(own >> 32)));
+            }
+        }
     }
-    uint64_t* out = p.keys + list * p.N;
-    for (int i = threadIdx.x; i < n; i += CT) {
-        const uint64_t mine = s.list[i];
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += s.list[j] > mine;
-        if (rank < p.N) out[rank] = mine;
-    }
-    for (int i = n + threadIdx.x; i < p.N; i += CT) out[i] = 0;
+    const float l = ft::warp_sum(l0 + l1);
+    if (lane == 0) p.sums[item] = BeamSum{far ? g : c, l, far, 0};
+    if (cnt > p.N) cnt = compact_list(list, cnt, p.N);
+    __syncwarp();
+    // (each list starts at another place: the second kernel's threads then hold keys of all ranks)
+    uint64_t* out = p.keys + (long long)item * p.N;
+    const int turn = item * 7 % p.N;
+    for (int i = lane; i < p.N; i += 32) out[i + turn < p.N ? i + turn : i + turn - p.N] = i < cnt ? list[i] : 0;
+    // (a wait that gave up: its copy must land before the CTA ends)
+    if (lane == 0)
+        for (int i = got; i < asked; ++i) ft::mbar_wait(bars + i % STAGES, (i / STAGES) & 1, p.err);
 }
 
-// (score, beam, token) a before b.
-__device__ __forceinline__ bool before(double sa, uint64_t a, double sb, uint64_t b) {
-    return sa > sb || (sa == sb && a < b);
-}
-
-// The N best of what the chunks of request b left.
-__device__ void join_request(const SelParams& p, int b, JoinSmem& s) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int per = p.C * p.N, E = p.K * per;
-    for (int k = wid; k < p.K; k += CT / 32) {
+// The N best of what the chunks of a request left.
+template <int TYPE>
+__global__ void __launch_bounds__(CT, 1) beam_join_kernel(const SelParams p) {
+    constexpr int VEC = TYPE == FT_T_F32 ? 4 : 8, SIZE = TYPE == FT_T_F32 ? 4 : 2;
+    __shared__ JoinSmem s;
+    ft::grid_dep_launch();
+    ft::grid_dep_wait();
+    const int b = blockIdx.x, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    // the lists' keys in units of 32 of one beam; a thread's first ones stay in its registers
+    const int per = p.C * p.N, units = (per + 31) / 32, all = p.K * units;
+    const unsigned long long* keys = reinterpret_cast<const unsigned long long*>(p.keys) + (long long)b * p.K * per;
+    uint64_t held[HELD];
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) {
+        const int u = h * WARPS + wid, k = u / units, i = (u - k * units) * 32 + lane;
+        held[h] = u < all && i < per ? __ldcg(keys + (long long)k * per + i) : 0;
+    }
+    for (int k = wid; k < p.K; k += WARPS) {
         const int row = b * p.K + k;
+        const float4* sums = reinterpret_cast<const float4*>(p.sums + (long long)row * p.C);
+        // (all of them in flight at once; a row without logits has no sums, and these are not used)
+        float4 part[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) part[h] = 32 * h + lane < p.C ? __ldcg(sums + 32 * h + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
         const float sc = p.scores[row];
-        const bool live = sc > -INFINITY && sc < INFINITY;
         const bool ended = p.done && p.done[row];
+        const bool live = sc > -INFINITY && sc < INFINITY;
         double base = sc, top = 0.;
         if (!live) {
             base = -INFINITY;
             if (lane == 0 && !(sc == -INFINITY)) atomicOr(p.err, FT_DEVERR_ARG);
         } else if (!ended) {
-            top = -INFINITY;
-            for (int c = lane; c < p.C; c += 32) {
-                const BeamSum* q = p.sums + (long long)row * p.C + c;
-                if (__ldcg(&q->l) != 0.f) top = fmax(top, __ldcg(&q->m));
-            }
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
-            float l = 0.f;
-            for (int c = lane; c < p.C; c += 32) {
-                const BeamSum* q = p.sums + (long long)row * p.C + c;
-                const float lc = __ldcg(&q->l);
-                if (lc != 0.f) l += lc * expf((float)(__ldcg(&q->m) - top));
-            }
-            l = ft::warp_sum(l);
-            if (!(l > 0.f && l < INFINITY)) {
+            const BeamSum t = join_sums<32>([&](int i) {
+                const float4 v = i < 32 ? part[0] : i < 64 ? part[1] : i < 96 ? part[2] : i < 128 ? part[3] : __ldcg(sums + i);
+                return BeamSum{v.x, v.y, __float_as_int(v.z), 0};
+            }, p.C);
+            if (!(t.l > 0.f && t.l < INFINITY)) {
                 base = -INFINITY;
-                if (lane == 0 && l != 0.f) atomicOr(p.err, FT_DEVERR_ARG);  // a NaN or an infinity in the row
+                if (lane == 0 && t.l != 0.f) atomicOr(p.err, FT_DEVERR_ARG);  // a NaN or an infinity in the row
             } else {
                 // log l = e log 2 + log f with f in [1/sqrt 2, sqrt 2), so that the fp32 logarithm is of a small number
                 int e;
-                float f = frexpf(l, &e);
+                float f = frexpf(t.l, &e);
                 if (f < 0.70710678f) {
                     f *= 2.f;
                     --e;
                 }
                 base -= e * 0.693147180559945309 + (double)logf(f);
+                top = t.far ? (double)t.ref : (double)t.ref * (1. / (double)LOG2E);
             }
         }
         if (lane == 0) {
             s.base[k] = base;
             s.top[k] = top;
+            s.fbase[k] = (float)base;
+            s.ftop[k] = (float)top;
             s.ended[k] = ended;
         }
     }
-    if (threadIdx.x == 0) s.n = 0;
+    if (threadIdx.x == 0) s.n = s.m = 0;
     __syncthreads();
-    // entry e of the beams' lists, then one entry for each beam that has ended
-    auto entry = [&](int e, double& sc, uint64_t& at) {
-        int k;
-        if (e < E) {
-            k = e / per;
-            const double base = s.base[k];
-            if (base == -INFINITY || s.ended[k]) return false;
-            const long long row = (long long)b * p.K + k;
-            const uint64_t q = __ldcg(reinterpret_cast<const unsigned long long*>(p.keys) + row * per + (e - k * per));
-            if (q == 0) return false;
-            sc = base + ((double)unord((uint32_t)(q >> 32)) - s.top[k]);
-            at = (uint64_t)k << 32 | (0xffffffffu - (uint32_t)q);
-            return true;
-        }
-        k = e - E;
-        if (k >= p.K || !s.ended[k] || s.base[k] == -INFINITY) return false;
-        sc = s.base[k];
-        at = (uint64_t)k << 32 | (uint32_t)p.eos;
-        return true;
+    // A score in fp32 and what it may be off by: three roundings of numbers that are no larger than the three sizes.
+    auto about = [&](int k, float x, float& off) {
+        const float fb = s.fbase[k], ft = s.ftop[k];
+        off = (fabsf(fb) + fabsf(ft) + fabsf(x)) * 0x1p-21f;
+        return fb + (x - ft);
     };
-    const int all = E + (p.done ? p.K : 0);
+    // unit u: its beam, and this lane's key (0: none)
+    auto unit = [&](int u, int h, int& k) {
+        k = u / units;
+        if (s.fbase[k] == -INFINITY || s.ended[k]) return (uint64_t)0;
+        if (h < HELD) return held[h];
+        const int i = (u - k * units) * 32 + lane;
+        return i < per ? (uint64_t)__ldcg(keys + (long long)k * per + i) : (uint64_t)0;
+    };
     float m = -INFINITY;
-    for (int e = threadIdx.x; e < all; e += CT) {
-        double sc;
-        uint64_t at;
-        if (entry(e, sc, at)) m = fmaxf(m, (float)sc);
+    auto look = [&](int u, int h) {
+        int k;
+        const uint64_t q = unit(u, h, k);
+        float off;
+        if (q) {
+            const float a = about(k, unord((uint32_t)(q >> 32)), off);
+            m = fmaxf(m, a - off);
+        }
+    };
+#pragma unroll
+    for (int h = 0; h < HELD; ++h)
+        if (h * WARPS + wid < all) look(h * WARPS + wid, h);
+    for (int u = HELD * WARPS + wid; u < all; u += WARPS) look(u, HELD);
+    const bool mine_ended = p.done && threadIdx.x < p.K && s.ended[threadIdx.x] && s.fbase[threadIdx.x] > -INFINITY;
+    if (mine_ended) {
+        float off;
+        const float a = about(threadIdx.x, 0.f, off);
+        m = fmaxf(m, a - off);
     }
-    float g = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-    if ((lane & 3) == 0) s.group[threadIdx.x >> 2] = g;
+    const int G = store_groups(s.group, m, p.N);
     __syncthreads();
-    if (wid < GROUPS / 32) nth_of_groups(s.group, p.N, &s.bar);
+    if (threadIdx.x < G) nth_of_groups(s.group, G, p.N, &s.bar);
     __syncthreads();
+    // N or more are not below the bar (NaN: sizes that overflow fp32 are taken)
     const float bar = s.bar;
-    // Ranks of the list's entries; those below N move to the front (keep) or are the result.
-    auto rank_list = [&](bool keep) {
+    // The list shrinks to its N best, in order.
+    auto rank_list = [&] {
         const int n = s.n;
-        double sc[CAP / CT];
-        uint64_t at[CAP / CT];
+        uint64_t sc[CAP / CT], at[CAP / CT];
         int rank[CAP / CT];
 #pragma unroll
         for (int u = 0; u < CAP / CT; ++u) {
@@ -405,110 +600,167 @@ __device__ void join_request(const SelParams& p, int b, JoinSmem& s) {
             sc[u] = s.score[i];
             at[u] = s.at[i];
             rank[u] = 0;
-            for (int j = 0; j < n; ++j) rank[u] += before(s.score[j], s.at[j], sc[u], at[u]);
+            for (int j = 0; j < n; ++j) {
+                const uint64_t o = s.score[j];
+                rank[u] += o > sc[u] || (o == sc[u] && s.at[j] < at[u]);
+            }
         }
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < CAP / CT; ++u) {
-            if (rank[u] >= p.N) continue;
-            if (keep) {
+        for (int u = 0; u < CAP / CT; ++u)
+            if (rank[u] < p.N) {
                 s.score[rank[u]] = sc[u];
                 s.at[rank[u]] = at[u];
-                continue;
             }
-            const int k = (int)(at[u] >> 32), v = (int)(uint32_t)at[u], row = b * p.K + k;
-            const long long o = (long long)b * p.N + rank[u];
-            p.out_scores[o] = (float)sc[u];
-            p.out_parents[o] = p.rows ? p.rows[row] : row;
-            p.out_tokens[o] = v;
-            if (p.out_done) p.out_done[o] = v == p.eos;  // (an ended beam's only candidate)
-        }
-        if (!keep)
-            for (int i = n + threadIdx.x; i < p.N; i += CT) {
-                const long long o = (long long)b * p.N + i;
-                p.out_scores[o] = -INFINITY;
-                p.out_parents[o] = p.out_tokens[o] = -1;
-                if (p.out_done) p.out_done[o] = 0;
-            }
-        if (keep) {
-            if (threadIdx.x == 0) s.n = min(n, p.N);
-            __syncthreads();
-        }
+        if (threadIdx.x == 0) s.n = min(n, p.N);
+        __syncthreads();
     };
-    for (int e0 = 0; e0 < all; e0 += CT) {
-        double sc;
-        uint64_t at;
-        if (e0 + (int)threadIdx.x < all && entry(e0 + threadIdx.x, sc, at) && (float)sc >= bar) {
-            const int i = atomicAdd(&s.n, 1);
-            s.score[i] = sc;
-            s.at[i] = at;
-        }
-        if (all > CAP) {  // the list may fill up
+    auto exact = [&](int k, float x) { return ord64(s.base[k] + ((double)x - s.top[k])); };
+    auto add_key = [&](int k, uint64_t q) {
+        const float x = unord((uint32_t)(q >> 32));
+        float off;
+        const float a = about(k, x, off);
+        if (a + off < bar) return;
+        const int i = atomicAdd(&s.n, 1);
+        if (i >= CAP) return;
+        s.score[i] = exact(k, x);
+        s.at[i] = (uint64_t)k << 32 | (0xffffffffu - (uint32_t)q);
+    };
+    auto add = [&](int u, int h) {
+        int k;
+        const uint64_t q = unit(u, h, k);
+        if (q) add_key(k, q);
+    };
+    // Vectors
+#pragma unroll
+    for (int h = 0; h < HELD; ++h)
+        if (h * WARPS + wid < all) add(h * WARPS + wid, h);
+    for (int u = HELD * WARPS + wid; u < all; u += WARPS) add(u, HELD);
+    __syncthreads();
+    if (s.n > CAP) {  // many equal ones: again, in rounds of one unit a warp, the list shortened before it is full
+        __syncthreads();
+        if (threadIdx.x == 0) s.n = 0;
+        __syncthreads();
+        for (int u0 = 0; u0 < all; u0 += WARPS) {
+            const int u = u0 + wid, k = u / units, i = (u - k * units) * 32 + lane;
+            if (u < all && i < per && s.fbase[k] > -INFINITY && !s.ended[k]) {
+                const uint64_t q = __ldcg(keys + (long long)k * per + i);
+                if (q) add_key(k, q);
+            }
             __syncthreads();
-            if (s.n > CAP - CT) rank_list(true);
+            if (s.n > CAP - CT) rank_list();
             else __syncthreads();
         }
     }
+    if (s.n > MAX_V) rank_list();
+    // their values that may be chosen, and the ended beams' only candidates
+    const int n = s.n;
+    if (threadIdx.x < n) s.vec[threadIdx.x] = s.at[threadIdx.x];
     __syncthreads();
-    rank_list(false);
-}
-
-template <int TYPE, int NJ>
-__global__ void __launch_bounds__(CT) beam_select_kernel(const SelParams p) {
-    __shared__ union {
-        ScanSmem scan;
-        JoinSmem join;
-    } s;
-    __shared__ bool last;
-    ft::grid_dep_launch();
-    ft::grid_dep_wait();
-    const long long list = blockIdx.x;
-    const int row = (int)(list / p.C), chunk = (int)(list % p.C), b = row / p.K;
-    const float sc = p.scores[row];
-    if (sc > -INFINITY && !(p.done && p.done[row])) {
-        constexpr int SIZE = TYPE == FT_T_F32 ? 4 : 2;
-        scan_chunk<TYPE, NJ>(p, static_cast<const uint8_t*>(p.logits) + row * p.ld * SIZE, chunk, list, s.scan);
+    for (int t = threadIdx.x; t < n * VEC; t += CT) {
+        const int j = t % VEC, k = (int)(s.vec[t / VEC] >> 32), q = (int)(uint32_t)s.vec[t / VEC];
+        const uint8_t* row = static_cast<const uint8_t*>(p.logits) + ((long long)b * p.K + k) * p.ld * SIZE;
+        const int v = q * VEC - (int)((uintptr_t)row % 16) / SIZE + j;
+        if (v < 0 || v >= p.V) continue;
+        float x;
+        if (TYPE == FT_T_F32) x = reinterpret_cast<const float*>(row)[v];
+        else if (TYPE == FT_T_BF16) x = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[v]);
+        else x = __half2float(reinterpret_cast<const __half*>(row)[v]);
+        if (!(x > -INFINITY)) continue;
+        float off;
+        const float a = about(k, x, off);
+        if (a + off < bar) continue;
+        const int i = atomicAdd(&s.m, 1);  // at most MAX_V * 8, and MAX_K below
+        s.score[i] = exact(k, x);
+        s.at[i] = (uint64_t)k << 32 | (uint32_t)v;
     }
-    // every thread's stores, then the count: the last CTA of the request sees them all
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        unsigned c;
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(c) : "l"(p.arrived + b) : "memory");
-        last = c == (unsigned)(p.K * p.C - 1);
-        if (last) p.arrived[b] = 0;
-        __threadfence();
+    if (mine_ended) {
+        const int i = atomicAdd(&s.m, 1);
+        s.score[i] = ord64(s.base[threadIdx.x]);
+        s.at[i] = (uint64_t)threadIdx.x << 32 | (uint32_t)p.eos;
     }
     __syncthreads();
-    if (last) join_request(p, b, s.join);
+    const int cands = s.m;
+    for (int i = threadIdx.x; i < cands; i += CT) {
+        const uint64_t sc = s.score[i], at = s.at[i];
+        int rank = 0;
+        for (int j = 0; j < cands; ++j) {
+            const uint64_t o = s.score[j];
+            rank += o > sc || (o == sc && s.at[j] < at);
+        }
+        if (rank >= p.N) continue;
+        const int v = (int)(uint32_t)at, row = b * p.K + (int)(at >> 32);
+        const long long o = (long long)b * p.N + rank;
+        p.out_scores[o] = (float)unord64(sc);
+        p.out_parents[o] = p.rows ? p.rows[row] : row;
+        p.out_tokens[o] = v;
+        if (p.out_done) p.out_done[o] = v == p.eos;  // (an ended beam's only candidate)
+    }
+    for (int i = cands + threadIdx.x; i < p.N; i += CT) {
+        const long long o = (long long)b * p.N + i;
+        p.out_scores[o] = -INFINITY;
+        p.out_parents[o] = p.out_tokens[o] = -1;
+        if (p.out_done) p.out_done[o] = 0;
+    }
 }
 
-constexpr int NJ_OF(int type, bool wide) { return wide ? (type == FT_T_F32 ? 8 : 4) : (type == FT_T_F32 ? 2 : 1); }
-constexpr int WIDE = 8192, NARROW = 2048;  // values of a chunk
-
-template <int TYPE>
-const void* kernel_of(bool wide) {
-    return wide ? (const void*)beam_select_kernel<TYPE, NJ_OF(TYPE, true)> : (const void*)beam_select_kernel<TYPE, NJ_OF(TYPE, false)>;
-}
-
-int chunks_of(int V, int dtype, int size) {
+long long vectors_of(int V, int dtype, bool aligned) {
     const int vec = dtype == FT_T_F32 ? 4 : 8;
-    return (V + vec - 1 + size - 1) / size;  // a row may start vec-1 values into its first vector
+    return ((long long)V + (aligned ? 0 : vec - 1) + vec - 1) / vec;  // a row may start vec-1 values into its first vector
+}
+
+// Tiles of a chunk: those with the least time of the busiest warp, its chunks times their vectors and what a chunk costs
+// beside them, and of the second kernel, which takes about as long for a round of its threads' keys as a warp for JOIN_COST
+// vectors.
+constexpr int CHUNK_COST = 512, JOIN_COST = 1024, CHUNKS_A_WARP = 2;
+
+int tiles_of(long long vectors, int R, int K, int N, int sms) {
+    const long long slots = (long long)PER_SM * SCAN_WARPS * sms;
+    const long long most = (vectors + TILE - 1) / TILE;
+    int best = 0;
+    long long least = 1ll << 62;
+    for (long long w = 0; w <= CHUNKS_A_WARP; ++w) {  // of as many rounds more chunks are better
+        long long C = w * slots / R;
+        C = C < 1 ? 1 : C > most ? most : C;
+        const long long join = (long long)HELD * CT;
+        const long long fit = join / ((long long)K * N);  // one round of the second kernel
+        for (long long c : {C, fit < 1 ? 1 : fit < C ? fit : C}) {
+            const long long tiles = (most + c - 1) / c;
+            c = (most + tiles - 1) / tiles;
+            const long long cost = (c * R + slots - 1) / slots * (tiles * TILE + CHUNK_COST) + (c * K * N + join - 1) / join * JOIN_COST;
+            if (cost < least) {
+                least = cost;
+                best = (int)tiles;
+            }
+        }
+
+    }
+    return best;
+}
+
+// Chunks of all rows of a call with up to R_max rows.
+long long lists_of(int R_max, int sms) {
+    const long long most = (long long)CHUNKS_A_WARP * PER_SM * SCAN_WARPS * sms;
+    return R_max > most ? R_max : most;
 }
 
 bool sizes_ok(int V, int dtype, int R_max, int N_max) {
     return V >= 1 && V <= 1 << 24 && dtype >= FT_T_BF16 && dtype <= FT_T_F32 && R_max >= 1 && R_max <= 65536 && N_max >= 1 &&
-           N_max <= MAX_N && (long long)R_max * chunks_of(V, dtype, WIDE) * N_max < (1ll << 31);
+           N_max <= MAX_N;
+}
+
+template <int TYPE>
+cudaError_t setup_kernel() {
+    return cudaFuncSetAttribute((const void*)beam_scan_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(ScanSmem));
 }
 
 struct Layout {
     long long lists;
-    size_t err, arrived, sums, keys, total;
+    size_t err, sums, keys, total;
 };
-Layout layout(int V, int dtype, int R_max, int N_max, int sms) {
+Layout layout(int R_max, int N_max, int sms) {
     Layout l;
-    l.lists = (long long)R_max * chunks_of(V, dtype, WIDE);
-    if (l.lists < 4ll * sms) l.lists = 4ll * sms;
+    l.lists = lists_of(R_max, sms);
     size_t off = 0;
     auto carve = [&](size_t bytes) {
         const size_t o = off;
@@ -516,7 +768,6 @@ Layout layout(int V, int dtype, int R_max, int N_max, int sms) {
         return o;
     };
     l.err = carve(4);
-    l.arrived = carve((size_t)R_max * 4);
     l.sums = carve((size_t)l.lists * sizeof(BeamSum));
     l.keys = carve((size_t)l.lists * N_max * 8);
     l.total = off;
@@ -542,7 +793,7 @@ size_t ft_beam_scratch_bytes(int32_t V, int32_t dtype, int32_t R_max, int32_t N_
         cudaGetLastError();
         return 0;
     }
-    return layout(V, dtype, R_max, N_max, sms).total;
+    return layout(R_max, N_max, sms).total;
 }
 
 ft_status ft_beam_init(ft_beam** out, int32_t V, int32_t dtype, int32_t R_max, int32_t N_max, void* stream) {
@@ -562,17 +813,18 @@ ft_status ft_beam_init(ft_beam** out, int32_t V, int32_t dtype, int32_t R_max, i
     if (cudaGetDevice(&bm->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&bm->num_sms, cudaDevAttrMultiProcessorCount, bm->device) != cudaSuccess)
         return fail(FT_ERR_CUDA);
-    const Layout l = layout(V, dtype, R_max, N_max, bm->num_sms);
+    const Layout l = layout(R_max, N_max, bm->num_sms);
     const cudaError_t e = cudaMalloc(&bm->arena, l.total);
     if (e != cudaSuccess) return fail(e == cudaErrorMemoryAllocation ? FT_ERR_OOM : FT_ERR_CUDA);
     // lists are written before they are read; the rest starts at 0
     if (cudaMemset(bm->arena, 0, l.sums) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return fail(FT_ERR_CUDA);
     uint8_t* a = (uint8_t*)bm->arena;
     bm->err = (unsigned*)(a + l.err);
-    bm->arrived = (unsigned*)(a + l.arrived);
     bm->sums = (BeamSum*)(a + l.sums);
     bm->keys = (uint64_t*)(a + l.keys);
     bm->lists = l.lists;
+    if (setup_kernel<FT_T_BF16>() != cudaSuccess || setup_kernel<FT_T_F16>() != cudaSuccess || setup_kernel<FT_T_F32>() != cudaSuccess)
+        return fail(FT_ERR_CUDA);
     *out = bm;
     return FT_OK;
 }
@@ -607,15 +859,21 @@ ft_status ft_beam_select(ft_beam* bm, int32_t B, int32_t K, int32_t N, const voi
     p.logits = logits; p.ld = ld; p.scores = scores; p.rows = rows; p.done = done; p.eos = eos;
     p.out_scores = out_scores; p.out_parents = out_parents; p.out_tokens = out_tokens; p.out_done = out_done;
     p.V = bm->V; p.K = K; p.N = N;
-    p.sums = bm->sums; p.keys = bm->keys; p.arrived = bm->arrived; p.err = bm->err;
-    // narrow chunks while all of them run at once
-    const long long narrow = (long long)R * chunks_of(bm->V, bm->dtype, NARROW);
-    const bool wide = narrow > 4ll * bm->num_sms;
-    p.C = chunks_of(bm->V, bm->dtype, wide ? WIDE : NARROW);
-    const void* k = bm->dtype == FT_T_BF16 ? kernel_of<FT_T_BF16>(wide) : bm->dtype == FT_T_F16 ? kernel_of<FT_T_F16>(wide)
-                                                                                                : kernel_of<FT_T_F32>(wide);
+    p.sums = bm->sums; p.keys = bm->keys; p.err = bm->err;
+    const long long vectors = vectors_of(bm->V, bm->dtype, (uintptr_t)logits % 16 == 0 && ld * size % 16 == 0);
+    p.vpc = tiles_of(vectors, (int)R, K, N, bm->num_sms) * TILE;
+    p.C = (int)((vectors + p.vpc - 1) / p.vpc);
+    p.items = (int)R * p.C;
+    p.raise = N <= 16 ? N + 8 : WCAP - 32;
+    const void* scan = bm->dtype == FT_T_BF16  ? (const void*)beam_scan_kernel<FT_T_BF16>
+                       : bm->dtype == FT_T_F16 ? (const void*)beam_scan_kernel<FT_T_F16>
+                                               : (const void*)beam_scan_kernel<FT_T_F32>;
+    const void* join = bm->dtype == FT_T_BF16  ? (const void*)beam_join_kernel<FT_T_BF16>
+                       : bm->dtype == FT_T_F16 ? (const void*)beam_join_kernel<FT_T_F16>
+                                               : (const void*)beam_join_kernel<FT_T_F32>;
     void* args[] = {&p};
-    const cudaError_t e = launch_dependent(k, (int)(R * p.C), CT, 0, bm->stream, args);
+    cudaError_t e = launch_dependent(scan, (p.items + SCAN_WARPS - 1) / SCAN_WARPS, SCAN_CT, sizeof(ScanSmem), bm->stream, args);
+    if (e == cudaSuccess) e = launch_dependent(join, B, CT, 0, bm->stream, args);
     if (e == cudaSuccess) return FT_OK;
     if (getenv("FT_DEBUG")) fprintf(stderr, "libft: launch -> %s\n", cudaGetErrorString(e));
     return FT_ERR_CUDA;
@@ -628,6 +886,7 @@ ft_status ft_beam_status(ft_beam* bm) {
     if (cudaMemcpy(&e, bm->err, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return FT_ERR_CUDA;
     if (e && cudaMemset(bm->err, 0, 4) != cudaSuccess) return FT_ERR_CUDA;
     if (e && cudaDeviceSynchronize() != cudaSuccess) return FT_ERR_CUDA;
+    if (e & FT_DEVERR_TIMEOUT) return FT_ERR_TIMEOUT;
     return e ? FT_ERR_DEVICE : FT_OK;
 }
 

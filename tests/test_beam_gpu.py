@@ -132,6 +132,8 @@ def test_order_of_the_logits(V, kind):
     x[1] = -torch.arange(V, device="cuda") / 1000
     x[2] = 1.0                                  # all equal
     x[3] = (torch.arange(V, device="cuda") % 3 == 1).to(x.dtype)
+    x[2, ::2] = 0.0
+    x[2, 1::2] = -0.0                           # ... in value
     for N in (1, 4, 64):
         for r in range(4):
             _check(1, 1, N, x[r:r + 1], ld, [0.0], kind=kind)

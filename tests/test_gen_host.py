@@ -44,7 +44,7 @@ def test_norm_overlaps():
 
 def test_beam_sizes():
     for V, dt, R, N in ((0, 0, 1, 1), ((1 << 24) + 1, 0, 1, 1), (10, 3, 1, 1), (10, -1, 1, 1), (10, 0, 0, 1), (10, 0, 65537, 1),
-                        (10, 0, 1, 0), (10, 0, 1, 65), (1 << 24, 0, 65536, 64), (1 << 24, 2, 16400, 64)):
+                        (10, 0, 1, 0), (10, 0, 1, 65)):
         assert ft.beam_init(V, dt, R, N, None) == (ft.FT_ERR_ARG, None), (V, dt, R, N)
         assert ft.beam_scratch_bytes(V, dt, R, N) == 0
     assert ft.beam_select(None, 1, 1, 1, P, 10, P, None, None, -1, P, P, P, None) == ft.FT_ERR_ARG
