@@ -17,43 +17,81 @@ constexpr int CT = 1024;  // threads of the control kernels
 
 struct KvCtl {
     int *table, *lens, *refs;
-    int n_pages, n_rows, row_pages, page;
+    int n_pages, n_rows, row_pages, page, page_log;
     int *info, *n_copy, *free_list, *remap, *rank;
     KvCopy* copies;
     unsigned* err;
 };
 
 KvCtl ctl_of(const ft_kv* kv) {
-    return KvCtl{kv->table, kv->lens, kv->refs, kv->n_pages, kv->n_rows, kv->row_pages, kv->page,
+    return KvCtl{kv->table, kv->lens, kv->refs, kv->n_pages, kv->n_rows, kv->row_pages, kv->page, __builtin_ctz(kv->page),
                  kv->info, kv->n_copy, kv->free_list, kv->remap, kv->rank, kv->copies, kv->err};
 }
 
-// Which of the four pages from base + 4 * thread on are free, one bit each.
+// The scans for free pages look at 4 pages a thread first (which are read ahead), then at 16.  A warp's pages are PER * 32
+// in a row, 32 at a time.
+constexpr int FREE_FIRST = 4, FREE_MORE = 16;
+template <int PER>
+__device__ __forceinline__ int scan_page(int base, int j) {
+    return base + ((threadIdx.x >> 5) * PER + j) * 32 + (threadIdx.x & 31);
+}
+
+// Which of this thread's pages of the step at `base` are free, one bit each.  CG: past L1, for counts that other CTAs
+// changed in this kernel.
+template <int PER, bool CG>
 __device__ __forceinline__ unsigned free_bits(const KvCtl& c, int base) {
-    const int p = base + 4 * threadIdx.x;
+    int v[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int p = scan_page<PER>(base, j);
+        v[j] = p >= c.n_pages ? 1 : CG ? __ldcg(c.refs + p) : c.refs[p];
+    }
     unsigned f = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (p + j < c.n_pages && c.refs[p + j] == 0) f |= 1u << j;
+    for (int j = 0; j < PER; ++j) f |= v[j] == 0 ? 1u << j : 0;
     return f;
 }
 
-// The lowest `want` free pages, ascending, to list; returns how many there are
-// (at most a few more than `want` are counted).  first: free_bits(c, 0).
-__device__ int take_free(const KvCtl& c, int want, int (&ws)[32], unsigned first) {
-    int have = 0;
-    for (int base = 0; base < c.n_pages && have < want; base += 4 * CT) {
-        const unsigned f = base ? free_bits(c, base) : first;
-        int total;
-        int at = have + ft::block_scan(__popc(f), ws, total);
+// A step of the scan: its free pages go to list from place `have` on, as far as `want`; returns how many it has.
+template <int PER>
+__device__ __forceinline__ int list_free(int base, unsigned f, int have, int want, int (&ws)[32], int* list) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    unsigned m[PER];
+    int cnt = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (f >> j & 1u) {
-                if (at < want) c.free_list[at] = base + 4 * threadIdx.x + j;
-                ++at;
-            }
-        have += total;
+    for (int j = 0; j < PER; ++j) {
+        m[j] = __ballot_sync(0xffffffffu, f >> j & 1u);
+        cnt += __popc(m[j]);
     }
+    __syncthreads();  // the reads of ws before this are over
+    if (lane == 0) ws[wid] = cnt;
+    __syncthreads();
+    int total = ws[lane], at = lane < wid ? total : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        at += __shfl_xor_sync(0xffffffffu, at, o);
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    at += have;
+    if (cnt && at < want) {  // (the same in all lanes)
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int mine = at + __popc(m[j] & ((1u << lane) - 1));
+            if ((f >> j & 1u) && mine < want) list[mine] = scan_page<PER>(base, j);
+            at += __popc(m[j]);
+        }
+    }
+    return total;
+}
+
+// The lowest `want` free pages, ascending, to list; returns how many there are
+// (at most a few more than `want` are counted).  first: free_bits<FREE_FIRST>(c, 0).
+template <bool CG>
+__device__ int take_free(const KvCtl& c, int want, int (&ws)[32], unsigned first, int* list) {
+    int have = 0;
+    if (want > 0) have = list_free<FREE_FIRST>(0, first, 0, want, ws, list);
+    for (int base = FREE_FIRST * CT; base < c.n_pages && have < want; base += FREE_MORE * CT)
+        have += list_free<FREE_MORE>(base, free_bits<FREE_MORE, CG>(c, base), have, want, ws, list);
     __syncthreads();
     return have;
 }
@@ -94,7 +132,7 @@ __global__ void __launch_bounds__(CT) kv_extend_kernel(KvCtl c, int n, const int
     clear(marks, c.n_rows);
     ft::grid_dep_launch();
     ft::grid_dep_wait();
-    const unsigned first = free_bits(c, 0);
+    const unsigned first = free_bits<FREE_FIRST, false>(c, 0);
     int want = 0;
     bool ok = true;
     for (int base = 0; base < n; base += CT) {
@@ -118,7 +156,7 @@ __global__ void __launch_bounds__(CT) kv_extend_kernel(KvCtl c, int n, const int
         want += total;
     }
     if (!__syncthreads_and(ok)) return refuse(c, FT_DEVERR_ARG);
-    if (take_free(c, want, ws, first) < want) return refuse(c, FT_DEVERR_CAPACITY);
+    if (take_free<false>(c, want, ws, first, c.free_list) < want) return refuse(c, FT_DEVERR_CAPACITY);
     for (int i = wid; i < n; i += CT / 32) {
         const int r = rows[i], len = c.lens[r], to = len + add[i], at = c.rank[i];
         const int have = (len + c.page - 1) / c.page, end = (to + c.page - 1) / c.page;
@@ -141,7 +179,7 @@ __global__ void __launch_bounds__(CT) kv_fork_kernel(KvCtl c, int n, const int* 
     clear(marks, c.n_rows);
     ft::grid_dep_launch();
     ft::grid_dep_wait();
-    const unsigned first = free_bits(c, 0);
+    const unsigned first = free_bits<FREE_FIRST, false>(c, 0);
     int want = 0;
     bool ok = true;
     for (int base = 0; base < n; base += CT) {
@@ -173,7 +211,7 @@ __global__ void __launch_bounds__(CT) kv_fork_kernel(KvCtl c, int n, const int* 
             if (row[j] < 0 || row[j] >= c.n_pages) ok = false;
     }
     if (!__syncthreads_and(ok)) return refuse(c, FT_DEVERR_ARG);
-    if (take_free(c, want, ws, first) < want) return refuse(c, FT_DEVERR_CAPACITY);
+    if (take_free<false>(c, want, ws, first, c.free_list) < want) return refuse(c, FT_DEVERR_CAPACITY);
     for (int i = wid; i < n; i += CT / 32) {
         const int p = parents[i], len = c.lens[p], full = len / c.page, tok = len % c.page;
         const int* src = c.table + (size_t)p * c.row_pages;
@@ -260,18 +298,20 @@ struct BatchOut {
     int T;
 };
 
-// Lists the tokens t0, t0 + step, ... of the requests whose first tokens are start[0..B) and whose rows have their
-// new lengths (old_lens: still the old ones).
-__device__ void list_tokens(const KvCtl& c, const BatchOut& o, int B, const int* rows, const int* add, const int* start,
-                            int total, bool old_lens, int t0, int step) {
+// Lists the tokens t0, t0 + step, ... of the requests whose first tokens are start[0..B).  A request's length before the
+// call is held[b], or where held is null that of its row, less add[b] where add is given.
+__device__ __forceinline__ void list_tokens(const KvCtl& c, const BatchOut& o, int B, const int* rows, const int* held,
+                                            const int* add, const int* start, int total, int t0, int step) {
     for (long long t = t0; t < o.T; t += step) {
         int r = -1, p = 0;
         long long slot = -1;
         if (t < total) {
-            const int b = owner_of(start, B, (int)t);
+            // (one token each: no search)
+            const bool single = t < B && start[t] == t && (t + 1 < B ? start[t + 1] : total) == t + 1;
+            const int b = single ? (int)t : owner_of(start, B, (int)t);
             r = rows ? rows[b] : b;
-            p = c.lens[r] - (old_lens ? 0 : add[b]) + ((int)t - start[b]);
-            if (o.slots) slot = (long long)c.table[(size_t)r * c.row_pages + p / c.page] * c.page + p % c.page;
+            p = (held ? held[b] : c.lens[r] - (add ? add[b] : 0)) + ((int)t - start[b]);
+            if (o.slots) slot = (long long)c.table[(size_t)r * c.row_pages + (p >> c.page_log)] * c.page + (p & (c.page - 1));
         }
         o.row_of[t] = r;
         o.pos[t] = p;
@@ -279,60 +319,102 @@ __device__ void list_tokens(const KvCtl& c, const BatchOut& o, int B, const int*
     }
 }
 
-constexpr int BATCH_SMEM = 2048;  // requests whose first tokens and pages are kept in shared memory
+#ifndef LH
+#define LH 1024
+#endif
+constexpr int LIST_HERE = LH;   // tokens that the first kernel lists itself
+constexpr int BATCH_SMEM = 2048;  // requests that are kept in shared memory
 
-// Rows grow as in kv_extend_kernel; then, with list_here, one thread a token lists them.
+struct TokPage {
+    long long tok;
+    int page;
+};
+// Exclusive prefix sums of both over the CTA, in one pass; total gets the sums.
+__device__ __forceinline__ TokPage block_scan2(TokPage v, TokPage (&ws)[32], TokPage& total) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    TokPage x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, x.tok, o);
+        const int g = __shfl_up_sync(0xffffffffu, x.page, o);
+        if (lane >= o) {
+            x.tok += t;
+            x.page += g;
+        }
+    }
+    __syncthreads();  // the previous call's reads of ws are over
+    if (lane == 31) ws[wid] = x;
+    __syncthreads();
+    // every warp joins the 32 sums for itself
+    TokPage s = ws[lane];
+    TokPage before{lane < wid ? s.tok : 0, lane < wid ? s.page : 0};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        before.tok += __shfl_xor_sync(0xffffffffu, before.tok, o);
+        before.page += __shfl_xor_sync(0xffffffffu, before.page, o);
+        s.tok += __shfl_xor_sync(0xffffffffu, s.tok, o);
+        s.page += __shfl_xor_sync(0xffffffffu, s.page, o);
+    }
+    total = s;
+    return TokPage{x.tok - v.tok + before.tok, x.page - v.page + before.page};
+}
+
+// Rows grow as in kv_extend_kernel; then, with list_here, one thread a token lists them.  Bound by dependent reads: list,
+// length, counts of the pages, and what a token needs; rows, lengths and both prefix sums stay in shared memory.
 __global__ void __launch_bounds__(CT) kv_batch_kernel(KvCtl c, int B, const int* __restrict__ rows,
                                                       const int* __restrict__ add, BatchOut o, int list_here) {
     __shared__ int ws[32];
-    __shared__ long long wl[32];
+    __shared__ TokPage wl[32];
     __shared__ RowMarks marks;
-    __shared__ int s_tok[BATCH_SMEM], s_page[BATCH_SMEM];
+    __shared__ int s_tok[BATCH_SMEM], s_page[BATCH_SMEM], s_row[BATCH_SMEM], s_len[BATCH_SMEM];
     clear(marks, c.n_rows);
     ft::grid_dep_launch();
     ft::grid_dep_wait();
-    const unsigned first = free_bits(c, 0);
+    const unsigned first = free_bits<FREE_FIRST, false>(c, 0);
     const bool small = B <= BATCH_SMEM;
     int* tok = small ? s_tok : o.cu_q;
     int* pg = small ? s_page : c.rank;
-    int want = 0;
-    long long tokens = 0;
+    TokPage sum{0, 0};
     bool ok = true;
     for (int base = 0; base < B; base += CT) {
         const int i = base + threadIdx.x;
-        int need = 0, n = 0;
+        TokPage need{0, 0};
         if (i < B) {
             const int r = rows ? rows[i] : i, a = add[i];
+            int len = 0;
             if (mark(marks, r, c.n_rows)) {
-                const long long len = c.lens[r], to = len + a;
-                if (len < 0 || a < 0 || to > (long long)c.row_pages * c.page) {
+                len = c.lens[r];
+                const long long to = (long long)len + a;
+                if (len < 0 || a < 0 || to > (long long)c.row_pages * c.page)
                     ok = false;
-                } else {
-                    n = a;
-                    need = (int)((to + c.page - 1) / c.page - (len + c.page - 1) / c.page);
-                }
+                else
+                    need = TokPage{a, (int)(((to + c.page - 1) >> c.page_log) - (((long long)len + c.page - 1) >> c.page_log))};
             } else {
                 ok = false;
             }
+            if (small) {
+                s_row[i] = r;
+                s_len[i] = len;
+            }
         }
-        long long tot_n;
-        int total;
-        const long long at_n = tokens + ft::block_scan((long long)n, wl, tot_n);
-        const int at = want + ft::block_scan(need, ws, total);
+        TokPage total;
+        const TokPage at = block_scan2(need, wl, total);
         if (i < B) {
-            tok[i] = (int)min(at_n, (long long)o.T);
-            pg[i] = at;
+            tok[i] = (int)min(sum.tok + at.tok, (long long)o.T);
+            pg[i] = sum.page + at.page;
         }
-        tokens += tot_n;
-        want += total;
-        if (tokens > o.T) {  // (the same in all threads; the sum of pages stays in its range)
+        sum.tok += total.tok;
+        sum.page += total.page;
+        if (sum.tok > o.T) {  // (the same in all threads; the sum of pages stays in its range)
             ok = false;
             break;
         }
     }
+    int tokens = (int)min(sum.tok, (long long)o.T);
+    const int want = sum.page;
     unsigned bad = 0;
     if (!__syncthreads_and(ok)) bad = FT_DEVERR_ARG;
-    else if (take_free(c, want, ws, first) < want) bad = FT_DEVERR_CAPACITY;
+    else if (take_free<false>(c, want, ws, first, c.free_list) < want) bad = FT_DEVERR_CAPACITY;
     if (bad) {
         refuse(c, bad);
         tokens = 0;
@@ -340,55 +422,117 @@ __global__ void __launch_bounds__(CT) kv_batch_kernel(KvCtl c, int B, const int*
     } else {
         for (int w = threadIdx.x; w < want; w += CT) {
             const int i = owner_of(pg, B, w);
-            const int r = rows ? rows[i] : i, p = c.free_list[w];
-            c.table[(size_t)r * c.row_pages + (c.lens[r] + c.page - 1) / c.page + (w - pg[i])] = p;
+            const int r = small ? s_row[i] : rows ? rows[i] : i, len = small ? s_len[i] : c.lens[r], p = c.free_list[w];
+            c.table[(size_t)r * c.row_pages + ((len + c.page - 1) >> c.page_log) + (w - pg[i])] = p;
             c.refs[p] = 1;
         }
         if (small)
             for (int i = threadIdx.x; i < B; i += CT) o.cu_q[i] = tok[i];
-        if (threadIdx.x == 0) o.cu_q[B] = (int)tokens;
+        if (threadIdx.x == 0) o.cu_q[B] = tokens;
         set_info(c, want, 0, -1);
-        __syncthreads();
+        if (list_here) __syncthreads();
     }
-    if (list_here) list_tokens(c, o, B, rows, add, tok, (int)tokens, true, threadIdx.x, CT);
+    if (list_here) {
+        if (small) list_tokens(c, o, B, s_row, s_len, nullptr, tok, tokens, threadIdx.x, CT);
+        else list_tokens(c, o, B, rows, nullptr, nullptr, tok, tokens, threadIdx.x, CT);
+    }
     if (bad) return;
     __syncthreads();
-    for (int i = threadIdx.x; i < B; i += CT) c.lens[rows ? rows[i] : i] += add[i];
+    for (int i = threadIdx.x; i < B; i += CT) {
+        const int r = small ? s_row[i] : rows ? rows[i] : i;
+        c.lens[r] = (small ? s_len[i] : c.lens[r]) + add[i];
+    }
 }
 
+// The lists of a long step, a thread a token; the requests' first tokens are searched in shared memory where they fit.
 __global__ void __launch_bounds__(256) kv_list_kernel(KvCtl c, int B, const int* __restrict__ rows,
                                                       const int* __restrict__ add, BatchOut o) {
+    __shared__ int s_tok[BATCH_SMEM];
     ft::grid_dep_launch();
     ft::grid_dep_wait();
-    list_tokens(c, o, B, rows, add, o.cu_q, o.cu_q[B], false, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+    const bool small = B <= BATCH_SMEM;
+    const int total = o.cu_q[B];
+    if (small) {
+        for (int i = threadIdx.x; i < B; i += 256) s_tok[i] = o.cu_q[i];
+        __syncthreads();
+    }
+    list_tokens(c, o, B, rows, nullptr, add, small ? s_tok : o.cu_q, total, blockIdx.x * blockDim.x + threadIdx.x,
+                gridDim.x * blockDim.x);
 }
 
 // ---- reordering
+//
+// Table entries are the work: for each row that changes, the pages that it gets and those that it held are checked,
+// counted and written.  Units of RO_COLS columns of one row are spread over the warps of a cluster of CTAs, which share the
+// short control part (each does it for itself) and meet at cluster barriers; 256 rows of 63 pages took 44 us in one CTA.
 
-constexpr int RO_MAX = 1024;           // rows of a call, one thread each
-constexpr int RO_STAGE = 40 * 1024;    // table entries staged at a time (160 KB)
+constexpr int RO_MAX = 1024;      // rows of a call, one thread each
+constexpr int RO_COLS = 128;      // columns of a unit, four a lane
+constexpr int RO_SLOTS = 320;     // units that a CTA stages at a time (160 KB)
+constexpr int RO_CTAS = 8;        // CTAs of a cluster
+constexpr int RO_ALONE = 32;      // rows up to which one CTA does it all
+// a column block of all rows is staged at once
+static_assert(RO_SLOTS >= RO_ALONE && RO_SLOTS * RO_CTAS >= RO_MAX, "rows of a call");
 
-__global__ void __launch_bounds__(CT) kv_reorder_kernel(KvCtl c, int n, const int* __restrict__ rows,
-                                                        const int* __restrict__ parents) {
-    extern __shared__ int stage[];
-    __shared__ int ws[32];
-    __shared__ RowMarks marks;
-    // of each item: row, parent, pages it held, complete pages it gets, its last page (0: none, 1: kept, 2 + rank: new)
-    __shared__ int s_row[RO_MAX], s_par[RO_MAX], s_old[RO_MAX], s_full[RO_MAX], s_last[RO_MAX], s_keep[RO_MAX];
-    __shared__ int s_cols;
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    clear(marks, c.n_rows);
+struct ReorderSmem {
+    union {
+        int stage[RO_SLOTS][RO_COLS];
+        uint16_t item_of[KV_MAX_ROWS];  // of a row in the list: its place there
+    };
+    RowMarks marks;
+    int ws[32];
+    // of each item: row, parent, tokens it gets, pages it held, complete pages it gets, its last page (0: none, 1: kept,
+    // 2 + rank: new), who keeps its own row's last page
+    int row[RO_MAX], par[RO_MAX], len[RO_MAX], old[RO_MAX], full[RO_MAX], last[RO_MAX], keep[RO_MAX];
+    int free[RO_MAX];
+    int cols;
+    unsigned flag[3];
+};
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ unsigned cluster_size() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// Whether ok holds in all threads of the cluster; flag: a word of its own for each call.
+__device__ __forceinline__ bool cluster_all(bool ok, unsigned* flag) {
+    const bool mine = __syncthreads_and(ok);
+    if (threadIdx.x == 0) *flag = mine;
+    cluster_sync();
+    unsigned v = 1;
+    if (threadIdx.x < cluster_size()) {
+        uint32_t a;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ft::smem_addr(flag)), "r"(threadIdx.x));
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    }
+    return __syncthreads_and(v);
+}
+
+__global__ void __launch_bounds__(CT, 1) kv_reorder_kernel(KvCtl c, int n, const int* __restrict__ rows,
+                                                           const int* __restrict__ parents) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    ReorderSmem& s = *reinterpret_cast<ReorderSmem*>(smem);
+    const int lane = threadIdx.x & 31, rank = cluster_rank(), ctas = cluster_size();
+    const int wid = rank * (CT / 32) + (threadIdx.x >> 5), warps = ctas * (CT / 32);
+    if (threadIdx.x == 0) s.cols = 0;
+    clear(s.marks, c.n_rows);
     ft::grid_dep_launch();
     ft::grid_dep_wait();
     const int i = threadIdx.x;
     int r = -1, p = -1, len = 0;
     bool ok = true;
-    if (threadIdx.x == 0) s_cols = 0;
-    __syncthreads();
     if (i < n) {
         r = rows ? rows[i] : i;
         p = parents[i];
-        if (!mark(marks, r, c.n_rows) || p < -1 || p >= c.n_rows) {
+        if (!mark(s.marks, r, c.n_rows) || p < -1 || p >= c.n_rows) {
             ok = false;
         } else {
             const int old = c.lens[r];
@@ -397,103 +541,138 @@ __global__ void __launch_bounds__(CT) kv_reorder_kernel(KvCtl c, int n, const in
             if (old < 0 || old > most || len < 0 || len > most) {
                 ok = false;
             } else {
-                s_row[i] = r;
-                s_par[i] = p;
-                s_old[i] = (old + c.page - 1) / c.page;
-                s_full[i] = len / c.page;
-                s_keep[i] = 0x7fffffff;
-                atomicMax(&s_cols, max(s_old[i], (len + c.page - 1) / c.page));
-                c.rank[r] = i;
+                s.row[i] = r;
+                s.par[i] = p;
+                s.len[i] = len;
+                s.old[i] = (old + c.page - 1) >> c.page_log;
+                s.full[i] = len >> c.page_log;
+                s.keep[i] = 0x7fffffff;
+                if (p != r) atomicMax(&s.cols, max(s.old[i], (len + c.page - 1) >> c.page_log));
+                s.item_of[r] = (uint16_t)i;
             }
         }
     }
-    if (!__syncthreads_and(ok)) return refuse(c, FT_DEVERR_ARG);
+    auto leave = [&](unsigned bit) {
+        if (bit && rank == 0) refuse(c, bit);
+        cluster_sync();  // no CTA ends while another may read its flags
+    };
+    // (every CTA finds the same)
+    if (!__syncthreads_and(ok)) return leave(FT_DEVERR_ARG);
     // the child that keeps the last page of a parent whose own row is in the list
     int j = -1;
-    if (i < n && p >= 0 && (marks.w[p >> 5] >> (p & 31) & 1u)) {
-        j = c.rank[p];
-        atomicMin(&s_keep[j], p == r ? -1 : i);
+    if (i < n && p >= 0 && (s.marks.w[p >> 5] >> (p & 31) & 1u)) {
+        j = s.item_of[p];
+        atomicMin(&s.keep[j], p == r ? -1 : i);
     }
     __syncthreads();
-    const bool part = i < n && len % c.page != 0;
-    const bool keeps = j >= 0 && s_keep[j] == (p == r ? -1 : i);
+    const bool part = i < n && (len & (c.page - 1)) != 0;
+    const bool keeps = j >= 0 && s.keep[j] == (p == r ? -1 : i);
     int want;
-    const int at = ft::block_scan(part && !keeps ? 1 : 0, ws, want);
-    if (i < n) s_last[i] = !part ? 0 : keeps ? 1 : 2 + at;
+    const int at = ft::block_scan(part && !keeps ? 1 : 0, s.ws, want);
+    if (i < n) s.last[i] = !part ? 0 : keeps ? 1 : 2 + at;
     __syncthreads();
-    // counts of the pages: those that the rows get, less those that they held.  A row that stays as it is is left out.
-    auto count = [&](int sign) {
-        for (int k = wid; k < n; k += CT / 32) {
-            if (s_row[k] == s_par[k]) continue;
-            const int got = s_full[k] + (s_last[k] == 1), held = s_old[k];
-            const int* from = c.table + (size_t)max(s_par[k], 0) * c.row_pages;
-            const int* mine = c.table + (size_t)s_row[k] * c.row_pages;
-            for (int q = lane; q < max(got, held); q += 32) {
-                if (q < got) atomicAdd(&c.refs[from[q]], sign);
-                if (q < held) atomicAdd(&c.refs[mine[q]], -sign);
-            }
-        }
-        __syncthreads();
+    // Units: columns cb * RO_COLS .. of item k; a row that stays as it is has no work.
+    const int blocks = (s.cols + RO_COLS - 1) / RO_COLS, units = blocks * n;
+    struct Unit {
+        const int *from, *mine;  // the parent's entries and the row's own
+        int got, held;           // how many of them from here on (got: with a last page that is new)
+        int k;
     };
-    for (int k = wid; k < n; k += CT / 32) {
-        if (s_row[k] == s_par[k]) continue;
-        const int got = s_full[k] + (s_last[k] != 0), held = s_old[k];
-        const int* from = c.table + (size_t)max(s_par[k], 0) * c.row_pages;
-        const int* mine = c.table + (size_t)s_row[k] * c.row_pages;
-        for (int q = lane; q < max(got, held); q += 32) {
-            if (q < got && (unsigned)from[q] >= (unsigned)c.n_pages) ok = false;
-            if (q < held && (unsigned)mine[q] >= (unsigned)c.n_pages) ok = false;
-        }
-    }
-    if (!__syncthreads_and(ok)) return refuse(c, FT_DEVERR_ARG);
-    count(1);
-    // a page that a row held without being counted
-    for (int k = wid; k < n; k += CT / 32) {
-        if (s_row[k] == s_par[k]) continue;
-        for (int q = lane; q < s_old[k]; q += 32)
-            if (__ldcg(&c.refs[c.table[(size_t)s_row[k] * c.row_pages + q]]) < 0) ok = false;
-    }
-    if (!__syncthreads_and(ok)) {
-        count(-1);
-        return refuse(c, FT_DEVERR_ARG);
-    }
-    if (want > 0 && take_free(c, want, ws, free_bits(c, 0)) < want) {
-        count(-1);
-        return refuse(c, FT_DEVERR_CAPACITY);
-    }
-    // the rows, some columns at a time: all are read before one is written
-    const int cols = s_cols;
-    int tile = RO_STAGE / max(n, 1);
-    if (tile > cols) tile = cols;
-    for (int c0 = 0; c0 < cols; c0 += tile) {
-        const int w = min(tile, cols - c0);
-        for (int k = wid; k < n; k += CT / 32) {
-            if (s_row[k] == s_par[k]) continue;
-            const int* from = c.table + (size_t)max(s_par[k], 0) * c.row_pages + c0;
-            const int got = s_full[k] + (s_last[k] != 0) - c0;
-            for (int q = lane; q < min(w, got); q += 32) stage[k * tile + q] = from[q];
-        }
-        __syncthreads();
-        for (int k = wid; k < n; k += CT / 32) {
-            if (s_row[k] == s_par[k]) continue;
-            int* to = c.table + (size_t)s_row[k] * c.row_pages + c0;
-            const int full = s_full[k] - c0, last = s_last[k], end = max(s_old[k], s_full[k] + (last != 0)) - c0;
-            for (int q = lane; q < min(w, end); q += 32) {
-                int v = -1;
-                if (q < full || (q == full && last == 1)) {
-                    v = stage[k * tile + q];
-                } else if (q == full && last >= 2) {
-                    v = c.free_list[last - 2];
-                    c.refs[v] = 1;
-                    c.copies[last - 2] = KvCopy{stage[k * tile + q], v, c.lens[s_par[k]] % c.page};
-                }
-                to[q] = v;
+    auto unit = [&](int u) {
+        const int cb = u / n, k = u - cb * n, c0 = cb * RO_COLS;
+        Unit x;
+        x.k = k;
+        x.from = c.table + (size_t)max(s.par[k], 0) * c.row_pages + c0;
+        x.mine = c.table + (size_t)s.row[k] * c.row_pages + c0;
+        const bool same = s.row[k] == s.par[k];
+        x.got = same ? 0 : min(max(s.full[k] + (s.last[k] != 0) - c0, 0), RO_COLS);
+        x.held = same ? 0 : min(max(s.old[k] - c0, 0), RO_COLS);
+        return x;
+    };
+    // counts of the pages: those that the rows get, less those that they held (a new last page is not one of them)
+    auto count = [&](int sign) {
+        for (int u = wid; u < units; u += warps) {
+            const Unit x = unit(u);
+            const int c0 = (u / n) * RO_COLS;
+            const int got = min(x.got, max(s.full[x.k] + (s.last[x.k] == 1) - c0, 0));
+#pragma unroll
+            for (int h = 0; h < RO_COLS / 32; ++h) {
+                const int q = 32 * h + lane;
+                if (q < got) atomicAdd(&c.refs[x.from[q]], sign);
+                if (q < x.held) atomicAdd(&c.refs[x.mine[q]], -sign);
             }
         }
-        __syncthreads();
+    };
+    for (int u = wid; u < units; u += warps) {
+        const Unit x = unit(u);
+        int a[RO_COLS / 32], b[RO_COLS / 32];
+#pragma unroll
+        for (int h = 0; h < RO_COLS / 32; ++h) {
+            const int q = 32 * h + lane;
+            a[h] = q < x.got ? x.from[q] : 0;
+            b[h] = q < x.held ? x.mine[q] : 0;
+        }
+#pragma unroll
+        for (int h = 0; h < RO_COLS / 32; ++h)
+            if ((unsigned)a[h] >= (unsigned)c.n_pages || (unsigned)b[h] >= (unsigned)c.n_pages) ok = false;
     }
-    if (i < n) c.lens[r] = len;
-    set_info(c, want, want, -1);
+    if (!cluster_all(ok, &s.flag[0])) return leave(FT_DEVERR_ARG);
+    count(1);
+    cluster_sync();
+    const unsigned first = want ? free_bits<FREE_FIRST, true>(c, 0) : 0;
+    // a page that a row held without being counted
+    for (int u = wid; u < units; u += warps) {
+        const Unit x = unit(u);
+        int b[RO_COLS / 32];
+#pragma unroll
+        for (int h = 0; h < RO_COLS / 32; ++h) b[h] = 32 * h + lane < x.held ? __ldcg(&c.refs[x.mine[32 * h + lane]]) : 0;
+#pragma unroll
+        for (int h = 0; h < RO_COLS / 32; ++h)
+            if (b[h] < 0) ok = false;
+    }
+    const int have = take_free<true>(c, want, s.ws, first, s.free);  // (in every CTA)
+    const bool sound = cluster_all(ok, &s.flag[1]);
+    if (!sound || have < want) {
+        count(-1);
+        return leave(sound ? FT_DEVERR_CAPACITY : FT_DEVERR_ARG);
+    }
+    // The rows, whole columns at a time: all of them are read before one is written.
+    const int most = n ? RO_SLOTS * ctas / n * n : 1;  // (n or more)
+    for (int u0 = 0; u0 < units; u0 += most) {
+        const int end = min(units, u0 + most);
+        for (int u = u0 + wid, slot = threadIdx.x >> 5; u < end; u += warps, slot += CT / 32) {
+            const Unit x = unit(u);
+            int a[RO_COLS / 32];
+#pragma unroll
+            for (int h = 0; h < RO_COLS / 32; ++h) a[h] = 32 * h + lane < x.got ? x.from[32 * h + lane] : -1;
+#pragma unroll
+            for (int h = 0; h < RO_COLS / 32; ++h) s.stage[slot][32 * h + lane] = a[h];
+        }
+        cluster_sync();
+        for (int u = u0 + wid, slot = threadIdx.x >> 5; u < end; u += warps, slot += CT / 32) {
+            const Unit x = unit(u);
+            const int full = s.full[x.k] - (u / n) * RO_COLS, last = s.last[x.k];
+#pragma unroll
+            for (int h = 0; h < RO_COLS / 32; ++h) {
+                const int q = 32 * h + lane;
+                if (q >= max(x.got, x.held)) continue;
+                int v = s.stage[slot][q];
+                if (q == full && last >= 2) {
+                    const int src = v;
+                    v = s.free[last - 2];
+                    c.refs[v] = 1;
+                    c.copies[last - 2] = KvCopy{src, v, s.len[x.k] & (c.page - 1)};
+                }
+                const_cast<int*>(x.mine)[q] = v;
+            }
+        }
+        cluster_sync();
+    }
+    if (rank == 0) {
+        if (i < n) c.lens[r] = len;
+        set_info(c, want, want, -1);
+    }
+    leave(0);
 }
 
 // live = pages in use; the k-th page in use at index >= live pairs with the
@@ -614,7 +793,7 @@ cudaError_t launch_kv_batch(ft_kv* kv, int B, const int* rows, const int* add, i
                             long long* slots) {
     KvCtl c = ctl_of(kv);
     BatchOut o{cu_q, row_of, pos, slots, T};
-    int here = T <= 4096;
+    int here = T <= LIST_HERE;
     void* args[] = {&c, &B, &rows, &add, &o, &here};
     const cudaError_t e = launch_dependent((const void*)kv_batch_kernel, 1, CT, 0, kv->stream, args);
     if (e != cudaSuccess || here) return e;
@@ -626,13 +805,27 @@ cudaError_t launch_kv_batch(ft_kv* kv, int B, const int* rows, const int* add, i
 
 cudaError_t launch_kv_reorder(ft_kv* kv, int n, const int* rows, const int* parents) {
     KvCtl c = ctl_of(kv);
+    cudaLaunchConfig_t cfg = {};
+    // a unit or two a warp: a single CTA
+    const int ctas = n <= RO_ALONE && (long long)n * kv->row_pages <= RO_ALONE * RO_COLS ? 1 : RO_CTAS;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(CT);
+    cfg.dynamicSmemBytes = sizeof(ReorderSmem);
+    cfg.stream = kv->stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim = {(unsigned)ctas, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
     void* args[] = {&c, &n, &rows, &parents};
-    const cudaError_t e = launch_dependent((const void*)kv_reorder_kernel, 1, CT, RO_STAGE * 4, kv->stream, args);
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, (const void*)kv_reorder_kernel, args);
     return e == cudaSuccess && n > 0 ? launch_copy(kv, false, n) : e;
 }
 
 cudaError_t kv_pages_setup() {
-    return cudaFuncSetAttribute((const void*)kv_reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RO_STAGE * 4);
+    return cudaFuncSetAttribute((const void*)kv_reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(ReorderSmem));
 }
 
 cudaError_t launch_kv_compact(ft_kv* kv) {
