@@ -8,7 +8,16 @@
 // Bound: HBM for prompts (a and r are read, h and y written, once each; the
 // weights stay in L2), latency for a few tokens.  A row lives in the registers
 // of its threads, NV vectors of 8 values each, between the loads and the stores,
-// so nothing is read twice.
+// so nothing is read twice.  Each CTA takes one row and ends: the loads of the
+// CTAs that follow fill the gaps that its barriers leave, so registers (that is,
+// CTAs an SM) decide.  Measured against that: CTAs that stay and ask for the next
+// row's values a row ahead, 2 x 512 threads an SM, 96 us instead of 67.6 for 8192
+// tokens of 4096; a gate of [T, H] held in registers from the start instead of
+// brought into L2, 18.4 us instead of 17.9 for 4001 tokens of 2048.
+//
+// Measured (a stream of calls on buffers larger than L2): 8192 tokens of 4096 in
+// fp32, out bf16, 67.6 us, 6.95 TB/s (the copy rate); 4001 of 2048 in f16 with
+// both norms and a full gate 17.9 us, 4.6 TB/s; one token of 2048 1.8 us.
 #include "ft_kv.cuh"
 #include "../../include/ft_gen.h"
 
@@ -29,17 +38,30 @@ struct NormParams {
     float eps, rs, bs;
 };
 
-// 8 values at element offset i of an array of fp32 or 16-bit values.
+// 8 values in memory's form, and as fp32.
+template <bool F32>
+struct Raw {
+    uint4 v[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ void load_raw(const void* p, long long i, Raw<F32>& r) {  // at element offset i
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * (F32 ? 4 : 2));
+    r.v[0] = q[0];
+    if (F32) r.v[F32 ? 1 : 0] = q[1];
+}
 template <bool F32, bool BF>
-__device__ __forceinline__ void load8(const void* p, long long i, float* f) {
+__device__ __forceinline__ void widen(const Raw<F32>& r, float* f) {
     if (F32) {
-        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-        const float4 a = q[0], b = q[1];
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4& v = r.v[F32 ? h : 0];
+            f[4 * h] = __uint_as_float(v.x);
+            f[4 * h + 1] = __uint_as_float(v.y);
+            f[4 * h + 2] = __uint_as_float(v.z);
+            f[4 * h + 3] = __uint_as_float(v.w);
+        }
     } else {
-        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (BF) {
@@ -77,47 +99,105 @@ __device__ __forceinline__ void store8(void* p, long long i, const float* f) {
     }
 }
 
-template <bool BF>
-__device__ __forceinline__ void load8_any(bool f32, const void* p, long long i, float* f) {
-    if (f32) load8<true, BF>(p, i, f);
-    else load8<false, BF>(p, i, f);
+template <bool F32, bool BF>
+__device__ __forceinline__ void load8(const void* p, long long i, float* f) {
+    Raw<F32> r;
+    load_raw<F32>(p, i, r);
+    widen<F32, BF>(r, f);
 }
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// Values whose type the kernel is not compiled for.  With AHEAD those of 16 bits are fetched ahead of their use, all others
+// at it.
+template <bool AHEAD>
+struct Later {
+    Raw<false> r;
+    __device__ __forceinline__ void fetch(bool f32, const void* p, long long i) {
+        if (AHEAD && !f32) load_raw<false>(p, i, r);
+    }
+    template <bool BF>
+    __device__ __forceinline__ void get(bool f32, const void* p, long long i, float* f) {
+        if (f32) {
+            Raw<true> q;
+            load_raw<true>(p, i, q);
+            widen<true, BF>(q, f);
+        } else {
+            if (!AHEAD) load_raw<false>(p, i, r);
+            widen<false, BF>(r, f);
+        }
+    }
+};
 
 // Sum over the threads of a row, the same in all of them.
 __device__ __forceinline__ float row_sum(float v, bool cta, float* ws) {
     v = ft::warp_sum(v);
     if (!cta) return v;
-    const int nw = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) ws[threadIdx.x >> 5] = v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) ws[threadIdx.x >> 5] = v;
     __syncthreads();
-    float s = 0.f;
-    for (int i = 0; i < nw; ++i) s += ws[i];
-    return s;
+    v = lane < (int)(blockDim.x >> 5) ? ws[lane] : 0.f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);  // (at most 16 warps)
+    return __shfl_sync(0xffffffffu, v, 0);
 }
 
 // BF: the 16-bit type is bf16, else f16; B32, R32, O32: block, residual, out are fp32.
 template <bool BF, bool B32, bool R32, bool O32, int NV>
-__global__ void __launch_bounds__(512) block_norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(512, NV == 1 ? 3 : 1) block_norm_kernel(const NormParams p) {
     __shared__ float ws[2][32];
     ft::grid_dep_launch();
-    ft::grid_dep_wait();
     const bool cta = p.tpr != 32;
-    const int t = cta ? blockIdx.x : blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const long long t = cta ? blockIdx.x : (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int tid = cta ? threadIdx.x : threadIdx.x & 31;
+    ft::grid_dep_wait();
     if (t >= p.T) return;  // whole warps
-    const long long rb = t * p.ld_b, rr = t * p.ld_r;
+    const long long rb = t * p.ld_b, rr = t * p.ld_r, rg = p.gate_kind == FT_GATE_FULL ? t * p.ld_g : 0;
+    // Of long rows the weights are asked for at once as well; of shorter ones their registers cost more CTAs than the wait for
+    // them (8192 tokens of 2048 30.0 us instead of 23.8; 2048 of 16384 69.0 instead of 83.8).
+    constexpr bool W_AHEAD = NV == 4;
+    Later<W_AHEAD> post_in[NV], pre_in[NV];
     float a[NV][8], h[NV][8];
+    if constexpr (W_AHEAD) {
+        Raw<B32> b_in[NV];
+        Raw<R32> r_in[NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int i = v * p.tpr + tid;
-        if (i < p.nvec) {
-            load8<R32, BF>(p.resid, rr + 8 * i, h[v]);
-            if (p.block) load8<B32, BF>(p.block, rb + 8 * i, a[v]);
-        } else {
+        for (int v = 0; v < NV; ++v) {
+            const int i = v * p.tpr + tid;
+            if (i >= p.nvec) continue;
+            load_raw<R32>(p.resid, rr + 8 * i, r_in[v]);
+            if (p.block) load_raw<B32>(p.block, rb + 8 * i, b_in[v]);
+            if (p.post) post_in[v].fetch(p.w32, p.post, 8 * i);
+            if (p.pre && p.out) pre_in[v].fetch(p.w32, p.pre, 8 * i);
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) h[v][k] = a[v][k] = 0.f;
+            if (v * p.tpr + tid < p.nvec) {
+                widen<R32, BF>(r_in[v], h[v]);
+                if (p.block) widen<B32, BF>(b_in[v], a[v]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int i = v * p.tpr + tid;
+            if (i < p.nvec) {
+                load8<R32, BF>(p.resid, rr + 8 * i, h[v]);
+                if (p.block) load8<B32, BF>(p.block, rb + 8 * i, a[v]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) h[v][k] = a[v][k] = 0.f;
+            }
         }
     }
+    if (p.gate_kind == FT_GATE_FULL)  // (into L2: no registers)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int i = v * p.tpr + tid;
+            if (i < p.nvec) prefetch_l2(static_cast<const uint8_t*>(p.gate) + (rg + 8 * i) * (p.g32 ? 4 : 2));
+        }
     if (p.block) {
         float f = p.bs;
         if (p.post_norm) {
@@ -133,7 +213,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const NormParams p) {
                 const int i = v * p.tpr + tid;
                 float w[8];
                 if (p.post && i < p.nvec) {
-                    load8_any<BF>(p.w32, p.post, 8 * i, w);
+                    post_in[v].template get<BF>(p.w32, p.post, 8 * i, w);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) a[v][k] = a[v][k] * r * w[k];
                 } else {
@@ -149,13 +229,12 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const NormParams p) {
             else g = __half2float(static_cast<const __half*>(p.gate)[t]);
             f *= g;
         } else if (p.gate_kind != FT_GATE_NONE) {
-            const long long g0 = p.gate_kind == FT_GATE_FULL ? t * p.ld_g : 0;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 const int i = v * p.tpr + tid;
                 float g[8];
                 if (i < p.nvec) {
-                    load8_any<BF>(p.g32, p.gate, g0 + 8 * i, g);
+                    Later<false>().get<BF>(p.g32, p.gate, rg + 8 * i, g);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) a[v][k] *= g[k];
                 }
@@ -192,7 +271,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const NormParams p) {
         if (i >= p.nvec) continue;
         float w[8];
         if (p.pre) {
-            load8_any<BF>(p.w32, p.pre, 8 * i, w);
+            pre_in[v].template get<BF>(p.w32, p.pre, 8 * i, w);
 #pragma unroll
             for (int k = 0; k < 8; ++k) h[v][k] = h[v][k] * r * w[k];
         } else {
@@ -293,11 +372,12 @@ extern "C" ft_status ft_block_norm(const ft_norm_desc* d, int32_t T, const void*
     p.resid_out = resid_out; p.out = out;
     p.ld_b = ld_b; p.ld_g = ld_g; p.ld_r = ld_r; p.ld_ro = ld_ro; p.ld_o = ld_o;
     p.eps = d->eps; p.rs = d->resid_scale; p.bs = d->block_scale;
-    // a row of at most 128 vectors is a warp's, a longer one a CTA's
+    // a row of at most 64 vectors is a warp's, a longer one a CTA's (8192 tokens of 1024: a warp 21.4 us, a CTA 16.3; 16384 of
+    // 512: 16.8 and 19.0)
     int nv, threads, grid;
-    if (p.nvec <= 128) {
+    if (p.nvec <= 64) {
         p.tpr = 32;
-        nv = p.nvec <= 32 ? 1 : p.nvec <= 64 ? 2 : 4;
+        nv = p.nvec <= 32 ? 1 : 2;
         threads = 128;
         grid = (T + 3) / 4;
     } else {

@@ -319,10 +319,9 @@ __device__ __forceinline__ void list_tokens(const KvCtl& c, const BatchOut& o, i
     }
 }
 
-#ifndef LH
-#define LH 1024
-#endif
-constexpr int LIST_HERE = LH;   // tokens that the first kernel lists itself
+// Tokens that the first kernel lists itself: 2000 tokens of 500 requests 7.6 us with one kernel, 8.8 with two; 3300 of 1024
+// requests 13.2 and 12.0.
+constexpr int LIST_HERE = 2048;
 constexpr int BATCH_SMEM = 2048;  // requests that are kept in shared memory
 
 struct TokPage {
