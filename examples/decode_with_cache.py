@@ -5,10 +5,11 @@ the expert cache.
 
     python examples/decode_with_cache.py
 
-Every layer of a step is: norm, projection, ft_qk_rope_store, ft_attn_forward,
-output projection, norm, router, ft_route_ctl, ft_moe_forward.  Weights are
-random; the projections, the residual sums and the choice of the next token
-are plain torch.
+A step starts with ft_kv_batch; every layer of it is: projection,
+ft_qk_rope_store, ft_attn_forward, output projection, ft_block_norm, router,
+ft_route_ctl, ft_moe_forward, ft_block_norm.  Weights are random; the projections
+and the choice of the next token are plain torch (beam_search.py has the
+library choose).
 """
 from __future__ import annotations
 
@@ -24,10 +25,6 @@ import moe_expert_cache_gb300 as ft  # noqa: E402
 import synth  # noqa: E402
 
 BF16 = torch.bfloat16
-
-
-def rms(x, eps=1e-6):
-    return x * torch.rsqrt((x * x).mean(-1, keepdim=True) + eps)
 
 
 class Model:
@@ -68,45 +65,55 @@ class Model:
         self.refs = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
         self.kv = ft.KvCache(L, Hq, Hkv, D, page, n_pages, rows, row_pages, self.pool, self.table, self.lens, self.refs,
                              T_max=T_max, B_max=rows)
+        # the norms: before the first layer, after attention, after the experts (fp32), and the last one, for the head
+        self.norm_in = ft.BlockNorm(H)
+        self.norm_attn = ft.BlockNorm(H)
+        self.norm_moe = ft.BlockNorm(H, block_type=ft.FT_T_F32)
+        self.norm_last = ft.BlockNorm(H, block_type=ft.FT_T_F32, out_type=ft.FT_T_F32)
 
     def ints(self, v):
         return torch.tensor(list(v), dtype=torch.int32, device="cuda")
 
-    def step(self, rows, tokens, starts, shared=0):
-        """tokens[i] (a list) go on row rows[i] from position starts[i] on; the rows' first `shared` tokens are on
-        the same pages.  Returns the hidden states of all tokens, in order."""
-        n = [len(t) for t in tokens]
-        T, w = sum(n), self.Hq * self.D
-        ids = torch.tensor([t for ts in tokens for t in ts], device="cuda")
-        row_ids = self.ints(rows)
-        row_of = self.ints(r for r, c in zip(rows, n) for _ in range(c))
-        pos = self.ints(s + i for s, c in zip(starts, n) for i in range(c))
-        cu = self.ints(np.concatenate([[0], np.cumsum(n)]).tolist())
-        self.kv.extend(len(rows), row_ids, self.ints(n))
-        group = {}
-        if shared and len(rows) > 1:  # (without a claim requests of few tokens run the faster form)
-            group = dict(n_groups=1, group_start=self.ints([0, len(rows)]), group_tokens=self.ints([shared]))
-        self.kv.attn_plan(len(rows), T, cu, rows=row_ids, **group)
-        h = self.embed[ids].clone()
+    def lay_out(self, B, add, T, rows=None):
+        """The rows grow by add[b] tokens (a device list); their lists are padded to T."""
+        self.cu, self.row_of, self.pos = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (B + 1, T, T))
+        self.kv.batch(B, add, T, self.cu, self.row_of, self.pos, rows=rows)
+
+    def forward(self, ids, B, T, rows=None, **group):
+        """ids [T] are the tokens that lay_out listed.  Returns their hidden states and those after the last norm."""
+        H, w = self.H, self.Hq * self.D
+        self.kv.attn_plan(B, T, self.cu, rows=rows, **group)
+        h = self.embed[ids]
         q = torch.empty(T, w, dtype=BF16, device="cuda")
-        o = torch.empty_like(q)
-        y = torch.empty(T, self.H, device="cuda")
+        o = torch.zeros_like(q)  # (nothing is written for padding)
+        x = torch.empty(T, H, dtype=BF16, device="cuda")
+        y, last = (torch.empty(T, H, device="cuda") for _ in range(2))
+        self.norm_in.forward(T, h, H, out=x, ld_o=H)
         for l in range(self.L):
-            qkv = rms(h).to(BF16) @ self.qkv[l]
-            self.kv.qk_rope_store(l, T, qkv, qkv.shape[1], row_of, pos, q, w, q_norm=self.q_norm[l], k_norm=self.k_norm[l],
-                                  cos_sin=self.cos_sin, max_pos=self.max_pos, rot=self.D)
+            qkv = x @ self.qkv[l]
+            self.kv.qk_rope_store(l, T, qkv, qkv.shape[1], self.row_of, self.pos, q, w, q_norm=self.q_norm[l],
+                                  k_norm=self.k_norm[l], cos_sin=self.cos_sin, max_pos=self.max_pos, rot=self.D)
             self.kv.attn_forward(l, q, w, o, w, self.D ** -0.5)
-            h += (o @ self.out[l]).float()
-            x = rms(h).to(BF16)
+            self.norm_attn.forward(T, h, H, block=o @ self.out[l], ld_b=H, resid_out=h, ld_ro=H, out=x, ld_o=H)
             logits = x.float() @ self.router[l]
             # B_P = B_H: every expert that is missing is fetched, none is left to the host
             self.moe.route_ctl(l, T, logits=logits, B_P=1.0, B_H=1.0)
             self.moe.moe_forward(x, None, y)
-            h += y
-        return h
+            norm, out = (self.norm_moe, x) if l + 1 < self.L else (self.norm_last, last)
+            norm.forward(T, h, H, block=y, ld_b=H, resid_out=h, ld_ro=H, out=out, ld_o=H)
+        return h, last
 
-    def next_tokens(self, h):
-        return (rms(h) @ self.head).argmax(-1).tolist()
+    def step(self, rows, tokens, shared=0):
+        """tokens[i] (a list) go on row rows[i]; the rows' first `shared` tokens are on the same pages.  Returns the
+        hidden states of all tokens, in order, and those after the last norm."""
+        n = [len(t) for t in tokens]
+        row_ids = self.ints(rows)
+        self.lay_out(len(rows), self.ints(n), sum(n), row_ids)
+        group = {}
+        if shared and len(rows) > 1:  # (without a claim requests of few tokens run the faster form)
+            group = dict(n_groups=1, group_start=self.ints([0, len(rows)]), group_tokens=self.ints([shared]))
+        ids = torch.tensor([t for ts in tokens for t in ts], device="cuda")
+        return self.forward(ids, len(rows), sum(n), row_ids, **group)
 
 
 def run(prompt_len=150, forks=4, new=12, seed=0, verbose=True, **sizes):
@@ -115,15 +122,15 @@ def run(prompt_len=150, forks=4, new=12, seed=0, verbose=True, **sizes):
     rng = np.random.default_rng(seed)
     prompt = [int(t) for t in rng.integers(0, m.embed.shape[0], prompt_len)]
     for at in range(0, prompt_len, m.T_max):  # the prompt in chunks
-        h = m.step([0], [prompt[at:at + m.T_max]], [at])
-    first = torch.topk(rms(h[-1:]) @ m.head, forks).indices[0].tolist()
+        h, last = m.step([0], [prompt[at:at + m.T_max]])
+    first = torch.topk(last[-1:] @ m.head, forks).indices[0].tolist()
     rows = list(range(1, forks + 1))
     m.kv.fork(forks, m.ints([0] * forks), m.ints(rows))  # complete pages are shared, the last one is copied
     shared = prompt_len // m.page * m.page
     answers = [[t] for t in first]
     for i in range(new):
-        h = m.step(rows, [[a[-1]] for a in answers], [prompt_len + i] * forks, shared)
-        for a, t in zip(answers, m.next_tokens(h)):
+        h, last = m.step(rows, [[a[-1]] for a in answers], shared)
+        for a, t in zip(answers, (last @ m.head).argmax(-1).tolist()):
             a.append(t)
     # the prompt's own row and every second answer end; the others' pages move together
     gone = [0] + rows[1::2]
@@ -131,7 +138,7 @@ def run(prompt_len=150, forks=4, new=12, seed=0, verbose=True, **sizes):
     m.kv.compact()
     info = m.kv.last()
     rows, answers = rows[::2], answers[::2]
-    h = m.step(rows, [[a[-1]] for a in answers], [prompt_len + new] * len(rows), shared)
+    h, _ = m.step(rows, [[a[-1]] for a in answers], shared)
     assert m.kv.status() == ft.FT_OK and m.moe.status() == ft.FT_OK
     if verbose:
         print("answers:", answers)
