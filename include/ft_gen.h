@@ -119,7 +119,10 @@ ft_status ft_beam_init(ft_beam** out, int32_t V, int32_t dtype, int32_t R_max, i
  * overlap anything else.
  * A row with a NaN or a logit of +inf, and a score that is NaN or +inf, latch
  * FT_ERR_DEVICE; that beam has no candidates.
- * Errors: FT_ERR_ARG, FT_ERR_CUDA.
+ * The calls of a handle share its scratch: they run one after another on its
+ * stream, and graphs captured from it must not run at the same time.
+ * Errors: FT_ERR_ARG, FT_ERR_STATE (another device than the handle's is
+ * current), FT_ERR_CUDA.
  */
 ft_status ft_beam_select(ft_beam* bm, int32_t B, int32_t K, int32_t N, const void* logits, int64_t ld,
                          const float* scores, const int32_t* rows, const int32_t* done, int32_t eos, float* out_scores,

@@ -109,7 +109,8 @@ ft_status ft_kv_fork(ft_kv* kv, int32_t n, const int32_t* parents, const int32_t
  * in the list; every other child gets a copy of its tokens on a new page.
  * parents[i] = -1: the row becomes empty.  A parent need not be in the list and
  * may be listed more than once.  Pages that no row holds any more are free, for
- * the new pages of this call too.  rows NULL: row i.  n is at most 1024. */
+ * the new pages of this call too.  rows NULL: row i.  n is at most 1024.
+ * FT_ERR_STATE, here and below: another device than the handle's is current. */
 ft_status ft_kv_reorder(ft_kv* kv, int32_t n, const int32_t* rows, const int32_t* parents);
 
 /* Lay out a step: row rows[b] of each of B requests grows by add[b] >= 0 tokens

@@ -836,6 +836,8 @@ ft_status ft_beam_select(ft_beam* bm, int32_t B, int32_t K, int32_t N, const voi
         (done && eos < 0))
         return FT_ERR_ARG;
     if (B == 0) return FT_OK;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != bm->device) return FT_ERR_STATE;  // (its memory is elsewhere)
     const int size = bm->dtype == FT_T_F32 ? 4 : 2;
     if (!logits || !scores || !out_scores || !out_parents || !out_tokens || ld < bm->V || ld > (1ll << 40) || (uintptr_t)logits % size)
         return FT_ERR_ARG;

@@ -340,7 +340,8 @@ extern "C" ft_status ft_block_norm(const ft_norm_desc* d, int32_t T, const void*
     if (T == 0) return FT_OK;
     const bool full = d->gate == FT_GATE_FULL;
     const long long H = d->H;
-    auto bad_rows = [&](const void* p, long long ld) { return p && ((uintptr_t)p % 16 || ld < H || ld % 8 || ld > (1ll << 40)); };
+    // (rows whose last byte has no 62-bit offset are refused)
+    auto bad_rows = [&](const void* p, long long ld) { return p && ((uintptr_t)p % 16 || ld < H || ld % 8 || ld > (1ll << 60) / T); };
     if (!resid || (!resid_out && !out) || bad_rows(block, ld_b) || bad_rows(resid, ld_r) || bad_rows(resid_out, ld_ro) ||
         bad_rows(out, ld_o) || (full && bad_rows(gate, ld_g)) || (uintptr_t)d->post % 16 || (uintptr_t)d->pre % 16 ||
         (!block && (d->post_norm || d->gate != FT_GATE_NONE)) || (d->gate != FT_GATE_NONE && !gate) ||

@@ -62,6 +62,12 @@ ft_status launched(cudaError_t e) {
     return FT_ERR_CUDA;
 }
 
+// Whether the handle's device is the current one: its memory is on no other.
+bool at_home(const ft_kv* kv) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == kv->device;
+}
+
 bool misaligned(const void* p, size_t a) { return (uintptr_t)p % a != 0; }
 
 // Whether rows [n] of w values of 2 bytes at a, ld values apart, and of v values at b, ld_b apart, may touch: their spans
@@ -176,7 +182,9 @@ ft_status ft_kv_compact(ft_kv* kv) {
 }
 
 ft_status ft_kv_reorder(ft_kv* kv, int32_t n, const int32_t* rows, const int32_t* parents) {
-    if (!kv || n < 0 || n > kv->n_rows || n > 1024 || (n > 0 && !parents)) return FT_ERR_ARG;
+    if (!kv || n < 0 || n > kv->n_rows || n > 1024 || (n > 0 && !parents) || misaligned(rows, 4) || misaligned(parents, 4))
+        return FT_ERR_ARG;
+    if (!at_home(kv)) return FT_ERR_STATE;
     return launched(launch_kv_reorder(kv, n, rows, parents));
 }
 
@@ -194,6 +202,7 @@ ft_status ft_kv_batch(ft_kv* kv, int32_t B, const int32_t* rows, const int32_t* 
             if (m[a].p && m[b].p && m[a].n && m[b].n && (uintptr_t)m[a].p < (uintptr_t)m[b].p + m[b].n &&
                 (uintptr_t)m[b].p < (uintptr_t)m[a].p + m[a].n)
                 return FT_ERR_ARG;
+    if (!at_home(kv)) return FT_ERR_STATE;
     return launched(launch_kv_batch(kv, B, rows, add, T, cu_q, row_of, pos, (long long*)slots));
 }
 

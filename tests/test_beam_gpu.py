@@ -291,3 +291,77 @@ def test_rows_far_apart():
     g = torch.Generator(device="cuda").manual_seed(0)
     x.copy_(torch.randn(10, V, generator=g, device="cuda"))
     _check(2, 5, 5, x, ld, [0.0] * 10, kind="bf16")
+
+
+def test_many_requests():
+    # more rows than warps run at once
+    x, ld = _logits(6000, 61, "f16", seed=8, extra=2)
+    r = np.random.default_rng(0)
+    _check(3000, 2, 3, x, ld, (-r.random(6000)).astype(np.float32), kind="f16")
+
+
+def test_what_lies_around_the_outputs():
+    import torch
+
+    import moe_expert_cache_gb300 as ft
+    B, K, N, V = 5, 3, 7, 2500
+    x, ld = _logits(B * K, V, "bf16", seed=1)
+    x[:, 3:] = -math.inf  # few candidates
+    bm = ft.Beams(V, B * K, N, dtype=ft.FT_T_BF16)
+    sc = torch.zeros(B * K, device="cuda")
+    buf = torch.full((4, 4 + B * N + 4), 99, dtype=torch.int32, device="cuda")
+    f = buf[0].view(torch.float32)
+    bm.select(B, K, N, x, ld, sc, f[4:], buf[1, 4:], buf[2, 4:], eos=2, out_done=buf[3, 4:])
+    assert bm.status() == ft.FT_OK
+    assert (buf[:, :4] == 99).all() and (buf[:, 4 + B * N:] == 99).all()
+    mid = slice(4, 4 + B * N)
+    assert bool(((buf[2, mid] >= 0) & (buf[2, mid] < 3)).all()) and torch.equal(buf[3, mid] == 1, buf[2, mid] == 2)
+
+
+def test_handles_at_once():
+    # two handles on two streams, calls of both in flight
+    import torch
+
+    import moe_expert_cache_gb300 as ft
+    B, K, V = 16, 4, 50003
+    x, ld = _logits(B * K, V, "f32", seed=3)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    sc = torch.zeros(B * K, device="cuda")
+    hs = [ft.Beams(V, B * K, K, stream=s.cuda_stream) for s in streams]
+    outs = [[[torch.empty(B * K, device="cuda")] + [torch.empty(B * K, dtype=torch.int32, device="cuda") for _ in range(2)]
+             for _ in range(8)] for _ in hs]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for h, o in zip(hs, outs):
+            h.select(B, K, K, x, ld, sc, *o[i])
+    torch.cuda.synchronize()
+    for o in outs:
+        for t in o:
+            assert all(torch.equal(a, b) for a, b in zip(t, outs[0][0]))
+
+
+def test_refusals():
+    import torch
+
+    import moe_expert_cache_gb300 as ft
+    B, K, N, V = 2, 3, 4, 100
+    x, ld = _logits(B * K, V, "bf16")
+    bm = ft.Beams(V, 6, 4, dtype=ft.FT_T_BF16)
+    i = torch.zeros(400, dtype=torch.int32, device="cuda")
+    f = torch.zeros(100, device="cuda")
+    P, F, X = i.data_ptr(), f.data_ptr(), x.data_ptr()
+    ok = dict(B=B, K=K, N=N, logits=X, ld=V, scores=F, rows=P, done=P + 128, eos=5, os=F + 128, op=P + 256, ot=P + 384, od=P + 512)
+
+    def call(**kw):
+        return ft.beam_select(bm.h, *{**ok, **kw}.values())
+    assert call() == ft.FT_OK and bm.status() == ft.FT_OK
+    for bad in (dict(B=-1), dict(B=3), dict(K=0), dict(K=65), dict(N=0), dict(N=5), dict(logits=None), dict(logits=X + 1), dict(ld=99),
+                dict(ld=1 << 41), dict(scores=None), dict(scores=F + 2), dict(eos=-2), dict(eos=100), dict(eos=-1), dict(os=None),
+                dict(op=None), dict(ot=None), dict(rows=P + 1), dict(done=P + 130), dict(od=P + 514), dict(os=F), dict(os=F + 4),
+                dict(op=P), dict(op=P + 20), dict(ot=P + 256), dict(ot=P + 280), dict(od=P + 128), dict(od=P + 384), dict(os=X), dict(os=X + 64),
+                dict(op=F + 20), dict(N=3, os=F + 4), dict(N=3, od=P + 132), dict(N=3, op=F), dict(N=3, od=P)):
+        assert call(**bad) == ft.FT_ERR_ARG, bad
+    assert call(N=3, os=F, od=P + 128) == ft.FT_OK  # in place
+    assert call(rows=None, done=None, eos=-1, od=None) == ft.FT_OK
+    assert bm.status() == ft.FT_OK
+    assert ft.beam_scratch_bytes(V, 0, 6, 4) > 0

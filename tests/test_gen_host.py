@@ -21,7 +21,7 @@ def test_norm_arguments():
            dict(resid_out=None, out=None), dict(ld_b=56), dict(ld_r=68), dict(ld_ro=0), dict(ld_o=-64), dict(block=P + 8), dict(out=P + 2),
            dict(pre=P + 8), dict(post=P + 2, post_norm=1),
            dict(gate=1, gp=5 * P + 8), dict(gate=3, gp=5 * P), dict(gate=2, gp=5 * P + 1), dict(gate=3, gp=5 * P, ld_g=60),
-           dict(gate=2, gate_type=2, gp=5 * P + 2), dict(ld_b=1 << 62)]
+           dict(gate=2, gate_type=2, gp=5 * P + 2), dict(ld_b=1 << 62), dict(ld_o=1 << 58, T=5), dict(ld_r=(1 << 60) + 8, T=1)]
     for b in bad:
         assert _norm(**b) == ft.FT_ERR_ARG, b
     assert _norm(T=0) == ft.FT_OK
