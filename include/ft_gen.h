@@ -129,8 +129,7 @@ ft_status ft_beam_select(ft_beam* bm, int32_t B, int32_t K, int32_t N, const voi
                          int32_t* out_parents, int32_t* out_tokens, int32_t* out_done);
 
 /* Synchronise the stream and return, then clear, what the device latched since
- * the last call: FT_OK, FT_ERR_DEVICE or FT_ERR_TIMEOUT (a bounded wait gave up;
- * outputs since the last status are not valid). */
+ * the last call: FT_OK or FT_ERR_DEVICE. */
 ft_status ft_beam_status(ft_beam* bm);
 
 /* Free the handle and its scratch.  Syncs.  bm may be NULL. */

@@ -23,6 +23,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <new>
+#include <type_traits>
 
 struct ft_beam {
     int V, dtype, R_max, N_max;
@@ -48,7 +49,6 @@ constexpr int SCAN_WARPS = SCAN_CT / 32;
 constexpr int PER_SM = 7;          // its CTAs of an SM
 constexpr int NJ = 4;              // vectors of a lane in a tile
 constexpr int TILE = 32 * NJ;      // vectors of a tile
-constexpr int STAGES = 3;          // tiles of a warp in shared memory
 constexpr int WCAP = 128;          // candidates of a warp
 constexpr int CT = 512;            // threads of a CTA of the second kernel
 constexpr int WARPS = CT / 32;
@@ -143,6 +143,28 @@ __device__ __forceinline__ float max_of(const uint4& v) {
     const __half2* h = reinterpret_cast<const __half2*>(w);
     const float2 t = __half22float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
     return fmaxf(t.x, t.y);
+}
+
+// The same of a lane's vectors of a tile.
+template <int TYPE>
+__device__ __forceinline__ float max_of_all(const uint4 (&v)[NJ]) {
+    if (TYPE == FT_T_F32) {
+        float m = max_of<TYPE>(v[0]);
+#pragma unroll
+        for (int j = 1; j < NJ; ++j) m = fmaxf(m, max_of<TYPE>(v[j]));
+        return m;
+    }
+    typedef typename std::conditional<TYPE == FT_T_BF16, __nv_bfloat162, __half2>::type Pair;
+    Pair m = *reinterpret_cast<const Pair*>(&v[0].x);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = __hmax2(m, *reinterpret_cast<const Pair*>(&w[k]));
+    }
+    const uint4 t = make_uint4(*reinterpret_cast<uint32_t*>(&m), *reinterpret_cast<uint32_t*>(&m), *reinterpret_cast<uint32_t*>(&m),
+                               *reinterpret_cast<uint32_t*>(&m));
+    return max_of<TYPE>(t);
 }
 
 // The vector of values i..i+VEC-1 of a row of V, of which some are outside it: those are -inf.
@@ -319,33 +341,34 @@ __device__ __forceinline__ uint4 load_vector(const uint8_t* row, int q, int shif
 }
 
 struct ScanSmem {
-    uint8_t ring[SCAN_WARPS][STAGES][TILE * 16];
     uint64_t list[SCAN_WARPS][WCAP];
     alignas(16) float group[SCAN_WARPS][TILE];
-    uint64_t bars[SCAN_WARPS][STAGES];
+    uint32_t row_bar[SCAN_WARPS];  // of each of the CTA's rows: order of a value that its N-th largest is not below
 };
 
-// Each warp: a chunk's sum and its N best vectors to the workspace.  Tiles that lie within the chunk and the row come by
-// bulk copies into STAGES places in shared memory, the next ones in flight while one is worked on; the few others (a
-// row's first and last) are loaded when their turn comes.
+// Each warp: a chunk's sum and its N best vectors to the workspace, a tile at a time, the next tile's loads in flight while
+// one is worked on.
+//
+// Bound: of a large batch by instructions (about 8 for each 32 logits of 16 bits: 1 to widen them, 1/2 each for the
+// argument and the sum as pairs, 1 for the exponential, 1/2 for the maximum, the rest for loads, loop and candidates; issue
+// slots 73% busy) and by HBM.  Measured: 128 x 8 rows of 131072 in bf16 49.4 us, 5.4 TB/s, of the call's 52.8.  Left out:
+// tiles by bulk copies of 2 KB into shared memory, 3 a warp, with as fast a loop (a copy alone runs at 3.6 TB/s with 84 of
+// them in flight an SM, at 7.2 with 8 KB, plain loads at 7.3); CTAs that share a chunk and meet at barriers (97 us); 8 CTAs
+// an SM, whose 64 registers spill (59.8).
 template <int TYPE>
 __global__ void __launch_bounds__(SCAN_CT, PER_SM) beam_scan_kernel(const SelParams p) {
     constexpr int VEC = TYPE == FT_T_F32 ? 4 : 8, SIZE = TYPE == FT_T_F32 ? 4 : 2;
-    extern __shared__ __align__(128) uint8_t smem[];
-    ScanSmem& s = *reinterpret_cast<ScanSmem*>(smem);
+    __shared__ ScanSmem s;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    uint64_t* bars = s.bars[wid];
     uint64_t* list = s.list[wid];
-    if (lane == 0) {
-        for (int i = 0; i < STAGES; ++i) ft::mbar_init(bars + i, 1);
-        ft::mbar_fence_init();
-    }
-    __syncwarp();
+    if (lane == 0) s.row_bar[wid] = 0;
+    __syncthreads();
     ft::grid_dep_launch();
     ft::grid_dep_wait();
     const int item = blockIdx.x * SCAN_WARPS + wid;
     if (item >= p.items) return;
     const int r = item / p.C;
+    uint32_t* row_bar = &s.row_bar[r - blockIdx.x * SCAN_WARPS / p.C];
     const float score = p.scores[r];
     const int ended = p.done ? p.done[r] : 0;
     if (!(score > -INFINITY) || ended) return;  // no candidates, or one that is not in the logits
@@ -356,21 +379,21 @@ __global__ void __launch_bounds__(SCAN_CT, PER_SM) beam_scan_kernel(const SelPar
     const int q1 = min(q + p.vpc, (p.V + shift + VEC - 1) / VEC);
     // tiles at q < w0 or >= w1 are not whole
     const int w0 = shift ? 1 : 0, w1 = min(q1, (p.V + shift) / VEC) - TILE + 1;
-    int ahead = q, asked = 0, got = 0;
-    auto ask = [&] {  // for the next whole tile, if there is one
-        if (ahead < w0) ahead += TILE;
-        if (ahead < w1) {
-            if (lane == 0) {
-                const int st = asked % STAGES;
-                ft::mbar_arrive_expect_tx(bars + st, TILE * 16);
-                ft::bulk_g2s(s.ring[wid][st], row + (long long)ahead * 16 - shift * SIZE, TILE * 16, bars + st);
+    const uint4* vectors = reinterpret_cast<const uint4*>(row - shift * SIZE);
+    auto load = [&](int q, uint4 (&v)[NJ]) {
+        if (q >= w0 && q < w1) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) v[j] = __ldcs(vectors + q + 32 * j + lane);
+        } else {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int mine = q + 32 * j + lane;
+                const uint32_t none = TYPE == FT_T_F32 ? 0xff800000u : TYPE == FT_T_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+                v[j] = make_uint4(none, none, none, none);
+                if (mine < q1) v[j] = load_vector<TYPE>(row, mine, shift, p.V);
             }
-            ++asked;
-            ahead += TILE;
         }
     };
-#pragma unroll
-    for (int i = 0; i < STAGES; ++i) ask();
 
     // Sum of exponentials, 2^(x log2(e) - c) with c a whole number near the first tile's largest exponent, so that each
     // exponent is rounded once; the reference in x is c / log2(e) with the same constant.  Beyond 2^20 an fp32 does not
@@ -383,32 +406,14 @@ __global__ void __launch_bounds__(SCAN_CT, PER_SM) beam_scan_kernel(const SelPar
     uint64_t own = 0;
     int cnt = 0;
     bool barred = false;
+    uint4 next[NJ];
+    if (q < q1) load(q, next);
     for (; q < q1; q += TILE) {
         uint4 v[NJ];
-        if (q >= w0 && q < w1) {
-            const int st = got % STAGES;
-            ft::mbar_wait(bars + st, (got / STAGES) & 1, p.err);
-            const uint4* t = reinterpret_cast<const uint4*>(s.ring[wid][st]);
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) v[j] = t[32 * j + lane];
-            ++got;
-            __syncwarp();  // all lanes have read: the place is free
-            ask();
-        } else {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int mine = q + 32 * j + lane;
-                const uint32_t none = TYPE == FT_T_F32 ? 0xff800000u : TYPE == FT_T_BF16 ? 0xff80ff80u : 0xfc00fc00u;
-                v[j] = make_uint4(none, none, none, none);
-                if (mine < q1) v[j] = load_vector<TYPE>(row, mine, shift, p.V);
-            }
-        }
-        float mj[NJ], m = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            mj[j] = max_of<TYPE>(v[j]);
-            m = fmaxf(m, mj[j]);
-        }
+        for (int j = 0; j < NJ; ++j) v[j] = next[j];
+        if (q + TILE < q1) load(q + TILE, next);
+        const float m = max_of_all<TYPE>(v);
         const bool rare = __any_sync(0xffffffffu, m > limit || (barred && m >= bar));
         if (rare && __any_sync(0xffffffffu, m > limit)) {
             float top = m;
@@ -453,10 +458,16 @@ __global__ void __launch_bounds__(SCAN_CT, PER_SM) beam_scan_kernel(const SelPar
             }
         }
         if (!rare) continue;
+        float mj[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) mj[j] = max_of<TYPE>(v[j]);
         if (!barred && set) {  // the first tile that has values
             bar = fmaxf(nth_of_warp(mj, m, p.N, s.group[wid]), __uint_as_float(0xff7fffffu));  // (no -inf passes)
             barred = true;
+            if (lane == 0) atomicMax(row_bar, ord(bar));
         }
+        // (what other warps found in the same row counts as well)
+        bar = fmaxf(bar, unord(max(*reinterpret_cast<volatile uint32_t*>(row_bar), 0x00800000u)));
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             if (!__any_sync(0xffffffffu, mj[j] >= bar)) continue;
@@ -470,6 +481,7 @@ __global__ void __launch_bounds__(SCAN_CT, PER_SM) beam_scan_kernel(const SelPar
                 cnt = compact_list(list, cnt, p.N);
                 own = list[cnt - 1];
                 bar = fmaxf(bar, unord((uint32_t)(own >> 32)));
+                if (lane == 0) atomicMax(row_bar, (uint32_t)(own >> 32));
             }
         }
     }
@@ -481,9 +493,6 @@ __global__ void __launch_bounds__(SCAN_CT, PER_SM) beam_scan_kernel(const SelPar
     uint64_t* out = p.keys + (long long)item * p.N;
     const int turn = item * 7 % p.N;
     for (int i = lane; i < p.N; i += 32) out[i + turn < p.N ? i + turn : i + turn - p.N] = i < cnt ? list[i] : 0;
-    // (a wait that gave up: its copy must land before the CTA ends)
-    if (lane == 0)
-        for (int i = got; i < asked; ++i) ft::mbar_wait(bars + i % STAGES, (i / STAGES) & 1, p.err);
 }
 
 // The N best of what the chunks of a request left.
@@ -749,11 +758,6 @@ bool sizes_ok(int V, int dtype, int R_max, int N_max) {
            N_max <= MAX_N;
 }
 
-template <int TYPE>
-cudaError_t setup_kernel() {
-    return cudaFuncSetAttribute((const void*)beam_scan_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(ScanSmem));
-}
-
 struct Layout {
     long long lists;
     size_t err, sums, keys, total;
@@ -823,8 +827,6 @@ ft_status ft_beam_init(ft_beam** out, int32_t V, int32_t dtype, int32_t R_max, i
     bm->sums = (BeamSum*)(a + l.sums);
     bm->keys = (uint64_t*)(a + l.keys);
     bm->lists = l.lists;
-    if (setup_kernel<FT_T_BF16>() != cudaSuccess || setup_kernel<FT_T_F16>() != cudaSuccess || setup_kernel<FT_T_F32>() != cudaSuccess)
-        return fail(FT_ERR_CUDA);
     *out = bm;
     return FT_OK;
 }
@@ -866,7 +868,7 @@ ft_status ft_beam_select(ft_beam* bm, int32_t B, int32_t K, int32_t N, const voi
     p.vpc = tiles_of(vectors, (int)R, K, N, bm->num_sms) * TILE;
     p.C = (int)((vectors + p.vpc - 1) / p.vpc);
     p.items = (int)R * p.C;
-    p.raise = N <= 16 ? N + 8 : WCAP - 32;
+    p.raise = N <= 16 ? N + 8 : WCAP - 32;  // (the ballot after it may add 32)
     const void* scan = bm->dtype == FT_T_BF16  ? (const void*)beam_scan_kernel<FT_T_BF16>
                        : bm->dtype == FT_T_F16 ? (const void*)beam_scan_kernel<FT_T_F16>
                                                : (const void*)beam_scan_kernel<FT_T_F32>;
@@ -874,7 +876,7 @@ ft_status ft_beam_select(ft_beam* bm, int32_t B, int32_t K, int32_t N, const voi
                        : bm->dtype == FT_T_F16 ? (const void*)beam_join_kernel<FT_T_F16>
                                                : (const void*)beam_join_kernel<FT_T_F32>;
     void* args[] = {&p};
-    cudaError_t e = launch_dependent(scan, (p.items + SCAN_WARPS - 1) / SCAN_WARPS, SCAN_CT, sizeof(ScanSmem), bm->stream, args);
+    cudaError_t e = launch_dependent(scan, (p.items + SCAN_WARPS - 1) / SCAN_WARPS, SCAN_CT, 0, bm->stream, args);
     if (e == cudaSuccess) e = launch_dependent(join, B, CT, 0, bm->stream, args);
     if (e == cudaSuccess) return FT_OK;
     if (getenv("FT_DEBUG")) fprintf(stderr, "libft: launch -> %s\n", cudaGetErrorString(e));
@@ -888,7 +890,6 @@ ft_status ft_beam_status(ft_beam* bm) {
     if (cudaMemcpy(&e, bm->err, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return FT_ERR_CUDA;
     if (e && cudaMemset(bm->err, 0, 4) != cudaSuccess) return FT_ERR_CUDA;
     if (e && cudaDeviceSynchronize() != cudaSuccess) return FT_ERR_CUDA;
-    if (e & FT_DEVERR_TIMEOUT) return FT_ERR_TIMEOUT;
     return e ? FT_ERR_DEVICE : FT_OK;
 }
 
