@@ -55,6 +55,7 @@ constexpr int WARPS = CT / 32;
 constexpr int CAP = 1024;          // candidates that it ranks at once
 constexpr int HELD = 8;            // vectors' keys that a thread of it holds
 constexpr int MAX_N = 64, MAX_K = 64;
+constexpr int FEW = 16;            // candidates for which a warp's 32 lanes are groups enough
 constexpr int MAX_V = 2 * MAX_N;   // vectors whose values it looks at
 constexpr float LOG2E = 1.44269504088896340736f;  // rounded to fp32; used in both directions, so its error cancels
 
@@ -228,34 +229,45 @@ __device__ __forceinline__ void nth_of_groups(const float* group, int G, int N, 
     if (rank == N - 1) *bar = mine;
 }
 
-// The same within a warp: of the lanes' maxima m, or, for many, of their vectors' maxima g.
-__device__ __forceinline__ float nth_of_warp(const float (&g)[NJ], float m, int N, float* sh) {
-    const int lane = threadIdx.x & 31;
-    const bool all = N > 16;
-    sh[lane] = all ? g[0] : m;
-    if (all)
-#pragma unroll
-        for (int j = 1; j < NJ; ++j) sh[32 * j + lane] = g[j];
-    __syncwarp();
-    float bar = -INFINITY;
-#pragma unroll 1
-    for (int j = 0; j < (all ? NJ : 1); ++j) {
-        const float mine = sh[32 * j + lane];
-        const int at = 32 * j + lane;
+// Within a warp: a value that N or a few more of the groups' maxima are not below, -FLT_MAX where fewer are finite.  Few: of
+// the lanes' maxima m, by their ranks (a chain of halvings is longer: one request of four beams 8.4 -> 8.8 us).  Many: of their
+// vectors' maxima g, the range of their orders halved until such a value is found (ranks of 128: 1 x 4 beams, N = 64, 24.2
+// -> 39.1 us).
+__device__ __forceinline__ float bar_of_warp(const float (&g)[NJ], float m, int N, float* sh) {
+    const float lowest = __uint_as_float(0xff7fffffu);
+    if (N <= FEW) {
+        const int lane = threadIdx.x & 31;
+        sh[lane] = m;
+        __syncwarp();
         int rank = 0;
 #pragma unroll 2
-        for (int i = 0; i < (all ? 32 * NJ : 32); i += 4) {
+        for (int i = 0; i < 32; i += 4) {
             const float4 o = *reinterpret_cast<const float4*>(sh + i);
-            rank += o.x > mine || (o.x == mine && i < at);
-            rank += o.y > mine || (o.y == mine && i + 1 < at);
-            rank += o.z > mine || (o.z == mine && i + 2 < at);
-            rank += o.w > mine || (o.w == mine && i + 3 < at);
+            rank += o.x > m || (o.x == m && i < lane);
+            rank += o.y > m || (o.y == m && i + 1 < lane);
+            rank += o.z > m || (o.z == m && i + 2 < lane);
+            rank += o.w > m || (o.w == m && i + 3 < lane);
         }
         const unsigned who = __ballot_sync(0xffffffffu, rank == N - 1);
-        if (who) bar = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
+        return who ? fmaxf(__shfl_sync(0xffffffffu, m, __ffs(who) - 1), lowest) : lowest;
     }
-    __syncwarp();
-    return bar;
+    uint32_t o[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) o[j] = ord(g[j]);
+    uint32_t lo = ord(lowest), hi = __reduce_max_sync(0xffffffffu, ord(m)) + 1;
+    while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        int c = 0;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) c += __popc(__ballot_sync(0xffffffffu, o[j] >= mid));
+        if (c >= N) {
+            lo = mid;
+            if (c <= N + N / 8) break;
+        } else {
+            hi = mid;
+        }
+    }
+    return unord(lo);
 }
 
 // The maxima of groups of threads of a CTA, of each thread's m: so many groups that there are four and more for each of
@@ -301,30 +313,49 @@ __device__ __forceinline__ BeamSum join_sums(F part, int n) {
     return BeamSum{ref, l, far, 0};
 }
 
-// A warp's list shrinks to its N best, in order; returns their number.
-__device__ __noinline__ int compact_list(uint64_t* list, int cnt, int N) {
+// A warp's list of cnt > N keys shrinks to its N best, in any order; returns a key that none of them is below.
+__device__ __noinline__ uint64_t shrink_list(uint64_t* list, int cnt, int N) {
     const int lane = threadIdx.x & 31;
-    uint64_t k[WCAP / 32];
-    int rank[WCAP / 32] = {};
     __syncwarp();
-#pragma unroll
-    for (int u = 0; u < WCAP / 32; ++u) k[u] = u * 32 + lane < cnt ? list[u * 32 + lane] : 0;
-    if (cnt <= 32) {
+    if (cnt <= 32) {  // by their ranks
+        const uint64_t k = lane < cnt ? list[lane] : 0;
+        int rank = 0;
 #pragma unroll 4
-        for (int i = 0; i < cnt; ++i) rank[0] += list[i] > k[0];
-    } else {
-        for (int i = 0; i < cnt; ++i) {
-            const uint64_t o = list[i];
+        for (int i = 0; i < cnt; ++i) rank += list[i] > k;
+        __syncwarp();
+        if (lane < cnt && rank < N) list[rank] = k;
+        __syncwarp();
+        return list[N - 1];
+    }
+    uint64_t k[WCAP / 32], top = 0;
 #pragma unroll
-            for (int u = 0; u < WCAP / 32; ++u) rank[u] += o > k[u];
+    for (int u = 0; u < WCAP / 32; ++u) {
+        k[u] = u * 32 + lane < cnt ? list[u * 32 + lane] : 0;
+        top = max(top, k[u]);
+    }
+    // keys are all different: some key is not above exactly N of them
+    uint64_t lo = 1, hi = ((uint64_t)__reduce_max_sync(0xffffffffu, (uint32_t)(top >> 32)) + 1) << 32;
+    for (;;) {
+        const uint64_t mid = lo + (hi - lo) / 2;
+        int c = 0;
+#pragma unroll
+        for (int u = 0; u < WCAP / 32; ++u) c += __popc(__ballot_sync(0xffffffffu, k[u] >= mid));
+        if (c == N || hi - lo <= 1) {
+            lo = mid;
+            break;
         }
+        if (c > N) lo = mid;
+        else hi = mid;
+    }
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < WCAP / 32; ++u) {
+        const unsigned who = __ballot_sync(0xffffffffu, k[u] >= lo);
+        if (k[u] >= lo) list[n + __popc(who & ((1u << lane) - 1))] = k[u];
+        n += __popc(who);
     }
     __syncwarp();
-#pragma unroll
-    for (int u = 0; u < WCAP / 32; ++u)
-        if (u * 32 + lane < cnt && rank[u] < N) list[rank[u]] = k[u];
-    __syncwarp();
-    return min(cnt, N);
+    return lo;
 }
 
 __device__ __forceinline__ uint64_t key_of(float f, int i) {
@@ -341,8 +372,8 @@ __device__ __forceinline__ uint4 load_vector(const uint8_t* row, int q, int shif
 }
 
 struct ScanSmem {
+    alignas(16) float group[SCAN_WARPS][32];
     uint64_t list[SCAN_WARPS][WCAP];
-    alignas(16) float group[SCAN_WARPS][TILE];
     uint32_t row_bar[SCAN_WARPS];  // of each of the CTA's rows: order of a value that its N-th largest is not below
 };
 
@@ -351,7 +382,7 @@ struct ScanSmem {
 //
 // Bound: of a large batch by instructions (about 8 for each 32 logits of 16 bits: 1 to widen them, 1/2 each for the
 // argument and the sum as pairs, 1 for the exponential, 1/2 for the maximum, the rest for loads, loop and candidates; issue
-// slots 73% busy) and by HBM.  Measured: 128 x 8 rows of 131072 in bf16 49.4 us, 5.4 TB/s, of the call's 52.8.  Left out:
+// slots 73% busy) and by HBM.  Measured: 128 x 8 rows of 131072 in bf16 48 us, 5.6 TB/s, of the call's 51.3.  Left out:
 // tiles by bulk copies of 2 KB into shared memory, 3 a warp, with as fast a loop (a copy alone runs at 3.6 TB/s with 84 of
 // them in flight an SM, at 7.2 with 8 KB, plain loads at 7.3); CTAs that share a chunk and meet at barriers (97 us); 8 CTAs
 // an SM, whose 64 registers spill (59.8).
@@ -462,7 +493,7 @@ __global__ void __launch_bounds__(SCAN_CT, PER_SM) beam_scan_kernel(const SelPar
 #pragma unroll
         for (int j = 0; j < NJ; ++j) mj[j] = max_of<TYPE>(v[j]);
         if (!barred && set) {  // the first tile that has values
-            bar = fmaxf(nth_of_warp(mj, m, p.N, s.group[wid]), __uint_as_float(0xff7fffffu));  // (no -inf passes)
+            bar = bar_of_warp(mj, m, p.N, s.group[wid]);  // (no -inf passes)
             barred = true;
             if (lane == 0) atomicMax(row_bar, ord(bar));
         }
@@ -478,8 +509,8 @@ __global__ void __launch_bounds__(SCAN_CT, PER_SM) beam_scan_kernel(const SelPar
             if (pass) list[cnt + __popc(who & ((1u << lane) - 1))] = key;
             cnt += __popc(who);
             if (cnt > p.raise) {
-                cnt = compact_list(list, cnt, p.N);
-                own = list[cnt - 1];
+                own = shrink_list(list, cnt, p.N);  // (of equal values in places as yet unseen it lets none pass)
+                cnt = p.N;
                 bar = fmaxf(bar, unord((uint32_t)(own >> 32)));
                 if (lane == 0) atomicMax(row_bar, (uint32_t)(own >> 32));
             }
@@ -487,7 +518,10 @@ __global__ void __launch_bounds__(SCAN_CT, PER_SM) beam_scan_kernel(const SelPar
     }
     const float l = ft::warp_sum(l0 + l1);
     if (lane == 0) p.sums[item] = BeamSum{far ? g : c, l, far, 0};
-    if (cnt > p.N) cnt = compact_list(list, cnt, p.N);
+    if (cnt > p.N) {
+        shrink_list(list, cnt, p.N);
+        cnt = p.N;
+    }
     __syncwarp();
     // (each list starts at another place: the second kernel's threads then hold keys of all ranks)
     uint64_t* out = p.keys + (long long)item * p.N;
@@ -868,7 +902,7 @@ ft_status ft_beam_select(ft_beam* bm, int32_t B, int32_t K, int32_t N, const voi
     p.vpc = tiles_of(vectors, (int)R, K, N, bm->num_sms) * TILE;
     p.C = (int)((vectors + p.vpc - 1) / p.vpc);
     p.items = (int)R * p.C;
-    p.raise = N <= 16 ? N + 8 : WCAP - 32;  // (the ballot after it may add 32)
+    p.raise = N <= FEW ? N + 8 : WCAP - 32;  // (the ballot after it may add 32)
     const void* scan = bm->dtype == FT_T_BF16  ? (const void*)beam_scan_kernel<FT_T_BF16>
                        : bm->dtype == FT_T_F16 ? (const void*)beam_scan_kernel<FT_T_F16>
                                                : (const void*)beam_scan_kernel<FT_T_F32>;
