@@ -607,8 +607,10 @@ __global__ void __launch_bounds__(CT, 1) kv_reorder_kernel(KvCtl c, int n, const
 #pragma unroll
             for (int h = 0; h < RO_COLS / 32; ++h) {
                 const int q = 32 * h + lane;
-                if (q < got) atomicAdd(&c.refs[x.from[q]], sign);
-                if (q < x.held) atomicAdd(&c.refs[x.mine[q]], -sign);
+                const int to = q < got ? x.from[q] : -1, was = q < x.held ? x.mine[q] : -1;
+                if (to == was) continue;  // (a page that the row keeps: beams of a request share many)
+                if (to >= 0) atomicAdd(&c.refs[to], sign);
+                if (was >= 0) atomicAdd(&c.refs[was], -sign);
             }
         }
     };
