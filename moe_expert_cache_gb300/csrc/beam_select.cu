@@ -33,7 +33,6 @@ struct ft_beam {
     unsigned* err;
     struct BeamSum* sums;  // [lists]
     uint64_t* keys;        // [lists][N_max]
-    long long lists;       // chunks of all rows
 };
 
 // Sum of exponentials over a part of a row: l * 2^ref, or l * e^ref where far.
@@ -279,19 +278,18 @@ __device__ __forceinline__ int store_groups(float* group, float m, int N) {
     return G;
 }
 
-// The sum of n parts, by a warp; of `step` lanes each takes parts lane, lane + step, ...  A part that is 0 (it has no value)
-// has no say in the reference.  Differences of references are exact in fp32 but where a far part meets one that is not.
-// (fp64 runs at a 64th of fp32's rate or less here, so it is kept out of what every CTA does.)
-template <int STEP, class F>
+// The sum of n parts, by a warp.  A part that is 0 (it has no value) has no say in the reference.  Differences of references
+// are exact in fp32 but where a far part meets one that is not (fp64 runs at a 64th of fp32's rate here).
+template <class F>
 __device__ __forceinline__ BeamSum join_sums(F part, int n) {
     const int lane = threadIdx.x & 31;
     float cf = -INFINITY, cn = -INFINITY;  // largest reference of each kind
-    for (int i = lane % STEP; i < n; i += STEP) {
+    for (int i = lane; i < n; i += 32) {
         const BeamSum t = part(i);
         if (t.l != 0.f) (t.far ? cf : cn) = fmaxf(t.far ? cf : cn, t.ref);
     }
 #pragma unroll
-    for (int o = 1; o < STEP; o <<= 1) {
+    for (int o = 1; o < 32; o <<= 1) {
         cf = fmaxf(cf, __shfl_xor_sync(0xffffffffu, cf, o));
         cn = fmaxf(cn, __shfl_xor_sync(0xffffffffu, cn, o));
     }
@@ -299,7 +297,7 @@ __device__ __forceinline__ BeamSum join_sums(F part, int n) {
     const bool far = cf > 0.f || (cf > -INFINITY && cn == -INFINITY);
     const float ref = far ? cf : cn == -INFINITY ? 0.f : cn;
     float l = 0.f;
-    for (int i = lane % STEP; i < n; i += STEP) {
+    for (int i = lane; i < n; i += 32) {
         const BeamSum t = part(i);
         if (t.l == 0.f) continue;
         float d;
@@ -309,7 +307,7 @@ __device__ __forceinline__ BeamSum join_sums(F part, int n) {
         l += t.l * ex2(d);
     }
 #pragma unroll
-    for (int o = 1; o < STEP; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     return BeamSum{ref, l, far, 0};
 }
 
@@ -561,7 +559,7 @@ __global__ void __launch_bounds__(CT, 1) beam_join_kernel(const SelParams p) {
             base = -INFINITY;
             if (lane == 0 && !(sc == -INFINITY)) atomicOr(p.err, FT_DEVERR_ARG);
         } else if (!ended) {
-            const BeamSum t = join_sums<32>([&](int i) {
+            const BeamSum t = join_sums([&](int i) {
                 const float4 v = i < 32 ? part[0] : i < 64 ? part[1] : i < 96 ? part[2] : i < 128 ? part[3] : __ldcg(sums + i);
                 return BeamSum{v.x, v.y, __float_as_int(v.z), 0};
             }, p.C);
@@ -776,7 +774,6 @@ int tiles_of(long long vectors, int R, int K, int N, int sms) {
                 best = (int)tiles;
             }
         }
-
     }
     return best;
 }
@@ -860,7 +857,6 @@ ft_status ft_beam_init(ft_beam** out, int32_t V, int32_t dtype, int32_t R_max, i
     bm->err = (unsigned*)(a + l.err);
     bm->sums = (BeamSum*)(a + l.sums);
     bm->keys = (uint64_t*)(a + l.keys);
-    bm->lists = l.lists;
     *out = bm;
     return FT_OK;
 }

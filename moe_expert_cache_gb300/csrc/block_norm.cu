@@ -380,7 +380,7 @@ extern "C" ft_status ft_block_norm(const ft_norm_desc* d, int32_t T, const void*
         p.tpr = 32;
         nv = p.nvec <= 32 ? 1 : 2;
         threads = 128;
-        grid = (T + 3) / 4;
+        grid = (int)(((long long)T + 3) / 4);
     } else {
         nv = p.nvec <= 512 ? 1 : p.nvec <= 1024 ? 2 : 4;
         threads = ((p.nvec + nv - 1) / nv + 31) / 32 * 32;

@@ -822,9 +822,9 @@ cudaError_t launch_kv_batch(ft_kv* kv, int B, const int* rows, const int* add, i
     const cudaError_t e = launch_dependent((const void*)kv_batch_kernel, 1, CT, 0, kv->stream, args);
     if (e != cudaSuccess || here) return e;
     void* list[] = {&c, &B, &rows, &add, &o};
-    const int ctas = (T + 255) / 256;
-    return launch_dependent((const void*)kv_list_kernel, ctas < kv->num_sms * 8 ? ctas : kv->num_sms * 8, 256, 0, kv->stream,
-                            list);
+    const long long ctas = ((long long)T + 255) / 256;
+    return launch_dependent((const void*)kv_list_kernel, (int)(ctas < kv->num_sms * 8 ? ctas : kv->num_sms * 8), 256, 0,
+                            kv->stream, list);
 }
 
 cudaError_t launch_kv_reorder(ft_kv* kv, int n, const int* rows, const int* parents) {
