@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(SCAN_CT, PER_SM) beam_scan_kernel(const SelPar
         }
         if (!far) {
             const uint64_t k2 = pair(LOG2E, LOG2E), c2 = pair(-c, -c);
-            uint64_t l2 = pair(l0, l1);
+            uint64_t l2 = 0;  // (a tile's sum by itself: the chains of additions stay short)
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 float f[VEC];
@@ -475,8 +475,8 @@ __global__ void __launch_bounds__(SCAN_CT, PER_SM) beam_scan_kernel(const SelPar
                 }
             }
             const float2 l = unpair(l2);
-            l0 = l.x;
-            l1 = l.y;
+            l0 += l.x;
+            l1 += l.y;
         } else {
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
