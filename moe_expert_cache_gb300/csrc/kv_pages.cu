@@ -490,7 +490,7 @@ struct ReorderSmem {
     int row[RO_MAX], par[RO_MAX], len[RO_MAX], old[RO_MAX], full[RO_MAX], last[RO_MAX], keep[RO_MAX];
     int free[RO_MAX];
     int cols;
-    unsigned flag[3];
+    unsigned flag[2];
 };
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }

@@ -83,6 +83,19 @@ def test_long_rows():
     _batch(c, list(range(32)), [int(x) for x in rng.integers(0, 900, 32)], 20000)
 
 
+def test_more_than_is_staged_at_once():
+    # 1024 rows of up to 300 pages, of which up to 256 are common: the columns are moved in several passes
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(16 * 90, 16 * 300, 1024)]
+    c = Cache(lens, D=64, page=16, Hq=1, Hkv=1, row_pages=301, shared=16 * 256, spare=1100, B_max=1)
+    for _ in range(2):
+        _reorder(c, [int(x) for x in rng.permutation(1024)], [int(x) for x in rng.integers(-1, 1024, 1024)])
+    # 1000 empty rows become copies of one of 291 pages: with too few free pages all is taken back
+    for spare in (999, 1000):
+        c = Cache([0] * 1000 + [16 * 290 + 3], D=64, page=16, Hq=1, Hkv=1, row_pages=301, spare=spare, B_max=1)
+        assert _reorder(c, list(range(1000)), [1000] * 1000, plain_rows=True) == ("capacity" if spare < 1000 else None)
+
+
 def test_reorder_refusals_change_nothing():
     c = Cache([40, 24, 16, 0], D=64, page=16, Hq=1, Hkv=1, row_pages=4, spare=0)
     ft = c.ft
