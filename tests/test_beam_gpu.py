@@ -123,6 +123,12 @@ def test_many_candidates_to_join():
     assert got[1][0].tolist() == [0] * 64 and got[2][0].tolist() == list(range(64))
 
 
+def test_more_candidates_than_the_threads_hold():
+    # 32 beams of more than 128 chunks of 64 candidates
+    x, ld = _logits(32, 600003, "f32", seed=11)
+    _check(1, 32, 64, x, ld, (-np.arange(32) / 64).astype(np.float32))
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [5000, 40000])
 def test_order_of_the_logits(V, kind):
